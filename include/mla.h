@@ -28,6 +28,16 @@
  *    element for MLA_KV_E4M3 (OCP E4M3: bias 7, max 448, no infinity), two
  *    (bfloat16) for MLA_KV_BF16. A token's slot is page_id * page_size + offset.
  *    page_size must be 64.
+ *  - MLA_KV_E2M1 pages are MLA_E2M1_PAGE_BYTES contiguous bytes each:
+ *      codes[18][64][16]  block b of token t (elements 32b .. 32b + 31), two e2m1
+ *                         codes per byte, the even element in the low nibble;
+ *      exps[9][64]        byte i of token t: the exponent nibbles of blocks 2i
+ *                         (low) and 2i + 1 (high).
+ *    An element's value is e2m1(code) * 2^(n - 8) * kv_scale, with e2m1 the
+ *    values 0, 0.5, 1, 1.5, 2, 3, 4, 6 (code bit 3: sign) and n = 0..14 the
+ *    block's nibble; n = 15 makes every element of the block NaN. Every such
+ *    value is kv_scale times an e4m3 number, so the scale that suits an e4m3
+ *    cache suits this one, and its kv_scale must lie in [2^-100, 2^100].
  *  - Pointers named "device" must point to device memory of the current CUDA
  *    device; all must be 16-byte aligned. The caller owns every buffer.
  *    The library allocates nothing and never synchronises the host: all work
@@ -77,7 +87,8 @@ typedef enum mla_status {
 
 typedef enum mla_kv_dtype {
   MLA_KV_E4M3 = 0, /* FP8 e4m3 codes, one byte per element */
-  MLA_KV_BF16 = 1  /* bfloat16, two bytes per element */
+  MLA_KV_BF16 = 1, /* bfloat16, two bytes per element */
+  MLA_KV_E2M1 = 2  /* FP4 e2m1 codes, 32 elements sharing a power of two (4.125 bits) */
 } mla_kv_dtype;
 
 #define MLA_D_LATENT 512
@@ -85,6 +96,8 @@ typedef enum mla_kv_dtype {
 #define MLA_D_ENTRY 576
 #define MLA_PAGE_SIZE 64
 #define MLA_MAX_QUERIES 4
+#define MLA_E2M1_BLOCK 32         /* elements that share an exponent in an MLA_KV_E2M1 cache */
+#define MLA_E2M1_PAGE_BYTES 19008 /* bytes of an MLA_KV_E2M1 page of 64 tokens */
 
 /* Bits of the device status word (first 4 bytes of the decode workspace). */
 #define MLA_DEVICE_ERR_BAD_PAGE 0x1u   /* a block-table entry outside the cache */
@@ -106,7 +119,15 @@ MLA_API const char* mla_status_string(int status);
  *                nearest with ties to even, of the exact quotient, and
  *                saturated to +-448 (NaN stays NaN), where x[t][0:512] =
  *                latent[t], x[t][512:576] = rope[t];
- *   MLA_KV_BF16: kv_pages[slot][d] = x[t][d] (a copy; kv_scale must be 1).
+ *   MLA_KV_BF16: kv_pages[slot][d] = x[t][d] (a copy; kv_scale must be 1);
+ *   MLA_KV_E2M1: per block of 32 elements with a = max |x|: n - 8 is the smallest
+ *                power in -8 .. 6 with a <= 7 * 2^(n - 8) * kv_scale (6 if there
+ *                is none), and each code is the exact quotient
+ *                x / (2^(n - 8) * kv_scale) rounded to the nearest e2m1 value,
+ *                ties to the even code, saturated at +-6 (between 6 and 7 the
+ *                error is at most the half step of 4 .. 6, which a larger power
+ *                would double). Infinities saturate; a block that holds a NaN
+ *                gets n = 15 and zero codes.
  * Slots with slot_mapping[t] < 0 are skipped (padding tokens).
  *
  * latent       device, bf16 [num_tokens][512], row-major
@@ -158,8 +179,11 @@ MLA_API size_t mla_decode_workspace_size(int batch, int num_queries, int num_hea
  * m, unless the weight accumulated so far exceeds 2^28 times the page's
  * largest), so every page's largest P lies in [1, 448]; what a page loses is
  * confined to its tokens below 2^-6 of its largest weight. Each piece of the
- * split (one per CTA) has its own maximum; pieces merge in fp32. For a bf16
- * cache both contractions use bf16 operands (kind::f16).
+ * split (one per CTA) has its own maximum; pieces merge in fp32. An e2m1 cache
+ * is expanded to e4m3 codes in shared memory as its pages arrive, which is
+ * exact, and then takes the same arithmetic; a visible token that holds a NaN
+ * block makes its rows NaN. For a bf16 cache both contractions use bf16
+ * operands (kind::f16).
  *
  * q           device, bf16 [batch][num_queries][num_heads][576]
  * kv_pages    device, the cache; num_pages pages of page_size (= 64) tokens
@@ -206,7 +230,7 @@ MLA_API mla_status mla_decode(const void* q, const void* kv_pages, int64_t num_p
  *               bad length: out = 0, lse = -inf, MLA_DEVICE_ERR_BAD_LENGTH.
  * workspace     at least mla_decode_grouped_workspace_size(batch, num_queries,
  *               num_heads, num_ctas) bytes, zero-filled before its first use.
- * kv_dtype      MLA_KV_E4M3 (MLA_ERR_UNSUPPORTED otherwise).
+ * kv_dtype      MLA_KV_E4M3 or MLA_KV_E2M1 (MLA_ERR_UNSUPPORTED otherwise).
  * Other arguments as mla_decode.
  */
 MLA_API size_t mla_decode_grouped_workspace_size(int batch, int num_queries, int num_heads,
@@ -228,8 +252,9 @@ MLA_API mla_status mla_decode_grouped(const void* q, const void* kv_pages, int64
  * as they are read (the FP8 cache of "Smaller, faster, safer: running Kimi and
  * GLM at scale", section "Quantizing the KV cache", converted on load) and both
  * contractions use kind::f16 with q and the softmax weights in f16; for a bf16
- * cache it is mla_decode. It exists to measure what reading the FP8 bytes as
- * operands saves; it has no counterpart on the pages.
+ * cache it is mla_decode; MLA_KV_E2M1 is refused (MLA_ERR_UNSUPPORTED). It
+ * exists to measure what reading the FP8 bytes as operands saves; it has no
+ * counterpart on the pages.
  */
 MLA_API mla_status mla_decode_f16_operands(const void* q, const void* kv_pages, int64_t num_pages,
                                    int page_size, int kv_dtype, const int32_t* block_table,
@@ -257,6 +282,143 @@ MLA_API mla_status mla_decode_f16_operands(const void* q, const void* kv_pages, 
  */
 MLA_API mla_status mla_decode_combine(const float* part_out, const float* part_lse, int num_parts,
                               int64_t num_rows, void* out, float* lse, mla_stream_t stream);
+
+/*
+ * mla_kv_gather -- read cached entries back as bfloat16 rows.
+ *
+ * The read side of mla_kv_append ("Smaller, faster, safer: running Kimi and GLM
+ * at scale", section "Quantizing the KV cache": values are converted back as
+ * they are read), for callers that need the entries themselves, such as a
+ * prefill chunk over a cached context. Row r with cu_tokens[b] <= r <
+ * cu_tokens[b + 1] receives token starts[b] + r - cu_tokens[b] of request b:
+ *   latent[r][0:512], rope[r][0:64] = bf16( value(code) * kv_scale )
+ * the product in fp32, rounded to bf16 (a bf16 cache is copied). A token beyond
+ * its block-table row or in a page outside the cache gives a row of zeros. Rows
+ * from cu_tokens[batch] on are left as they were.
+ *
+ * kv_pages, num_pages, page_size, kv_dtype, kv_scale  as for mla_kv_append
+ * block_table device, int32 [batch][max_pages]
+ * starts      device, int32 [batch]; NULL: every range starts at token 0
+ * cu_tokens   device, int32 [batch + 1], ascending
+ * num_tokens  rows of latent and rope; ranges beyond it are cut
+ * latent      device, bf16 [num_tokens][512] (written)
+ * rope        device, bf16 [num_tokens][64] (written)
+ */
+MLA_API mla_status mla_kv_gather(const void* kv_pages, int64_t num_pages, int page_size,
+                                 int kv_dtype, float kv_scale, const int32_t* block_table,
+                                 int max_pages, const int32_t* starts, const int32_t* cu_tokens,
+                                 int batch, int64_t num_tokens, void* latent, void* rope,
+                                 mla_stream_t stream);
+
+/*
+ * mla_kv_alloc -- extend requests by new tokens: pages, block tables, slots.
+ *
+ * The page allocator's side of a step, on the device, from the requests'
+ * lengths (see mla_kv_check for the page tags). For request b = 0, 1, ... in
+ * order, with L = seq_lens[b] cached tokens, n = new_tokens[b] and
+ * h = pages_held[b] block-table entries in use (pages kept from rejected drafts
+ * among them: h >= ceil(L / 64)):
+ *   cu_tokens[b + 1] = cu_tokens[b] + max(n, 0), cu_tokens[0] = 0;
+ *   it takes max(0, ceil((L + n) / 64) - h) pages off the end of the free list,
+ *   the last one first, and appends them to its block-table row; with tags,
+ *   page_tags[p] += 1 for each and expected_tags beside the entry = the new tag;
+ *   slot_mapping[cu_tokens[b] + i] = slot of token L + i, for mla_kv_append;
+ *   seq_lens_out[b] = L + n, pages_held_out[b] = h + pages taken.
+ * A refused request takes no page; its slots are -1, seq_lens_out[b] = -1 and
+ * request_status[b] says why:
+ *   MLA_KV_ALLOC_BAD_LENGTH  L < 0 (as mla_kv_check marks a failed request),
+ *                            n < 0, h outside [ceil(L / 64), max_pages];
+ *   MLA_KV_ALLOC_TABLE_FULL  L + n tokens need more than max_pages pages;
+ *   MLA_KV_ALLOC_SLOTS_FULL  its rows end beyond num_slots;
+ *   MLA_KV_ALLOC_NO_PAGES    the pages asked for so far, its own included,
+ *                            exceed the free list (so does every later request
+ *                            that needs a page).
+ * Slots from cu_tokens[batch] on are -1 (padding, which mla_kv_append skips). A
+ * free-list entry outside [0, num_pages) reaches the block table as it is, where
+ * mla_kv_check and mla_decode report it; its slots are -1.
+ *
+ * seq_lens, new_tokens, pages_held  device, int32 [batch]
+ * free_pages      device, int32 [free_capacity]; the first *free_count are free
+ * free_count      device, int32; taken as 0 below 0, free_capacity above it
+ * block_table     device, int32 [batch][max_pages], updated in place
+ * page_tags       device, uint32 [num_pages], updated in place; or NULL
+ * expected_tags   device, uint32 [batch][max_pages], updated in place; NULL
+ *                 exactly if page_tags is
+ * seq_lens_out, pages_held_out  device, int32 [batch]
+ * free_count_out  device, int32
+ *                 Each output of these three may be the same buffer as its
+ *                 input, so that a captured step can be replayed.
+ * cu_tokens       device, int32 [batch + 1] (saturates at 2^31 - 1)
+ * slot_mapping    device, int32 [num_slots]
+ * request_status  device, uint32 [batch]
+ * Pointers need 4-byte alignment here. A page named twice by the free list, or
+ * free and held, is the caller's error.
+ */
+#define MLA_KV_ALLOC_BAD_LENGTH 0x1u
+#define MLA_KV_ALLOC_TABLE_FULL 0x2u
+#define MLA_KV_ALLOC_SLOTS_FULL 0x4u
+#define MLA_KV_ALLOC_NO_PAGES 0x8u
+MLA_API mla_status mla_kv_alloc(const int32_t* seq_lens, const int32_t* new_tokens, int batch,
+                                int page_size, const int32_t* pages_held,
+                                const int32_t* free_pages, const int32_t* free_count,
+                                int64_t free_capacity, int64_t num_pages, int32_t* block_table,
+                                int max_pages, uint32_t* page_tags, uint32_t* expected_tags,
+                                int32_t* seq_lens_out, int32_t* pages_held_out,
+                                int32_t* free_count_out, int32_t* cu_tokens,
+                                int32_t* slot_mapping, int64_t num_slots,
+                                uint32_t* request_status, mla_stream_t stream);
+
+/*
+ * mla_verify_drafts -- accept or reject drafted tokens, sample the next one.
+ *
+ * The end of a speculative step ("How to serve trillions of tokens for
+ * trillion-parameter coding agents", section "Use custom speculative decoding
+ * ...": drafts are verified in parallel without changing the target model's
+ * distribution). For request b with k = num_drafts[b] drafts x_0 .. x_{k-1},
+ * p_j = target_probs[b][j], q_j = draft_probs[b][j] and u = uniforms[b]:
+ *   draft j is kept while u_j * q_j(x_j) < p_j(x_j) (and every earlier one was);
+ *   a = num_accepted[b] = the number kept;
+ *   the next token is drawn from max(p_a - q_a, 0) if a < k (from p_a if that is
+ *   zero everywhere), from p_k if a = k: the smallest i with
+ *   w_0 + .. + w_i > uniforms[b][max_drafts] * (w_0 + .. + w_{vocab-1});
+ *   out_tokens[b] = x_0 .. x_{a-1}, the next token, then -1;
+ *   seq_lens_out[b] = seq_lens[b] - (k - a), the cached tokens that stay
+ *   (seq_lens[b] counts the k + 1 queries of the step, as for mla_decode).
+ * With draft_probs NULL, q_j puts all its weight on x_j: u_j < p_j(x_j), and the
+ * rest is p_a without x_a. A draft outside [0, vocab) is rejected. If all
+ * weights are zero the next token is -1. A request with k outside
+ * [0, max_drafts] or a negative length is left out: out_tokens[b] = -1
+ * throughout, num_accepted[b] = -1, seq_lens_out[b] = seq_lens[b].
+ *
+ * Arithmetic: probabilities are taken within [0, 1] (NaN as 0), uniforms within
+ * [0, 1 - 2^-24] (NaN as 0). The acceptance test is exact; weights are summed as
+ * integers in units of 2^-60 (a probability below 2^-37 is truncated to them),
+ * so the result does not depend on the order of the sum. A row's probabilities
+ * must sum to less than 16.
+ *
+ * target_probs  device, [batch][max_drafts + 1] rows of `vocab` probabilities,
+ *               target_stride >= vocab elements apart
+ * draft_probs   device, [batch][max_drafts] rows, draft_stride apart; or NULL
+ * prob_dtype    MLA_PROB_F32 or MLA_PROB_BF16, of both
+ * draft_tokens  device, int32 [batch][max_drafts] (may be NULL if max_drafts = 0)
+ * uniforms      device, fp32 [batch][max_drafts + 1]
+ * num_drafts    device, int32 [batch]; NULL: max_drafts each
+ * seq_lens      device, int32 [batch]; may be NULL (then seq_lens_out is too)
+ * max_drafts    0 .. MLA_MAX_DRAFTS
+ * out_tokens    device, int32 [batch][max_drafts + 1]
+ * num_accepted  device, int32 [batch]
+ * seq_lens_out  device, int32 [batch]; may be seq_lens, or NULL
+ * Pointers need the alignment of their elements here.
+ */
+#define MLA_MAX_DRAFTS 31
+typedef enum mla_prob_dtype { MLA_PROB_F32 = 0, MLA_PROB_BF16 = 1 } mla_prob_dtype;
+MLA_API mla_status mla_verify_drafts(const void* target_probs, int64_t target_stride,
+                                     const void* draft_probs, int64_t draft_stride,
+                                     int prob_dtype, const int32_t* draft_tokens,
+                                     const float* uniforms, const int32_t* num_drafts,
+                                     const int32_t* seq_lens, int batch, int max_drafts,
+                                     int vocab, int32_t* out_tokens, int32_t* num_accepted,
+                                     int32_t* seq_lens_out, mla_stream_t stream);
 
 /*
  * mla_kv_check -- integrity check of requests' page mappings before decode.

@@ -34,9 +34,14 @@ Modules:
 * :mod:`oracle.integrity` -- the KV-cache integrity check of [CF] section
   "Protecting a shared KV cache": per-request comparison of the pages' current
   tags with the tags the request expects, one status word per request.
+* :mod:`oracle.e2m1` -- the 4-bit cache codec: E2M1 codes, an exponent per 32
+  elements, the page layout.
+* :mod:`oracle.paging` -- the page allocator's side of a step, request by request.
+* :mod:`oracle.verify` -- verification of drafted tokens in rational arithmetic
+  ([K2.6] section "Use custom speculative decoding ...").
 
 Every function is pinned by ``tests/test_oracle_*.py`` against closed forms,
 library routines, brute force and invariants (see each test's docstring).
 """
 
-from . import attention, e4m3, integrity  # noqa: F401
+from . import attention, e2m1, e4m3, integrity, paging, verify  # noqa: F401

@@ -53,6 +53,7 @@ D_ENTRY = D_LATENT + D_ROPE
 
 KV_E4M3 = "e4m3"
 KV_BF16 = "bf16"
+KV_VALUES = "values"  # pages given as float64 values, their scale included (any codec's)
 
 
 def dequant(codes: np.ndarray, kv_dtype: str, kv_scale: float) -> np.ndarray:
@@ -62,6 +63,8 @@ def dequant(codes: np.ndarray, kv_dtype: str, kv_scale: float) -> np.ndarray:
         return e4m3.decode(codes) * scale
     if kv_dtype == KV_BF16:
         return e4m3.bf16_bits_to_f64(codes) * scale
+    if kv_dtype == KV_VALUES:
+        return np.asarray(codes, dtype=np.float64)
     raise ValueError(f"unknown kv dtype {kv_dtype!r}")
 
 

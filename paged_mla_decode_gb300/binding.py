@@ -23,6 +23,9 @@ MLA_ERR_CUDA = 4
 
 MLA_KV_E4M3 = 0
 MLA_KV_BF16 = 1
+MLA_KV_E2M1 = 2
+
+MLA_E2M1_PAGE_BYTES = 19008
 
 MLA_DEVICE_ERR_BAD_PAGE = 0x1
 MLA_DEVICE_ERR_BAD_LENGTH = 0x2
@@ -32,10 +35,20 @@ MLA_KV_CHECK_TAG_MISMATCH = 0x1
 MLA_KV_CHECK_PAGE_RANGE = 0x2
 MLA_KV_CHECK_BAD_LENGTH = 0x4
 
+MLA_KV_ALLOC_BAD_LENGTH = 0x1
+MLA_KV_ALLOC_TABLE_FULL = 0x2
+MLA_KV_ALLOC_SLOTS_FULL = 0x4
+MLA_KV_ALLOC_NO_PAGES = 0x8
+
+MLA_PROB_F32 = 0
+MLA_PROB_BF16 = 1
+MLA_MAX_DRAFTS = 31
+
 EXPORTED = ("mla_abi_version", "mla_status_string", "mla_kv_append",
             "mla_decode_workspace_size", "mla_decode", "mla_decode_f16_operands",
             "mla_decode_grouped_workspace_size", "mla_decode_grouped",
-            "mla_decode_combine", "mla_kv_check", "mla_decode_static_scratch")
+            "mla_decode_combine", "mla_kv_check", "mla_decode_static_scratch",
+            "mla_kv_gather", "mla_kv_alloc", "mla_verify_drafts")
 
 _lib = None
 
@@ -98,6 +111,20 @@ def open_library(path: str) -> ctypes.CDLL:
         c.c_void_p, c.c_void_p, c.c_int64, c.c_int, c.c_int, c.c_void_p, c.c_int, c.c_void_p,
         c.c_int, c.c_int, c.c_int, c.c_float, c.c_float, c.c_int, c.c_void_p, c.c_void_p,
         c.c_void_p, c.c_void_p]
+    lib.mla_kv_gather.restype = c.c_int
+    lib.mla_kv_gather.argtypes = [c.c_void_p, c.c_int64, c.c_int, c.c_int, c.c_float, c.c_void_p,
+                                  c.c_int, c.c_void_p, c.c_void_p, c.c_int, c.c_int64, c.c_void_p,
+                                  c.c_void_p, c.c_void_p]
+    lib.mla_kv_alloc.restype = c.c_int
+    lib.mla_kv_alloc.argtypes = [c.c_void_p, c.c_void_p, c.c_int, c.c_int, c.c_void_p, c.c_void_p,
+                                 c.c_void_p, c.c_int64, c.c_int64, c.c_void_p, c.c_int, c.c_void_p,
+                                 c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p,
+                                 c.c_void_p, c.c_int64, c.c_void_p, c.c_void_p]
+    lib.mla_verify_drafts.restype = c.c_int
+    lib.mla_verify_drafts.argtypes = [c.c_void_p, c.c_int64, c.c_void_p, c.c_int64, c.c_int,
+                                      c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p, c.c_int,
+                                      c.c_int, c.c_int, c.c_void_p, c.c_void_p, c.c_void_p,
+                                      c.c_void_p]
     return lib
 
 
@@ -121,11 +148,26 @@ def _check(status: int, where: str):
 
 
 def kv_dtype_code(kv_pages: torch.Tensor) -> int:
+    """The cache's element type, from its tensor (and a check of its shape).
+
+    uint8 ``[num_pages, 64, 576]`` holds e4m3 codes, bfloat16 of that shape bf16
+    values, uint8 ``[num_pages, 19008]`` e2m1 pages.
+    """
+    assert kv_pages.is_contiguous()
+    if kv_pages.dtype == torch.uint8 and kv_pages.dim() == 2:
+        assert kv_pages.shape[1] == MLA_E2M1_PAGE_BYTES
+        return MLA_KV_E2M1
+    assert kv_pages.dim() == 3 and kv_pages.shape[2] == 576
     if kv_pages.dtype == torch.uint8:
         return MLA_KV_E4M3
     if kv_pages.dtype == torch.bfloat16:
         return MLA_KV_BF16
-    raise TypeError("kv_pages must be uint8 (e4m3 codes) or bfloat16")
+    raise TypeError("kv_pages must be uint8 (e4m3 codes or e2m1 pages) or bfloat16")
+
+
+def _page_size(kv_pages: torch.Tensor) -> int:
+    """Tokens per page: the second dimension, 64 by definition of an e2m1 page."""
+    return 64 if kv_pages.dim() == 2 else int(kv_pages.shape[1])
 
 
 def mla_kv_append(latent: torch.Tensor, rope: torch.Tensor, slot_mapping: torch.Tensor,
@@ -134,12 +176,12 @@ def mla_kv_append(latent: torch.Tensor, rope: torch.Tensor, slot_mapping: torch.
     num_tokens = int(slot_mapping.numel())
     assert latent.dtype == torch.bfloat16 and rope.dtype == torch.bfloat16
     assert slot_mapping.dtype == torch.int32
-    assert latent.is_contiguous() and rope.is_contiguous() and kv_pages.is_contiguous()
+    assert latent.is_contiguous() and rope.is_contiguous()
     assert latent.shape == (num_tokens, 512) and rope.shape == (num_tokens, 64)
-    assert kv_pages.dim() == 3 and kv_pages.shape[2] == 576
+    dtype = kv_dtype_code(kv_pages)
     st = load_library().mla_kv_append(_ptr(latent), _ptr(rope), _ptr(slot_mapping), num_tokens,
                                       _ptr(kv_pages), int(kv_pages.shape[0]),
-                                      int(kv_pages.shape[1]), kv_dtype_code(kv_pages),
+                                      _page_size(kv_pages), dtype,
                                       float(kv_scale), _stream(stream))
     _check(st, "mla_kv_append")
 
@@ -155,6 +197,7 @@ def mla_decode(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tenso
                stream=None, f16_operands: bool = False) -> None:
     """Split-KV paged MLA decode (combine included) into ``out`` and ``lse``.
 
+    ``kv_pages`` as in :func:`kv_dtype_code` (e4m3, bf16 or e2m1 pages).
     ``f16_operands`` calls mla_decode_f16_operands (the e4m3 cache widened to f16
     operands) instead of mla_decode."""
     assert q.dtype == torch.bfloat16 and q.dim() == 4 and q.shape[3] == 576 and q.is_contiguous()
@@ -164,12 +207,12 @@ def mla_decode(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tenso
     assert seq_lens.dtype == torch.int32 and seq_lens.numel() == batch
     assert out.dtype == torch.bfloat16 and tuple(out.shape) == (batch, nq, heads, 512)
     assert lse.dtype == torch.float32 and tuple(lse.shape) == (batch, nq, heads)
-    assert kv_pages.is_contiguous() and kv_pages.dim() == 3 and kv_pages.shape[2] == 576
+    dtype = kv_dtype_code(kv_pages)
     lib = load_library()
     fn = lib.mla_decode_f16_operands if f16_operands else lib.mla_decode
     st = fn(
-        _ptr(q), _ptr(kv_pages), int(kv_pages.shape[0]), int(kv_pages.shape[1]),
-        kv_dtype_code(kv_pages), _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
+        _ptr(q), _ptr(kv_pages), int(kv_pages.shape[0]), _page_size(kv_pages),
+        dtype, _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
         batch, nq, heads, float(sm_scale), float(kv_scale), int(num_ctas), _ptr(workspace),
         int(workspace.numel() * workspace.element_size()), _ptr(out), _ptr(lse),
         _stream(stream))
@@ -195,10 +238,10 @@ def mla_decode_grouped(q: torch.Tensor, kv_pages: torch.Tensor, block_table: tor
     assert prefix_pages.dtype == torch.int32 and prefix_pages.is_contiguous()
     assert out.dtype == torch.bfloat16 and tuple(out.shape) == (batch, nq, heads, 512)
     assert lse.dtype == torch.float32 and tuple(lse.shape) == (batch, nq, heads)
-    assert kv_pages.is_contiguous() and kv_pages.dim() == 3 and kv_pages.shape[2] == 576
+    dtype = kv_dtype_code(kv_pages)
     st = load_library().mla_decode_grouped(
-        _ptr(q), _ptr(kv_pages), int(kv_pages.shape[0]), int(kv_pages.shape[1]),
-        kv_dtype_code(kv_pages), _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
+        _ptr(q), _ptr(kv_pages), int(kv_pages.shape[0]), _page_size(kv_pages),
+        dtype, _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
         batch, nq, heads, int(forks), _ptr(prefix_pages), float(sm_scale), float(kv_scale),
         int(num_ctas), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
         _ptr(out), _ptr(lse), _stream(stream))
@@ -248,6 +291,141 @@ def mla_kv_check(page_tags: torch.Tensor, block_table: torch.Tensor,
     _check(st, "mla_kv_check")
 
 
+def _int32(device: torch.device, *tensors) -> None:
+    """Each tensor is a contiguous int32 (or, for tags and status words, uint32) one on `device`."""
+    for t in tensors:
+        assert t.dtype == torch.int32 or t.dtype == torch.uint32
+        assert t.is_contiguous() and t.device == device
+
+
+def mla_kv_gather(kv_pages: torch.Tensor, kv_scale: float, block_table: torch.Tensor,
+                  cu_tokens: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor,
+                  starts: torch.Tensor | None = None, stream=None) -> None:
+    """Read cached entries back as bfloat16 rows ``latent [n, 512]`` and ``rope [n, 64]``.
+
+    Rows ``cu_tokens[b] .. cu_tokens[b + 1] - 1`` receive tokens ``starts[b]``
+    (0 without ``starts``) and on of request b, through ``block_table [batch,
+    max_pages]``. Tokens in no page of the cache give zero rows; rows from
+    ``cu_tokens[batch]`` on are left as they were. ``kv_pages`` as in
+    :func:`kv_dtype_code`.
+    """
+    dtype, device = kv_dtype_code(kv_pages), kv_pages.device
+    assert kv_pages.is_cuda and block_table.dim() == 2
+    batch, max_pages = block_table.shape
+    rows = latent.shape[0]
+    _int32(device, block_table, cu_tokens)
+    assert cu_tokens.dim() == 1 and cu_tokens.shape[0] == batch + 1
+    if starts is not None:
+        _int32(device, starts)
+        assert starts.numel() == batch
+    assert latent.dtype == torch.bfloat16 and rope.dtype == torch.bfloat16
+    assert latent.shape == (rows, 512) and rope.shape == (rows, 64)
+    assert latent.is_contiguous() and rope.is_contiguous()
+    assert latent.device == device and rope.device == device
+    st = load_library().mla_kv_gather(_ptr(kv_pages), kv_pages.shape[0], _page_size(kv_pages),
+                                      dtype, kv_scale, _ptr(block_table), max_pages, _ptr(starts),
+                                      _ptr(cu_tokens), batch, rows, _ptr(latent), _ptr(rope),
+                                      _stream(stream))
+    _check(st, "mla_kv_gather")
+
+
+def mla_kv_alloc(seq_lens: torch.Tensor, new_tokens: torch.Tensor, pages_held: torch.Tensor,
+                 free_pages: torch.Tensor, free_count: torch.Tensor, num_pages: int,
+                 block_table: torch.Tensor, seq_lens_out: torch.Tensor,
+                 pages_held_out: torch.Tensor, free_count_out: torch.Tensor,
+                 cu_tokens: torch.Tensor, slot_mapping: torch.Tensor,
+                 request_status: torch.Tensor, page_tags: torch.Tensor | None = None,
+                 expected_tags: torch.Tensor | None = None, stream=None) -> None:
+    """Extend each request by ``new_tokens[b]`` tokens: pages, block-table rows, tags, slots.
+
+    Takes the pages it needs off the end of ``free_pages[:free_count]``, appends
+    them to ``block_table`` rows (``pages_held[b]`` entries in use), raises their
+    ``page_tags`` and records the new tags in ``expected_tags`` (both or neither),
+    and writes ``slot_mapping`` (the new tokens' slots, request by request, -1
+    behind the last), ``cu_tokens [batch + 1]`` (first row of each request),
+    ``seq_lens_out``, ``pages_held_out`` and ``free_count_out`` (each may be its
+    input) and ``request_status`` (MLA_KV_ALLOC_* bits; a refused request gets
+    length -1 and slots -1).
+    """
+    device = block_table.device
+    assert block_table.is_cuda and block_table.dim() == 2
+    batch, max_pages = block_table.shape
+    _int32(device, seq_lens, new_tokens, pages_held, free_pages, free_count, block_table,
+           seq_lens_out, pages_held_out, free_count_out, cu_tokens, slot_mapping, request_status)
+    assert seq_lens.numel() == batch and new_tokens.numel() == batch
+    assert pages_held.numel() == batch and pages_held_out.numel() == batch
+    assert seq_lens_out.numel() == batch and request_status.numel() == batch
+    assert free_count.numel() == 1 and free_count_out.numel() == 1
+    assert cu_tokens.numel() == batch + 1
+    assert (page_tags is None) == (expected_tags is None)
+    if page_tags is not None:
+        _int32(device, page_tags, expected_tags)
+        assert page_tags.numel() == num_pages and expected_tags.shape == block_table.shape
+    st = load_library().mla_kv_alloc(
+        _ptr(seq_lens), _ptr(new_tokens), batch, 64, _ptr(pages_held), _ptr(free_pages),
+        _ptr(free_count), free_pages.numel(), num_pages, _ptr(block_table), max_pages,
+        _ptr(page_tags), _ptr(expected_tags), _ptr(seq_lens_out), _ptr(pages_held_out),
+        _ptr(free_count_out), _ptr(cu_tokens), _ptr(slot_mapping), slot_mapping.numel(),
+        _ptr(request_status), _stream(stream))
+    _check(st, "mla_kv_alloc")
+
+
+def _row_stride(probs: torch.Tensor) -> int:
+    """Elements between the rows of ``[batch, rows, vocab]`` probabilities, evenly apart."""
+    batch, rows, vocab = probs.shape
+    assert vocab == 1 or probs.stride(2) == 1
+    stride = probs.stride(1) if rows > 1 else probs.stride(0) if batch > 1 else vocab
+    assert stride >= vocab and (batch == 1 or probs.stride(0) == rows * stride)
+    return stride
+
+
+def mla_verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | None,
+                      draft_tokens: torch.Tensor, uniforms: torch.Tensor,
+                      out_tokens: torch.Tensor, num_accepted: torch.Tensor,
+                      num_drafts: torch.Tensor | None = None,
+                      seq_lens: torch.Tensor | None = None,
+                      seq_lens_out: torch.Tensor | None = None, stream=None) -> None:
+    """Keep drafted tokens with probability min(1, p / q) and sample the next token.
+
+    ``target_probs [batch, K + 1, vocab]`` and ``draft_probs [batch, K, vocab]``
+    (or None: the drafter was certain) are float32 or bfloat16 probabilities whose
+    rows may be padded (an even stride), ``draft_tokens [batch, K]``, ``uniforms
+    [batch, K + 1]`` float32 in [0, 1): one per draft, the last for the sample.
+    ``num_drafts [batch]`` limits a request to fewer than K drafts. Writes
+    ``out_tokens [batch, K + 1]`` (kept drafts, next token, then -1),
+    ``num_accepted [batch]`` and, given ``seq_lens``, ``seq_lens_out``: the
+    lengths without the rejected drafts (may be ``seq_lens`` itself).
+    """
+    assert target_probs.is_cuda and target_probs.dim() == 3
+    device = target_probs.device
+    batch, rows, vocab = target_probs.shape
+    drafts = rows - 1
+    assert target_probs.dtype in (torch.float32, torch.bfloat16)
+    dtype = MLA_PROB_F32 if target_probs.dtype == torch.float32 else MLA_PROB_BF16
+    target_stride = _row_stride(target_probs) if batch > 0 else vocab
+    draft_stride = vocab
+    if draft_probs is not None:
+        assert draft_probs.dtype == target_probs.dtype and draft_probs.device == device
+        assert draft_probs.shape == (batch, drafts, vocab)
+        if batch > 0 and drafts > 0:
+            draft_stride = _row_stride(draft_probs)
+    assert draft_tokens.shape == (batch, drafts) and out_tokens.shape == (batch, rows)
+    assert uniforms.dtype == torch.float32 and uniforms.shape == (batch, rows)
+    assert uniforms.is_contiguous() and uniforms.device == device
+    assert num_accepted.numel() == batch
+    _int32(device, draft_tokens, out_tokens, num_accepted)
+    assert seq_lens_out is None or seq_lens is not None
+    for t in (num_drafts, seq_lens, seq_lens_out):
+        if t is not None:
+            _int32(device, t)
+            assert t.numel() == batch
+    st = load_library().mla_verify_drafts(
+        _ptr(target_probs), target_stride, _ptr(draft_probs), draft_stride, dtype,
+        _ptr(draft_tokens), _ptr(uniforms), _ptr(num_drafts), _ptr(seq_lens), batch, drafts, vocab,
+        _ptr(out_tokens), _ptr(num_accepted), _ptr(seq_lens_out), _stream(stream))
+    _check(st, "mla_verify_drafts")
+
+
 def mla_decode_static_scratch(q: torch.Tensor, kv_pages: torch.Tensor,
                               block_table: torch.Tensor, seq_lens: torch.Tensor, sm_scale: float,
                               kv_scale: float, out: torch.Tensor, lse: torch.Tensor,
@@ -268,12 +446,12 @@ def mla_decode_static_scratch(q: torch.Tensor, kv_pages: torch.Tensor,
     assert seq_lens.dtype == torch.int32 and seq_lens.numel() == batch
     assert out.dtype == torch.bfloat16 and tuple(out.shape) == (batch, nq, heads, 512)
     assert lse.dtype == torch.float32 and tuple(lse.shape) == (batch, nq, heads)
-    assert kv_pages.is_contiguous() and kv_pages.dim() == 3 and kv_pages.shape[2] == 576
+    dtype = kv_dtype_code(kv_pages)
     if device_status is not None:
         assert device_status.dtype == torch.int32 and device_status.numel() >= 1
     st = load_library().mla_decode_static_scratch(
-        _ptr(q), _ptr(kv_pages), int(kv_pages.shape[0]), int(kv_pages.shape[1]),
-        kv_dtype_code(kv_pages), _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
+        _ptr(q), _ptr(kv_pages), int(kv_pages.shape[0]), _page_size(kv_pages),
+        dtype, _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
         batch, nq, heads, float(sm_scale), float(kv_scale), int(num_ctas), _ptr(out), _ptr(lse),
         _ptr(device_status), _stream(stream))
     _check(st, "mla_decode_static_scratch")

@@ -2,6 +2,7 @@
 // workspace carving and the two launches (decode kernel, then piece combine).
 #include <atomic>
 
+#include "kv_e2m1.cuh"
 #include "mla_common.cuh"
 #include "mla_internal.h"
 
@@ -56,9 +57,12 @@ mla_status decode_impl(const void* q, const void* kv_pages, int64_t num_pages, i
   if (batch < 0 || num_pages < 0 || max_pages < 1 || num_ctas < 0) return MLA_ERR_INVALID_ARG;
   if (num_queries < 1 || num_queries > MLA_MAX_QUERIES) return MLA_ERR_INVALID_ARG;
   if (page_size != kPageSize) return MLA_ERR_UNSUPPORTED;
-  if (kv_dtype != MLA_KV_E4M3 && kv_dtype != MLA_KV_BF16) return MLA_ERR_INVALID_ARG;
+  if (kv_dtype != MLA_KV_E4M3 && kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_E2M1)
+    return MLA_ERR_INVALID_ARG;
   if (num_heads != 16 && num_heads != 32 && num_heads != 64) return MLA_ERR_UNSUPPORTED;
   if (!isfinite(sm_scale) || !isfinite(kv_scale) || !(kv_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+  if (kv_dtype == MLA_KV_E2M1 && f16_operands) return MLA_ERR_UNSUPPORTED;
+  if (kv_dtype == MLA_KV_E2M1 && !e2m1_scale_ok(kv_scale)) return MLA_ERR_INVALID_ARG;
   if (batch == 0) return MLA_OK;
   if (!q || !kv_pages || !block_table || !seq_lens || !out || !lse) return MLA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(kv_pages, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
@@ -88,6 +92,7 @@ mla_status decode_impl(const void* q, const void* kv_pages, int64_t num_pages, i
   p.nq = num_queries;
   p.heads = num_heads;
   p.bf16 = kv_dtype == MLA_KV_BF16;
+  p.e2m1 = kv_dtype == MLA_KV_E2M1;
   p.score_mul = sm_scale * kLog2e * kv_scale;
   p.kv_scale = kv_scale;
   p.G = G;
@@ -103,7 +108,7 @@ mla_status decode_impl(const void* q, const void* kv_pages, int64_t num_pages, i
 
   if (!p.bf16 && num_pages > (int64_t)(0x7fffffff / kPageSize)) return MLA_ERR_UNSUPPORTED;
   if (grouped) {
-    if (p.bf16 || f16_operands) return MLA_ERR_UNSUPPORTED;  // FP8 cache, FP8 operands only
+    if (p.bf16 || f16_operands) return MLA_ERR_UNSUPPORTED;  // FP8 operands only
     p.forks = forks;
     p.prefix_pages = prefix_pages;
   }

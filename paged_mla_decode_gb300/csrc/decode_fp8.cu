@@ -22,7 +22,12 @@
 // is read in place through an MN-major descriptor (no distinct values: "How to
 // serve trillions of tokens ...", section "First, understand the workload").
 //
-// Warp roles (416 threads):
+// A 4-bit cache (kv_e2m1.cuh) takes the same path (kE2m1): its pages land in a second,
+// smaller ring as stored, four expander warps rewrite each as the swizzled e4m3 page
+// that the contractions read (a table lookup, exact), and everything after that is
+// the e4m3 kernel. It trades one ring slot for the raw pages (kRing 4 + 2 raw).
+//
+// Warp roles (416 threads; 544 with the expanders):
 //   warps 0-7  q loading, softmax and epilogue. Row t of A and S is (head
 //              16*(t/32) + t%16, part (t/16)%2), part 0 = hi, 1 = lo. Warp w reads
 //              TMEM lanes 32*(w%4) .. +31; thread (w, lane) handles head
@@ -36,6 +41,9 @@
 //              (128-byte swizzled latent blocks, 64-byte swizzled rope block).
 //   warps 9-10 issue QK of even / odd pages (lane 0); warp 9 allocates TMEM.
 //   warps 11-12 issue PV of even / odd pages (lane 0).
+//   warps 13-16 (4-bit cache only) expand raw pages into the ring. 1,152 blocks of 32
+//              elements a page, 9 a thread; a thread keeps one token, so its swizzle
+//              is a constant, and eight threads write eight rows without conflicts.
 // A thread that issues MMAs stalls for a while after each batch (until the
 // tensor pipe's queue has room), so two issuers per contraction keep the pipe
 // fed: one issues while the other waits.
@@ -50,6 +58,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include "kv_e2m1.cuh"
 #include "mla_common.cuh"
 #include "mla_internal.h"
 #include "tc_ptx.cuh"
@@ -76,8 +85,8 @@ constexpr int kTmaWarp = kSmWarps;                   // 8
 // of MMAs (an issuing thread waits on its MMA queue) overlaps the other's issue.
 constexpr int kQkWarp0 = kSmWarps + 1;               // 9: also allocates TMEM
 constexpr int kPvWarp0 = kSmWarps + 3;               // 11
-constexpr int kThreads = 32 * (kSmWarps + 5);        // 416
-constexpr int kRing = 5;                             // pages in flight
+constexpr int kExpWarp0 = kSmWarps + 5;              // 13: expanders of a 4-bit cache
+constexpr int kExpWarps = 4;
 constexpr int kPageBytes = kPageSize * kDEntry;      // 36864
 constexpr int kLatBlock = kPageSize * 128;           // 8192: 64 rows x 128 dims
 constexpr int kRopeOff = 4 * kLatBlock;              // rope block within a page slot
@@ -106,59 +115,75 @@ constexpr uint32_t kQCol = 0;
 __device__ __forceinline__ uint32_t s_col(int b) { return 128u + 64u * (uint32_t)b; }
 constexpr uint32_t kOCol = 256;
 
-// shared memory map (offsets from a 1024-aligned base)
-constexpr int kOffPages = 0;
-constexpr int kOffQRope = kOffPages + kRing * kPageBytes;   // 128 rows x 64 B, 64B swizzle
-constexpr int kPBufs = 3;                                   // P^T buffers (QK runs 2 pages ahead)
-constexpr int kOffP = kOffQRope + 128 * 64;                 // [kPBufs] P^T buffers
-constexpr int kOffAlpha = kOffP + kPBufs * kPBytes;         // float [64]
-constexpr int kOffLinv = kOffAlpha + 256;                   // float [64]
-constexpr int kOffPmax = kOffLinv + 256;                    // float [2 pages][2 halves][64]
-constexpr int kOffLsum = kOffPmax + 1024;                   // float [2 halves][64]
-constexpr int kOffFlags = kOffLsum + 512;                   // int [4]
-constexpr int kOffPlan = kOffFlags + 16;                    // int64 [6]
-constexpr int kDescRing = 64;                               // page descriptors in flight
+constexpr int kPBufs = 3;        // P^T buffers (QK runs 2 pages ahead)
+constexpr int kDescRing = 64;    // page descriptors in flight
 constexpr int kTableAhead = 32;  // pages described (block-table read started) before issue
-constexpr int kOffDesc = kOffPlan + 48;                     // PageDesc [kDescRing]
-constexpr int kOffBar = kOffDesc + 16 * kDescRing;
-constexpr int BAR_PAGE_FULL = 0;                  // [kRing] TMA bytes (or zero fill) landed
-// PV(k) completes barrier BAR_PV_DONE + k % kRing (one commit per page): it frees
-// page slot k % kRing for the TMA warp, P buffer k % 3 for the softmax warps, and
-// marks O^T current for a rescale. Every wait on it names a page whose successor
-// on the same barrier (k + kRing) cannot have completed yet, so parities are exact.
-constexpr int BAR_PV_DONE = kRing;                // [kRing]
-constexpr int BAR_S_FULL = 2 * kRing;             // [2] page j: buffer j % 2
-constexpr int BAR_S_EMPTY = BAR_S_FULL + 2;       // [2] (softmax warps)
-constexpr int BAR_P_FULL = BAR_S_EMPTY + 2;       // [kPBufs] page j: buffer j % 3 (softmax warps)
-constexpr int BAR_O_FULL = BAR_P_FULL + kPBufs;
-constexpr int BAR_O_EMPTY = BAR_O_FULL + 1;       // (softmax warps)
-constexpr int BAR_Q_READY = BAR_O_EMPTY + 1;      // (softmax warps)
-constexpr int BAR_Q_EMPTY = BAR_Q_READY + 1;
-constexpr int BAR_DRAIN = BAR_Q_EMPTY + 1;       // [4] one per issuer warp
+
+// Shared memory map (offsets from a 1024-aligned base) and barriers.
+template <bool kE2m1>
+struct Map {
+  static constexpr int kThreads = 32 * (kExpWarp0 + (kE2m1 ? kExpWarps : 0));  // 416, 544
+  static constexpr int kRing = kE2m1 ? 4 : 5;          // e4m3 pages in flight
+  static constexpr int kRawRing = kE2m1 ? 2 : 0;       // 4-bit pages in flight
+  static constexpr int kOffPages = 0;
+  static constexpr int kOffQRope = kOffPages + kRing * kPageBytes;  // 128 rows x 64 B, 64B swizzle
+  static constexpr int kOffP = kOffQRope + 128 * 64;                // [kPBufs] P^T buffers
+  static constexpr int kOffRaw = kOffP + kPBufs * kPBytes;          // [kRawRing] 4-bit pages
+  static constexpr int kOffAlpha = kOffRaw + kRawRing * kE2m1PageBytes;  // float [64]
+  static constexpr int kOffLinv = kOffAlpha + 256;                  // float [64]
+  static constexpr int kOffPmax = kOffLinv + 256;                   // float [2 pages][2 halves][64]
+  static constexpr int kOffLsum = kOffPmax + 1024;                  // float [2 halves][64]
+  static constexpr int kOffLut = kOffLsum + 512;                    // uint64 [16] (4-bit cache)
+  static constexpr int kOffFlags = kOffLut + (kE2m1 ? 128 : 0);     // int [4]
+  static constexpr int kOffPlan = kOffFlags + 16;                   // int64 [6]
+  static constexpr int kOffDesc = kOffPlan + 48;                    // PageDesc [kDescRing]
+  static constexpr int kOffBar = kOffDesc + 16 * kDescRing;
+  // the page is readable in its ring slot: its TMA bytes landed (or there are none), or
+  // every expander warp has written its part
+  static constexpr int BAR_PAGE_FULL = 0;                 // [kRing]
+  // PV(k) completes barrier BAR_PV_DONE + k % kRing (one commit per page): it frees
+  // page slot k % kRing for the TMA warp (the expanders), P buffer k % 3 for the softmax
+  // warps, and marks O^T current for a rescale. Every wait on it names a page whose
+  // successor on the same barrier (k + kRing) cannot have completed yet, so parities
+  // are exact.
+  static constexpr int BAR_PV_DONE = kRing;               // [kRing]
+  static constexpr int BAR_S_FULL = 2 * kRing;            // [2] page j: buffer j % 2
+  static constexpr int BAR_S_EMPTY = BAR_S_FULL + 2;      // [2] (softmax warps)
+  static constexpr int BAR_P_FULL = BAR_S_EMPTY + 2;      // [kPBufs] page j: buffer j % 3 (softmax warps)
+  static constexpr int BAR_O_FULL = BAR_P_FULL + kPBufs;
+  static constexpr int BAR_O_EMPTY = BAR_O_FULL + 1;      // (softmax warps)
+  static constexpr int BAR_Q_READY = BAR_O_EMPTY + 1;     // (softmax warps)
+  static constexpr int BAR_Q_EMPTY = BAR_Q_READY + 1;
+  static constexpr int BAR_DRAIN = BAR_Q_EMPTY + 1;       // [4] one per issuer warp
+  static constexpr int BAR_RAW_FULL = BAR_DRAIN + 4;      // [kRawRing] bulk-copy bytes landed
+  static constexpr int BAR_RAW_EMPTY = BAR_RAW_FULL + kRawRing;  // [kRawRing] (expander warps)
 #ifdef MLA_TEST_STALL_QK
-// Test build only: a barrier that nothing ever completes. The MMA issuer waits on
-// it before the QK of its third page, so the wait runs out and the CTA takes the
-// timeout path (stop every role, drain the copies and MMAs in flight, free TMEM).
-constexpr int BAR_TEST_STALL = BAR_DRAIN + 4;
-constexpr int kNumBars = BAR_TEST_STALL + 1;
+  // Test build only: a barrier that nothing ever completes. The MMA issuer waits on
+  // it before the QK of its third page, so the wait runs out and the CTA takes the
+  // timeout path (stop every role, drain the copies and MMAs in flight, free TMEM).
+  static constexpr int BAR_TEST_STALL = BAR_RAW_EMPTY + kRawRing;
+  static constexpr int kNumBars = BAR_TEST_STALL + 1;
 #else
-constexpr int kNumBars = BAR_DRAIN + 4;
+  static constexpr int kNumBars = BAR_RAW_EMPTY + kRawRing;
 #endif
-// arrivals that complete a phase of barrier i
-__device__ __forceinline__ uint32_t bar_count(int i) {
-  if ((i >= BAR_S_EMPTY && i < BAR_S_EMPTY + 2) || (i >= BAR_P_FULL && i < BAR_P_FULL + kPBufs) ||
-      i == BAR_O_EMPTY || i == BAR_Q_READY)
-    return kSmWarps;
-  if (i == BAR_Q_EMPTY || i == BAR_O_FULL) return 2;  // both issuer warps of the kind commit
-  return 1;
-}
-constexpr int kOffTmem = kOffBar + 8 * kNumBars;
-constexpr int kSmemUsed = kOffTmem + 16;
-constexpr int kSmemBytes = kSmemUsed + 1024;  // slack for the 1024 alignment
-// grouped decode: the two segments' plans (int64 [32]) after the common map
-constexpr int kOffPlanX = (kSmemUsed + 15) & ~15;
-constexpr int kSmemBytesGrouped = kOffPlanX + 256 + 1024;
-static_assert(kSmemBytesGrouped <= 227 * 1024, "shared memory map exceeds 227 KB");
+  // arrivals that complete a phase of barrier i
+  static __device__ __forceinline__ uint32_t bar_count(int i) {
+    if ((i >= BAR_S_EMPTY && i < BAR_S_EMPTY + 2) || (i >= BAR_P_FULL && i < BAR_P_FULL + kPBufs) ||
+        i == BAR_O_EMPTY || i == BAR_Q_READY)
+      return kSmWarps;
+    if (i == BAR_Q_EMPTY || i == BAR_O_FULL) return 2;  // both issuer warps of the kind commit
+    if (kE2m1 && (i < kRing || (i >= BAR_RAW_EMPTY && i < BAR_RAW_EMPTY + kRawRing)))
+      return kExpWarps;
+    return 1;
+  }
+  static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
+  static constexpr int kSmemUsed = kOffTmem + 16;
+  static constexpr int kSmemBytes = kSmemUsed + 1024;  // slack for the 1024 alignment
+  // grouped decode: the two segments' plans (int64 [32]) after the common map
+  static constexpr int kOffPlanX = (kSmemUsed + 15) & ~15;
+  static constexpr int kSmemBytesGrouped = kOffPlanX + 256 + 1024;
+  static_assert(kSmemBytesGrouped <= 227 * 1024, "shared memory map exceeds 227 KB");
+};
 
 enum Flag { F_ABORT = 0, F_PIECE_BAD = 1 };
 
@@ -177,6 +202,7 @@ constexpr int16_t kDescShared = 8;  // grouped decode: a shared-prefix page (inf
 
 struct Fp8Params {
   const __nv_bfloat16* q;
+  const uint8_t* kv;  // 4-bit cache only (an e4m3 cache is read through the tensor maps)
   int64_t num_pages;
   const int32_t* block_table;
   int max_pages;
@@ -306,24 +332,91 @@ __device__ __forceinline__ uint32_t e5m2x2_of(float lo, float hi) {
   return r;
 }
 
+// Rows of the expansion table by exponent nibble (e2m1_as_e4m3), copied to shared memory.
+__device__ const uint64_t kE2m1Lut[16] = {
+    e2m1_as_e4m3(0),  e2m1_as_e4m3(1),  e2m1_as_e4m3(2),  e2m1_as_e4m3(3),
+    e2m1_as_e4m3(4),  e2m1_as_e4m3(5),  e2m1_as_e4m3(6),  e2m1_as_e4m3(7),
+    e2m1_as_e4m3(8),  e2m1_as_e4m3(9),  e2m1_as_e4m3(10), e2m1_as_e4m3(11),
+    e2m1_as_e4m3(12), e2m1_as_e4m3(13), e2m1_as_e4m3(14), e2m1_as_e4m3(15)};
+
+// One expander thread's share of a page: token t = x % 64, and of each pair of blocks
+// (2i, 2i + 1) the one of its half x / 64, whose nibble lies in byte i of the token's
+// exponents. Three blocks at a time, so that their loads overlap.
+__device__ __forceinline__ void expand_page(uint32_t raw, uint32_t page, uint32_t lut, int x) {
+  const int t = x & 63, half = x >> 6;
+  const uint32_t row = page + t * 128, sw = (uint32_t)(t & 7);
+  const uint32_t rope = page + kRopeOff + t * 64, sw_rope = (uint32_t)((t >> 1) & 3);
+#pragma unroll
+  for (int i0 = 0; i0 < kE2m1Blocks / 2; i0 += 3) {
+    uint4 w[3];
+    uint2 tab[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int i = i0 + k;
+      uint32_t e;
+      asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(e) : "r"(raw + e2m1_exp_offset(2 * i, t)));
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                   : "=r"(w[k].x), "=r"(w[k].y), "=r"(w[k].z), "=r"(w[k].w)
+                   : "r"(raw + e2m1_code_offset(2 * i, t) + half * e2m1_code_offset(1, 0)));
+      asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n"
+                   : "=r"(tab[k].x), "=r"(tab[k].y)
+                   : "r"(lut + 8 * (half ? e >> 4 : e & 15u)));
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int i = i0 + k;
+      const uint2 c0 = e2m1x8_to_e4m3(w[k].x, tab[k].x, tab[k].y);
+      const uint2 c1 = e2m1x8_to_e4m3(w[k].y, tab[k].x, tab[k].y);
+      const uint2 c2 = e2m1x8_to_e4m3(w[k].z, tab[k].x, tab[k].y);
+      const uint2 c3 = e2m1x8_to_e4m3(w[k].w, tab[k].x, tab[k].y);
+      // block b = 2i + half: chunks 2(b % 4), 2(b % 4) + 1 of the token's row of latent
+      // block b / 4; the last two blocks are the rope row's four chunks
+      uint32_t d0, d1;
+      if (i < 8) {
+        const uint32_t c = 4u * (i & 1) + 2u * half;
+        d0 = row + (i >> 1) * kLatBlock + ((c ^ sw) << 4);
+        d1 = row + (i >> 1) * kLatBlock + (((c + 1) ^ sw) << 4);
+      } else {
+        const uint32_t c = 2u * half;
+        d0 = rope + ((c ^ sw_rope) << 4);
+        d1 = rope + (((c + 1) ^ sw_rope) << 4);
+      }
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(d0), "r"(c0.x), "r"(c0.y),
+                   "r"(c1.x), "r"(c1.y) : "memory");
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(d1), "r"(c2.x), "r"(c2.y),
+                   "r"(c3.x), "r"(c3.y) : "memory");
+    }
+  }
+}
+
 // kGrouped: the grouped decode (GroupPlan): this CTA's shared-prefix range, then
 // its suffix range; otherwise mla_decode's single plan (Plan).
-template <bool kGrouped>
-__global__ void __launch_bounds__(kThreads, 1)
+// kE2m1: a 4-bit cache, expanded to e4m3 pages by four more warps; otherwise e4m3.
+template <bool kGrouped, bool kE2m1>
+__global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
     decode_fp8_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap lat_map,
                       const __grid_constant__ CUtensorMap rope_map) {
+  using M = Map<kE2m1>;
+  constexpr int kRing = M::kRing;
+  constexpr int kOffPages = M::kOffPages, kOffQRope = M::kOffQRope, kOffP = M::kOffP;
+  constexpr int kOffDesc = M::kOffDesc;
+  constexpr int BAR_PAGE_FULL = M::BAR_PAGE_FULL, BAR_PV_DONE = M::BAR_PV_DONE;
+  constexpr int BAR_S_FULL = M::BAR_S_FULL, BAR_S_EMPTY = M::BAR_S_EMPTY;
+  constexpr int BAR_P_FULL = M::BAR_P_FULL, BAR_O_FULL = M::BAR_O_FULL;
+  constexpr int BAR_O_EMPTY = M::BAR_O_EMPTY, BAR_Q_READY = M::BAR_Q_READY;
+  constexpr int BAR_Q_EMPTY = M::BAR_Q_EMPTY, BAR_DRAIN = M::BAR_DRAIN;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_a = smem_u32(smem_raw);
   const uint32_t sbase = (raw_a + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - raw_a);
-  float* alpha_s = reinterpret_cast<float*>(smem + kOffAlpha);
-  float* linv_s = reinterpret_cast<float*>(smem + kOffLinv);
-  float* pmax_s = reinterpret_cast<float*>(smem + kOffPmax);
-  float* lsum_s = reinterpret_cast<float*>(smem + kOffLsum);
-  volatile int* flags = reinterpret_cast<volatile int*>(smem + kOffFlags);
-  int64_t* s_plan = reinterpret_cast<int64_t*>(smem + kOffPlan);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffTmem);
-  auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * (uint32_t)i; };
+  float* alpha_s = reinterpret_cast<float*>(smem + M::kOffAlpha);
+  float* linv_s = reinterpret_cast<float*>(smem + M::kOffLinv);
+  float* pmax_s = reinterpret_cast<float*>(smem + M::kOffPmax);
+  float* lsum_s = reinterpret_cast<float*>(smem + M::kOffLsum);
+  volatile int* flags = reinterpret_cast<volatile int*>(smem + M::kOffFlags);
+  int64_t* s_plan = reinterpret_cast<int64_t*>(smem + M::kOffPlan);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::kOffTmem);
+  auto bar = [&](int i) -> uint32_t { return sbase + M::kOffBar + 8u * (uint32_t)i; };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) MLA_STAMP(kStEntry, 0);
@@ -335,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // itself needs the split kernel to have completed (griddep_wait before q_op).
   Plan plan{p.seq_lens, p.batch, p.nq, p.max_pages, kPageSize, p.G, 0};
   const int c = blockIdx.x;
-  int64_t* s_plan_x = reinterpret_cast<int64_t*>(smem + kOffPlanX);  // kGrouped only
+  int64_t* s_plan_x = reinterpret_cast<int64_t*>(smem + M::kOffPlanX);  // kGrouped only
   if (warp == 0) {
     if constexpr (kGrouped) {
       // both plans (row table written by group_plan_kernel): this CTA's prefix
@@ -375,12 +468,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if (warp == kTmaWarp && lane == 0) {
-    tc::prefetch_tensormap(&lat_map);
-    tc::prefetch_tensormap(&rope_map);
-    for (int i = 0; i < kNumBars; ++i) tc::mbar_init(bar(i), bar_count(i));
+    if constexpr (!kE2m1) {
+      tc::prefetch_tensormap(&lat_map);
+      tc::prefetch_tensormap(&rope_map);
+    }
+    for (int i = 0; i < M::kNumBars; ++i) tc::mbar_init(bar(i), M::bar_count(i));
     tc::fence_mbar_init();
     flags[F_ABORT] = 0;
     flags[F_PIECE_BAD] = 0;
+  }
+  if constexpr (kE2m1) {
+    if (warp == kExpWarp0 && lane < 16)
+      reinterpret_cast<uint64_t*>(smem + M::kOffLut)[lane] = kE2m1Lut[lane];
   }
   if (warp == kQkWarp0) {
     tc::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -471,6 +570,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t page = d->page;
           const bool page_ok = page >= 0 && (int64_t)page < p.num_pages;
           if (page_ok) d->flags |= kDescPageOk;
+          if constexpr (kE2m1) {
+            // the page as stored, one contiguous copy into the raw ring
+            const int slot = (int)(j % M::kRawRing);
+            if (j >= M::kRawRing &&
+                (!tc::mbar_wait(bar(M::BAR_RAW_EMPTY + slot),
+                                ((uint32_t)(j / M::kRawRing) - 1) & 1, kWaitNs) ||
+                 flags[F_ABORT])) {
+              ok = false;
+              break;
+            }
+            if (page_ok) {
+              tc::mbar_arrive_expect_tx(bar(M::BAR_RAW_FULL + slot), (uint32_t)kE2m1PageBytes);
+              tc::bulk_load_hint(sbase + M::kOffRaw + slot * kE2m1PageBytes,
+                                 p.kv + (int64_t)page * kE2m1PageBytes, (uint32_t)kE2m1PageBytes,
+                                 bar(M::BAR_RAW_FULL + slot), pol);
+            } else {
+              tc::mbar_arrive(bar(M::BAR_RAW_FULL + slot));  // bad id: nothing to expand
+            }
+            for (int u = 0; u < 2 && jn < npages && jn <= j + kTableAhead; ++u) describe_next();
+            continue;
+          }
           const int slot = (int)(j % kRing);
           const uint32_t round = (uint32_t)(j / kRing);
           const uint32_t page_base = sbase + kOffPages + slot * kPageBytes;
@@ -502,11 +622,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         cp_async_wait<0>();
         if (!ok) abort_cta();
         // no copy may land after the CTA exits: wait for the last issued pages
-        for (int64_t jj = j > kRing ? j - kRing : 0; jj < j; ++jj)
-          tc::mbar_wait(bar(BAR_PAGE_FULL + (int)(jj % kRing)), (uint32_t)(jj / kRing) & 1,
+        constexpr int kLanding = kE2m1 ? M::kRawRing : kRing;
+        constexpr int kLandBar = kE2m1 ? M::BAR_RAW_FULL : BAR_PAGE_FULL;
+        for (int64_t jj = j > kLanding ? j - kLanding : 0; jj < j; ++jj)
+          tc::mbar_wait(bar(kLandBar + (int)(jj % kLanding)), (uint32_t)(jj / kLanding) & 1,
                         kDrainWaitNs);
       }
       __syncwarp();
+    } else if (kE2m1 && warp >= kExpWarp0) {
+      // =================== expanders of a 4-bit cache (4 warps) ===================
+      if constexpr (kE2m1) {
+        const int x = tid - 32 * kExpWarp0;
+        bool ok = true;
+        for (int64_t j = 0; j < npages; ++j) {
+          const int rs = (int)(j % M::kRawRing), slot = (int)(j % kRing);
+          ok = tc::mbar_wait(bar(M::BAR_RAW_FULL + rs), (uint32_t)(j / M::kRawRing) & 1, kWaitNs);
+          // the page that held the slot has been read by its PV (and its QK before that)
+          if (ok && j >= kRing)
+            ok = tc::mbar_wait(bar(BAR_PV_DONE + slot), ((uint32_t)(j / kRing) - 1) & 1, kWaitNs);
+          ok = __all_sync(0xffffffffu, ok && !flags[F_ABORT]);
+          if (!ok) break;
+          // a bad page id brought no bytes: its tokens are masked and its value rows
+          // zeroed by the softmax warps
+          if (desc[j % kDescRing].flags & kDescPageOk)
+            expand_page(sbase + M::kOffRaw + rs * kE2m1PageBytes,
+                        sbase + kOffPages + slot * kPageBytes, sbase + M::kOffLut, x);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tc::mbar_arrive(bar(BAR_PAGE_FULL + slot));
+            tc::mbar_arrive(bar(M::BAR_RAW_EMPTY + rs));
+          }
+        }
+        if (!ok && lane == 0) abort_cta();
+      }
     } else if (warp >= kQkWarp0) {
       // ============ MMA issuers: two QK warps, two PV warps; lane 0 issues ============
       // Page k's QK is issued by QK warp k % 2 (into S buffer k % 2, which is that
@@ -554,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (is_qk) {
               // ---- S(k) = A . page(k)^T: latent part of A from TMEM, rope from shared memory ----
 #ifdef MLA_TEST_STALL_QK
-              if (k == 2 && !wait(BAR_TEST_STALL, 0)) {
+              if (k == 2 && !wait(M::BAR_TEST_STALL, 0)) {
                 ok = false;
                 break;
               }
@@ -888,8 +1037,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float l = lsum_s[h] + lsum_s[64 + h];
             linv_s[h] = l > 0.f ? p.kv_scale / l : 0.f;
             if (h < H)
+              // (a NaN in a 4-bit page: lse = +inf, with which the merge makes the row NaN)
               p.ws.part_lse[(int64_t)slot * H + h] =
-                  l > 0.f ? (m - (float)kPOffset + log2f(l)) * kLn2 : -INFINITY;
+                  l > 0.f                 ? (m - (float)kPOffset + log2f(l)) * kLn2
+                  : kE2m1 && !(l == 0.f) ? INFINITY
+                                          : -INFINITY;
           }
           if (t == 0) p.ws.piece_err[slot] = bad;
           named_bar_softmax();
@@ -1082,21 +1234,36 @@ __global__ void __launch_bounds__(32) group_plan_kernel(const Fp8Params p) {
 
 }  // namespace
 
-cudaError_t launch_decode_fp8(const DecodeLaunch& d, cudaStream_t stream) {
+// One variant of the decode kernel: its shared-memory limit once per device, then the launch.
+template <bool kGrouped, bool kE2m1>
+static cudaError_t launch_variant(const Fp8Params& p, const CUtensorMap& lat_map,
+                                  const CUtensorMap& rope_map, cudaStream_t stream) {
+  using M = Map<kE2m1>;
+  constexpr int kBytes = kGrouped ? M::kSmemBytesGrouped : M::kSmemBytes;
   static std::atomic<int> configured[64];
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && !configured[dev].load()) {
-    cudaError_t e = cudaFuncSetAttribute(decode_fp8_kernel<false>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(decode_fp8_kernel<true>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytesGrouped);
+  if (dev < 0 || dev >= 64 || !configured[dev].load()) {
+    cudaError_t e = cudaFuncSetAttribute(decode_fp8_kernel<kGrouped, kE2m1>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
-    configured[dev].store(1);
+    if (dev >= 0 && dev < 64) configured[dev].store(1);
   }
-  const bool grouped = d.prefix_pages != nullptr;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.G);
+  cfg.blockDim = dim3(M::kThreads);
+  cfg.dynamicSmemBytes = kBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_fp8_kernel<kGrouped, kE2m1>, p, lat_map, rope_map);
+}
+
+// Tensor maps of an e4m3 pool viewed as [num_pages * 64 rows][576 bytes] (a page is 64
+// rows): boxes of 64 rows x 128 latent bytes and 64 rows x 64 rope bytes.
+static cudaError_t encode_page_maps(const DecodeLaunch& d, CUtensorMap* lat_map,
+                                    CUtensorMap* rope_map) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (encode == nullptr) {
     cudaDriverEntryPointQueryResult qr;
@@ -1107,24 +1274,32 @@ cudaError_t launch_decode_fp8(const DecodeLaunch& d, cudaStream_t stream) {
       return cudaErrorNotSupported;
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
-  // the page pool viewed as [num_pages * 64 rows][576 bytes]; a page is 64 rows
   const int64_t rows = (d.num_pages > 0 ? d.num_pages : 1) * kPageSize;
   const cuuint64_t dims[2] = {(cuuint64_t)kDEntry, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)kDEntry};
   const cuuint32_t box_lat[2] = {128, (cuuint32_t)kPageSize};
   const cuuint32_t box_rope[2] = {(cuuint32_t)kDRope, (cuuint32_t)kPageSize};
   const cuuint32_t estr[2] = {1, 1};
-  CUtensorMap lat_map, rope_map;
   void* base = const_cast<uint8_t*>(d.kv);
-  CUresult r1 = encode(&lat_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box_lat,
+  CUresult r1 = encode(lat_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box_lat,
                        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  CUresult r2 = encode(&rope_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box_rope,
+  CUresult r2 = encode(rope_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box_rope,
                        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r1 != CUDA_SUCCESS || r2 != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  return r1 == CUDA_SUCCESS && r2 == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_decode_fp8(const DecodeLaunch& d, cudaStream_t stream) {
+  const bool grouped = d.prefix_pages != nullptr;
+  CUtensorMap lat_map = {}, rope_map = {};
+  if (!d.e2m1) {
+    const cudaError_t e = encode_page_maps(d, &lat_map, &rope_map);
+    if (e != cudaSuccess) return e;
+  }
   Fp8Params p;
   p.q = d.q;
+  p.kv = d.kv;
   p.num_pages = d.num_pages;
   p.block_table = d.block_table;
   p.max_pages = d.max_pages;
@@ -1163,15 +1338,11 @@ cudaError_t launch_decode_fp8(const DecodeLaunch& d, cudaStream_t stream) {
                                        d.ws.q_op, d.ws.q_mul);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)d.G);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = grouped ? kSmemBytesGrouped : kSmemBytes;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return grouped ? cudaLaunchKernelEx(&cfg, decode_fp8_kernel<true>, p, lat_map, rope_map)
-                 : cudaLaunchKernelEx(&cfg, decode_fp8_kernel<false>, p, lat_map, rope_map);
+  if (d.e2m1)
+    return grouped ? launch_variant<true, true>(p, lat_map, rope_map, stream)
+                   : launch_variant<false, true>(p, lat_map, rope_map, stream);
+  return grouped ? launch_variant<true, false>(p, lat_map, rope_map, stream)
+                 : launch_variant<false, false>(p, lat_map, rope_map, stream);
 }
 
 }  // namespace mla

@@ -13,6 +13,10 @@
 // sign) tells on which side the real quotient lies, and q is moved one float32
 // ulp toward it before the hardware rounds to e4m3. Away from midpoints the
 // float32 rounding cannot change the e4m3 result.
+//
+// An e2m1 cache (kv_e2m1.cuh) stores two codes per byte and an exponent nibble per
+// 32 elements; its roundings are decided by comparisons with exact thresholds.
+#include "kv_e2m1.cuh"
 #include "mla_common.cuh"
 #include "mla_internal.h"
 
@@ -94,6 +98,75 @@ __global__ void kv_append_bf16_kernel(const __nv_bfloat16* __restrict__ latent,
       *reinterpret_cast<const uint4*>(src);
 }
 
+// One thread quantises one block of 32 elements (64 bytes of bf16 in, 16 bytes of codes
+// out); 18 threads cover a token. The threads of blocks 2i and 2i + 1 are neighbours in a
+// warp (18 is even) and share an exponent byte.
+__global__ void kv_append_e2m1_kernel(const __nv_bfloat16* __restrict__ latent,
+                                      const __nv_bfloat16* __restrict__ rope,
+                                      const int32_t* __restrict__ slots, int64_t num_tokens,
+                                      uint8_t* __restrict__ kv_pages, int64_t num_slots,
+                                      const E2m1Steps steps) {
+  griddep_launch_dependents();  // a following decode launch may start its set-up
+  const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t tok = gid / kE2m1Blocks;
+  const int b = (int)(gid - tok * kE2m1Blocks);
+  const int64_t slot = tok < num_tokens ? slots[tok] : -1;
+  const bool live = slot >= 0 && slot < num_slots;
+  uint32_t raw[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) raw[i] = 0u;
+  if (live) {
+    const __nv_bfloat16* src = b < kDLatent / kE2m1Block
+                                   ? latent + tok * kDLatent + b * kE2m1Block
+                                   : rope + tok * kDRope + (b - kDLatent / kE2m1Block) * kE2m1Block;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(src)[i];
+      raw[4 * i] = v.x;
+      raw[4 * i + 1] = v.y;
+      raw[4 * i + 2] = v.z;
+      raw[4 * i + 3] = v.w;
+    }
+  }
+  // largest magnitude by its bits (their order is the values'; a NaN comes out on top)
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    top = max(top, max(raw[i] & 0x7fffu, (raw[i] >> 16) & 0x7fffu));
+  const bool nan = top > 0x7f80u;
+  // smallest e with amax <= steps.top * 2^e: the difference of the two numbers' bits in
+  // units of a binade, rounded up; stored as n = e + 8 in 0..14
+  const int diff = (int)(top << 16) - __float_as_int(steps.top);
+  const int n = nan ? kE2m1NanExp : min(max(((diff + 0x7fffff) >> 23) + 8, 0), 14);
+  const float down = __int_as_float((127 + 8 - min(n, 14)) << 23);  // 2^-e
+  uint32_t words[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t bits = (i & 1) ? raw[4 * w + i / 2] >> 16 : raw[4 * w + i / 2] & 0xffffu;
+      const float y = __uint_as_float((bits & 0x7fffu) << 16) * down;
+      // three comparisons find the number of thresholds at or below y
+      const bool c4 = y >= steps.step[3];
+      const bool c2 = y >= (c4 ? steps.step[5] : steps.step[1]);
+      const float last = c4 ? (c2 ? steps.step[6] : steps.step[4])
+                            : (c2 ? steps.step[2] : steps.step[0]);
+      const uint32_t code = (c4 ? 4u : 0u) | (c2 ? 2u : 0u) | (y >= last ? 1u : 0u) |
+                            ((bits >> 12) & 8u);
+      word |= code << (4 * i);
+    }
+    words[w] = nan ? 0u : word;
+  }
+  const int other = __shfl_xor_sync(0xffffffffu, n, 1);
+  if (!live) return;
+  uint8_t* page = kv_pages + (slot / kPageSize) * kE2m1PageBytes;
+  const int t = (int)(slot % kPageSize);
+  *reinterpret_cast<uint4*>(page + e2m1_code_offset(b, t)) =
+      make_uint4(words[0], words[1], words[2], words[3]);
+  if ((b & 1) == 0) page[e2m1_exp_offset(b, t)] = (uint8_t)(n | (other << 4));
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
@@ -106,8 +179,10 @@ extern "C" mla_status mla_kv_append(const void* latent, const void* rope,
   using namespace mla;
   if (num_tokens < 0 || num_pages < 0) return MLA_ERR_INVALID_ARG;
   if (page_size != kPageSize) return MLA_ERR_UNSUPPORTED;
-  if (kv_dtype != MLA_KV_E4M3 && kv_dtype != MLA_KV_BF16) return MLA_ERR_INVALID_ARG;
+  if (kv_dtype != MLA_KV_E4M3 && kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_E2M1)
+    return MLA_ERR_INVALID_ARG;
   if (!(kv_scale > 0.0f) || !isfinite(kv_scale)) return MLA_ERR_INVALID_ARG;
+  if (kv_dtype == MLA_KV_E2M1 && !e2m1_scale_ok(kv_scale)) return MLA_ERR_INVALID_ARG;
   if (kv_dtype == MLA_KV_BF16 && kv_scale != 1.0f) return MLA_ERR_INVALID_ARG;
   if (num_tokens == 0) return MLA_OK;
   if (!latent || !rope || !slot_mapping || !kv_pages) return MLA_ERR_INVALID_ARG;
@@ -115,8 +190,9 @@ extern "C" mla_status mla_kv_append(const void* latent, const void* rope,
       (reinterpret_cast<uintptr_t>(slot_mapping) & 3u))
     return MLA_ERR_INVALID_ARG;
   const int64_t num_slots = num_pages * page_size;
-  const int64_t threads = num_tokens * (kDEntry / 8);
-  const int block = 288;  // 4 tokens per block
+  const int64_t threads =
+      num_tokens * (kv_dtype == MLA_KV_E2M1 ? kE2m1Blocks : kDEntry / 8);
+  const int block = 288;  // 4 tokens per block (16 of an e2m1 cache)
   const int64_t grid = (threads + block - 1) / block;
   if (grid > 0x7fffffffLL) return MLA_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -124,6 +200,11 @@ extern "C" mla_status mla_kv_append(const void* latent, const void* rope,
     kv_append_e4m3_kernel<<<(unsigned)grid, block, 0, s>>>(
         static_cast<const __nv_bfloat16*>(latent), static_cast<const __nv_bfloat16*>(rope),
         slot_mapping, num_tokens, static_cast<uint8_t*>(kv_pages), num_slots, kv_scale);
+  } else if (kv_dtype == MLA_KV_E2M1) {
+    kv_append_e2m1_kernel<<<(unsigned)grid, block, 0, s>>>(
+        static_cast<const __nv_bfloat16*>(latent), static_cast<const __nv_bfloat16*>(rope),
+        slot_mapping, num_tokens, static_cast<uint8_t*>(kv_pages), num_slots,
+        e2m1_steps(kv_scale));
   } else {
     kv_append_bf16_kernel<<<(unsigned)grid, block, 0, s>>>(
         static_cast<const __nv_bfloat16*>(latent), static_cast<const __nv_bfloat16*>(rope),

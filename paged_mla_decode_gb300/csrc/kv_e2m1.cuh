@@ -1,0 +1,109 @@
+// kv_e2m1.cuh -- the 4-bit cache format (MLA_KV_E2M1): page layout, the rounding
+// thresholds of the write side and the expansion tables of the read side.
+//
+// A page of 64 tokens is 19,008 contiguous bytes:
+//   codes [18 blocks][64 tokens][16 B]  block b of a token = its elements 32b .. 32b+31,
+//                                       two e2m1 codes per byte, the even element low
+//   exps  [9][64 tokens]                byte i: blocks 2i (low nibble) and 2i+1 (high)
+// value = e2m1(code) * 2^(n - 8) * kv_scale with n the block's nibble; n = 15: NaN.
+// Codes of one block lie beside each other for consecutive tokens, so that eight
+// threads with consecutive tokens read 128 contiguous bytes and write eight rows of a
+// swizzled tensor-core operand without bank conflicts (decode_fp8.cu).
+//
+// The exponents 2^-8 .. 2^6 are those for which every e2m1 value times the power is an
+// e4m3 number (0.5 * 2^-8 = 2^-9, the smallest; 6 * 2^6 = 384 <= 448): a 4-bit page
+// expands to e4m3 codes exactly, and the tensor-core path of the e4m3 cache applies.
+#pragma once
+
+#include <stdint.h>
+
+#include "mla_common.cuh"
+
+namespace mla {
+
+constexpr int kE2m1Block = MLA_E2M1_BLOCK;                  // 32 elements share an exponent
+constexpr int kE2m1Blocks = kDEntry / kE2m1Block;           // 18
+constexpr int kE2m1CodeBytes = kE2m1Blocks * kPageSize * 16;  // 18,432
+constexpr int kE2m1PageBytes = MLA_E2M1_PAGE_BYTES;         // 19,008
+constexpr int kE2m1NanExp = 15;
+static_assert(kE2m1CodeBytes + kE2m1Blocks / 2 * kPageSize == kE2m1PageBytes, "page layout");
+
+// Byte offset within a page of the 16 code bytes of (block, token), and of the exponent
+// byte that holds the block's nibble.
+__host__ __device__ constexpr int e2m1_code_offset(int block, int token) {
+  return (block * kPageSize + token) * 16;
+}
+__host__ __device__ constexpr int e2m1_exp_offset(int block, int token) {
+  return kE2m1CodeBytes + (block >> 1) * kPageSize + token;
+}
+
+// ---- write side ----
+// Thresholds as float32 for scale s, such that for every float32 y:
+//   y >= step[i]  <=>  |x| = y (already divided by 2^e) rounds above e2m1 value i, i.e.
+//                      y is beyond the midpoint of values i and i + 1 times s, or on it
+//                      when the even code is i + 1;
+//   amax <= top * 2^e  <=>  amax <= 7 * s * 2^e.
+// The products (27 significant bits at most) are formed exactly in double; the nearest
+// float32 on the right side of each decides every float32 y as the product would.
+// s must lie in [2^-100, 2^100], so that no threshold over- or underflows.
+struct E2m1Steps {
+  float step[7];
+  float top;
+};
+inline float e2m1_round_down(double d) {
+  const float f = (float)d;
+  return (double)f > d ? nextafterf(f, -INFINITY) : f;
+}
+inline float e2m1_round_up(double d) {
+  const float f = (float)d;
+  return (double)f < d ? nextafterf(f, INFINITY) : f;
+}
+inline E2m1Steps e2m1_steps(float s) {
+  const double mid[7] = {0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0};
+  E2m1Steps r;
+  for (int i = 0; i < 7; ++i) {
+    const double t = mid[i] * (double)s;
+    r.step[i] = (i & 1) ? e2m1_round_up(t) : nextafterf(e2m1_round_down(t), INFINITY);
+  }
+  r.top = e2m1_round_down(7.0 * (double)s);
+  return r;
+}
+inline bool e2m1_scale_ok(float s) { return s >= 0x1p-100f && s <= 0x1p100f; }
+
+// ---- read side ----
+// e4m3 codes of the eight magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 times 2^(n - 8), one byte
+// each, magnitude 0 in the lowest byte; 0x7f (NaN) throughout for n = 15.
+__host__ __device__ constexpr uint64_t e2m1_as_e4m3(int n) {
+  const int halves[8] = {0, 1, 2, 3, 4, 6, 8, 12};  // the magnitudes in units of 0.5
+  uint64_t row = 0;
+  for (int c = 0; c < 8; ++c) {
+    uint64_t code = 0;
+    const int v = halves[c];
+    if (n == kE2m1NanExp) {
+      code = 0x7f;
+    } else if (v > 0) {
+      int k = 0;
+      while ((v >> (k + 1)) > 0) ++k;     // v = (1 + m/2) * 2^k
+      const int m = v == (1 << k) ? 0 : 1;
+      const int e = k + n - 9;            // value = (1 + m/2) * 2^e
+      code = e >= -6 ? (uint64_t)(((e + 7) << 3) | (m << 2)) : (uint64_t)(v << n);
+    }
+    row |= code << (8 * c);
+  }
+  return row;
+}
+
+// Eight e2m1 codes (nibble i = element i) -> eight e4m3 codes, given the block's table
+// row (lo: magnitudes 0..3, hi: 4..7). A byte permute looks up four magnitudes at once;
+// a second one, whose selectors still carry the sign bit, replicates the top bit of a
+// constant 0x80 where the sign is set: 0xff against 0x80, whose lowest bit is the sign.
+__device__ __forceinline__ uint2 e2m1x8_to_e4m3(uint32_t w, uint32_t lo, uint32_t hi) {
+  const uint32_t mag = w & 0x77777777u;
+  const uint32_t a0 = __byte_perm(lo, hi, mag), a1 = __byte_perm(lo, hi, mag >> 16);
+  uint32_t s0, s1;
+  asm("prmt.b32 %0, %1, %1, %2;\n" : "=r"(s0) : "r"(0x80808080u), "r"(w));
+  asm("prmt.b32 %0, %1, %1, %2;\n" : "=r"(s1) : "r"(0x80808080u), "r"(w >> 16));
+  return make_uint2(a0 | ((s0 << 7) & 0x80808080u), a1 | ((s1 << 7) & 0x80808080u));
+}
+
+}  // namespace mla

@@ -33,7 +33,8 @@ struct DecodeLaunch {
   int max_pages;
   const int32_t* seq_lens;
   int batch, nq, heads;
-  bool bf16;         // cache holds bf16 (else e4m3 codes)
+  bool bf16;         // cache holds bf16 (else e4m3 codes, or e2m1 pages)
+  bool e2m1;         // cache holds e2m1 pages
   float score_mul;   // sm_scale * log2(e) * kv_scale
   float kv_scale;
   int G;             // CTAs launched
@@ -48,7 +49,7 @@ struct DecodeLaunch {
 cudaError_t launch_decode_tensor_core(const DecodeLaunch& d, cudaStream_t stream);
 
 // Split-KV decode with the e4m3 cache bytes as tensor-core operands
-// (decode_fp8.cu); e4m3 caches only, heads <= 64, num_pages * 64 < 2^31.
+// (decode_fp8.cu); e4m3 and e2m1 caches, heads <= 64, num_pages * 64 < 2^31.
 // Launches the query split (one pass per row into ws.q_op / ws.q_mul), then the
 // decode kernel, which reads it.
 cudaError_t launch_decode_fp8(const DecodeLaunch& d, cudaStream_t stream);
