@@ -25,7 +25,11 @@
 // A 4-bit cache (kv_e2m1.cuh) takes the same path (kE2m1): its pages land in a second,
 // smaller ring as stored, four expander warps rewrite each as the swizzled e4m3 page
 // that the contractions read (a table lookup, exact), and everything after that is
-// the e4m3 kernel. It trades one ring slot for the raw pages (kRing 4 + 2 raw).
+// the e4m3 kernel. It trades one ring slot for the raw pages (kRing 4 + 2 raw). What
+// bounds it is shared-memory bandwidth: a page's MMAs read 140 KB of operands (V twice,
+// for P's two terms), the P buffers and page copies move 35 KB, the expansion reads and
+// writes another 55 KB: 1,800 cycles at 128 B a cycle, of the 2,330 a page takes
+// (31 requests of 60k-140k tokens, 64 heads: 488 us, 307 pages a CTA).
 //
 // Warp roles (416 threads; 544 with the expanders):
 //   warps 0-7  q loading, softmax and epilogue. Row t of A and S is (head
@@ -41,9 +45,7 @@
 //              (128-byte swizzled latent blocks, 64-byte swizzled rope block).
 //   warps 9-10 issue QK of even / odd pages (lane 0); warp 9 allocates TMEM.
 //   warps 11-12 issue PV of even / odd pages (lane 0).
-//   warps 13-16 (4-bit cache only) expand raw pages into the ring. 1,152 blocks of 32
-//              elements a page, 9 a thread; a thread keeps one token, so its swizzle
-//              is a constant, and eight threads write eight rows without conflicts.
+//   warps 13-16 (4-bit cache only) expand raw pages into the ring, one per scheduler.
 // A thread that issues MMAs stalls for a while after each batch (until the
 // tensor pipe's queue has room), so two issuers per contraction keep the pipe
 // fed: one issues while the other waits.
@@ -122,7 +124,7 @@ constexpr int kTableAhead = 32;  // pages described (block-table read started) b
 // Shared memory map (offsets from a 1024-aligned base) and barriers.
 template <bool kE2m1>
 struct Map {
-  static constexpr int kThreads = 32 * (kExpWarp0 + (kE2m1 ? kExpWarps : 0));  // 416, 544
+  static constexpr int kThreads = 32 * (kE2m1 ? kExpWarp0 + kExpWarps : kSmWarps + 5);  // 544, 416
   static constexpr int kRing = kE2m1 ? 4 : 5;          // e4m3 pages in flight
   static constexpr int kRawRing = kE2m1 ? 2 : 0;       // 4-bit pages in flight
   static constexpr int kOffPages = 0;
@@ -339,54 +341,81 @@ __device__ const uint64_t kE2m1Lut[16] = {
     e2m1_as_e4m3(8),  e2m1_as_e4m3(9),  e2m1_as_e4m3(10), e2m1_as_e4m3(11),
     e2m1_as_e4m3(12), e2m1_as_e4m3(13), e2m1_as_e4m3(14), e2m1_as_e4m3(15)};
 
-// One expander thread's share of a page: token t = x % 64, and of each pair of blocks
-// (2i, 2i + 1) the one of its half x / 64, whose nibble lies in byte i of the token's
-// exponents. Three blocks at a time, so that their loads overlap.
-__device__ __forceinline__ void expand_page(uint32_t raw, uint32_t page, uint32_t lut, int x) {
-  const int t = x & 63, half = x >> 6;
-  const uint32_t row = page + t * 128, sw = (uint32_t)(t & 7);
-  const uint32_t rope = page + kRopeOff + t * 64, sw_rope = (uint32_t)((t >> 1) & 3);
+// One expander warp's share of a page: of every 128-dim block the quarter g (blocks g,
+// 4 + g, 8 + g, 12 + g), two tokens (lane, lane + 32) a thread, and a quarter of the two
+// rope blocks. Alone on an SM it is bound by the ALU pipe (a warp instruction per two
+// cycles; 32 of the 50 that 32 elements take convert), so there is one expander per
+// scheduler, the exponents are read once, the next blocks' loads and table rows are in
+// flight while a block is written, and a thread's place in a row is a constant: 974
+// cycles a page. Only two blocks are unrolled: the roles' loops share the instruction
+// cache (all nine unrolled: 510 us on the 31 requests above). Three warps with 128
+// registers a thread instead of four with 96 took 493 us, five warpgroups with registers
+// moved to the softmax (setmaxnreg) 515.
+struct ExpandUnit {
+  uint4 codes;
+  uint2 row;  // of the expansion table
+};
+__device__ __forceinline__ void expand_load(ExpandUnit& u, uint32_t code_at, uint32_t lut,
+                                            uint32_t n) {
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(u.codes.x), "=r"(u.codes.y), "=r"(u.codes.z), "=r"(u.codes.w)
+               : "r"(code_at));
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n"
+               : "=r"(u.row.x), "=r"(u.row.y)
+               : "r"(lut + 8 * (n & 15u)));
+}
+// Chunks c and c + 1 of a row (c even): the swizzle makes them each other's neighbour.
+__device__ __forceinline__ void expand_write(const ExpandUnit& u, uint32_t at) {
+  const uint2 c0 = e2m1x8_to_e4m3(u.codes.x, u.row.x, u.row.y);
+  const uint2 c1 = e2m1x8_to_e4m3(u.codes.y, u.row.x, u.row.y);
+  const uint2 c2 = e2m1x8_to_e4m3(u.codes.z, u.row.x, u.row.y);
+  const uint2 c3 = e2m1x8_to_e4m3(u.codes.w, u.row.x, u.row.y);
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(c0.x), "r"(c0.y),
+               "r"(c1.x), "r"(c1.y) : "memory");
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(at ^ 16u), "r"(c2.x), "r"(c2.y),
+               "r"(c3.x), "r"(c3.y) : "memory");
+}
+__device__ __forceinline__ void expand_page(uint32_t raw, uint32_t page, uint32_t lut, int g,
+                                            int lane) {
+  const int rt = lane + 32 * (g & 1);  // rope: block 16 + g / 2 of token rt
+  uint32_t exps[2], rope_exps;         // four bytes each, this quarter's nibble the lowest
 #pragma unroll
-  for (int i0 = 0; i0 < kE2m1Blocks / 2; i0 += 3) {
-    uint4 w[3];
-    uint2 tab[3];
+  for (int k = 0; k < 2; ++k) {
+    uint32_t b[4];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const int i = i0 + k;
-      uint32_t e;
-      asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(e) : "r"(raw + e2m1_exp_offset(2 * i, t)));
-      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                   : "=r"(w[k].x), "=r"(w[k].y), "=r"(w[k].z), "=r"(w[k].w)
-                   : "r"(raw + e2m1_code_offset(2 * i, t) + half * e2m1_code_offset(1, 0)));
-      asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n"
-                   : "=r"(tab[k].x), "=r"(tab[k].y)
-                   : "r"(lut + 8 * (half ? e >> 4 : e & 15u)));
-    }
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const int i = i0 + k;
-      const uint2 c0 = e2m1x8_to_e4m3(w[k].x, tab[k].x, tab[k].y);
-      const uint2 c1 = e2m1x8_to_e4m3(w[k].y, tab[k].x, tab[k].y);
-      const uint2 c2 = e2m1x8_to_e4m3(w[k].z, tab[k].x, tab[k].y);
-      const uint2 c3 = e2m1x8_to_e4m3(w[k].w, tab[k].x, tab[k].y);
-      // block b = 2i + half: chunks 2(b % 4), 2(b % 4) + 1 of the token's row of latent
-      // block b / 4; the last two blocks are the rope row's four chunks
-      uint32_t d0, d1;
-      if (i < 8) {
-        const uint32_t c = 4u * (i & 1) + 2u * half;
-        d0 = row + (i >> 1) * kLatBlock + ((c ^ sw) << 4);
-        d1 = row + (i >> 1) * kLatBlock + (((c + 1) ^ sw) << 4);
-      } else {
-        const uint32_t c = 2u * half;
-        d0 = rope + ((c ^ sw_rope) << 4);
-        d1 = rope + (((c + 1) ^ sw_rope) << 4);
-      }
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(d0), "r"(c0.x), "r"(c0.y),
-                   "r"(c1.x), "r"(c1.y) : "memory");
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(d1), "r"(c2.x), "r"(c2.y),
-                   "r"(c3.x), "r"(c3.y) : "memory");
-    }
+    for (int i = 0; i < 4; ++i)
+      asm volatile("ld.shared.u8 %0, [%1];\n"
+                   : "=r"(b[i])
+                   : "r"(raw + e2m1_exp_offset(4 * i + g, lane + 32 * k)));
+    exps[k] = (b[0] + b[1] * 0x100u + b[2] * 0x10000u + b[3] * 0x1000000u) >> (4 * (g & 1));
   }
+  asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(rope_exps) : "r"(raw + e2m1_exp_offset(16, rt)));
+  uint32_t code_at = raw + e2m1_code_offset(g, lane);
+  uint32_t at = page + lane * 128 + (((uint32_t)g << 5) ^ ((uint32_t)(lane & 7) << 4));
+  auto load = [&](ExpandUnit (&u)[2]) {
+    expand_load(u[0], code_at, lut, exps[0]);
+    expand_load(u[1], code_at + e2m1_code_offset(0, 32), lut, exps[1]);
+    exps[0] >>= 8;
+    exps[1] >>= 8;
+    code_at += e2m1_code_offset(4, 0);
+  };
+  auto write = [&](const ExpandUnit (&u)[2]) {
+    expand_write(u[0], at);
+    expand_write(u[1], at + 32 * 128);  // 32 rows on: the same swizzle
+    at += kLatBlock;
+  };
+  ExpandUnit even[2], odd[2];
+  load(even);
+#pragma unroll 1
+  for (int i = 0; i < 4; i += 2) {
+    load(odd);
+    write(even);
+    if (i == 0) load(even);
+    else expand_load(even[0], raw + e2m1_code_offset(16 + (g >> 1), rt), lut, rope_exps >> (4 * (g >> 1)));
+    write(odd);
+  }
+  expand_write(even[0], page + kRopeOff + rt * 64 +
+                            (((uint32_t)(g >> 1) << 5) ^ ((uint32_t)((rt >> 1) & 3) << 4)));
 }
 
 // kGrouped: the grouped decode (GroupPlan): this CTA's shared-prefix range, then
@@ -632,7 +661,6 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
     } else if (kE2m1 && warp >= kExpWarp0) {
       // =================== expanders of a 4-bit cache (4 warps) ===================
       if constexpr (kE2m1) {
-        const int x = tid - 32 * kExpWarp0;
         bool ok = true;
         for (int64_t j = 0; j < npages; ++j) {
           const int rs = (int)(j % M::kRawRing), slot = (int)(j % kRing);
@@ -646,7 +674,8 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
           // zeroed by the softmax warps
           if (desc[j % kDescRing].flags & kDescPageOk)
             expand_page(sbase + M::kOffRaw + rs * kE2m1PageBytes,
-                        sbase + kOffPages + slot * kPageBytes, sbase + M::kOffLut, x);
+                        sbase + kOffPages + slot * kPageBytes, sbase + M::kOffLut,
+                        warp - kExpWarp0, lane);
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {

@@ -93,17 +93,29 @@ __host__ __device__ constexpr uint64_t e2m1_as_e4m3(int n) {
   return row;
 }
 
+// For n = 3 .. 14 every magnitude but 0 is a normal e4m3 number times 2^(n - 8), and its
+// code is linear in n: the table row (bytes 0, 8n - 16, 8n - 8, 8n - 4 | 8n, 8n + 4,
+// 8n + 8, 8n + 12) costs two multiply-adds instead of a shared-memory read.
+__device__ __forceinline__ void e2m1_linear_row(uint32_t n, uint32_t& lo, uint32_t& hi) {
+  lo = n * 0x08080800u - 0x04081000u;
+  hi = n * 0x08080808u + 0x0c080400u;
+}
+// Whether the low nibbles of all four bytes lie in 3 .. 14: n + 13 carries into bit 4
+// from n = 3 on, n + 1 at n = 15 only.
+__device__ __forceinline__ bool e2m1_all_linear(uint32_t nibbles) {
+  const uint32_t m = nibbles & 0x0f0f0f0fu;
+  return ((m + 0x0d0d0d0du) & ~(m + 0x01010101u) & 0x10101010u) == 0x10101010u;
+}
+
 // Eight e2m1 codes (nibble i = element i) -> eight e4m3 codes, given the block's table
-// row (lo: magnitudes 0..3, hi: 4..7). A byte permute looks up four magnitudes at once;
-// a second one, whose selectors still carry the sign bit, replicates the top bit of a
-// constant 0x80 where the sign is set: 0xff against 0x80, whose lowest bit is the sign.
+// row (lo: magnitudes 0..3, hi: 4..7): nine instructions. A byte permute looks up four
+// magnitudes at once; the signs are the top bits of w's bytes (odd elements) and of
+// w << 4 (even elements), which another permute puts in element order.
 __device__ __forceinline__ uint2 e2m1x8_to_e4m3(uint32_t w, uint32_t lo, uint32_t hi) {
-  const uint32_t mag = w & 0x77777777u;
-  const uint32_t a0 = __byte_perm(lo, hi, mag), a1 = __byte_perm(lo, hi, mag >> 16);
-  uint32_t s0, s1;
-  asm("prmt.b32 %0, %1, %1, %2;\n" : "=r"(s0) : "r"(0x80808080u), "r"(w));
-  asm("prmt.b32 %0, %1, %1, %2;\n" : "=r"(s1) : "r"(0x80808080u), "r"(w >> 16));
-  return make_uint2(a0 | ((s0 << 7) & 0x80808080u), a1 | ((s1 << 7) & 0x80808080u));
+  const uint32_t mag = w & 0x77777777u, even = w << 4;
+  const uint32_t s0 = __byte_perm(even, w, 0x5140), s1 = __byte_perm(even, w, 0x7362);
+  return make_uint2(__byte_perm(lo, hi, mag) | (s0 & 0x80808080u),
+                    __byte_perm(lo, hi, mag >> 16) | (s1 & 0x80808080u));
 }
 
 }  // namespace mla
