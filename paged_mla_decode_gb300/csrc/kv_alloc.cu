@@ -10,9 +10,14 @@
 //   need_b  = max(0, ceil((L_b + n_b) / 64) - held_b)     (0 for a refused request)
 //   first_b = running sum of need: request b takes free_pages[count - 1 - first_b - k]
 //
-// Two running sums over the batch and 4 bytes per new token: latency bound. One block
-// scans the requests in chunks of its size; each chunk's pages and slots are then spread
-// over the threads, which find their request by bisection in shared memory.
+// Two running sums over the batch and 4 bytes written per new token: latency bound for a
+// step's few tokens, then bound by the slots' stores. Every block scans the requests, in
+// chunks of its size, and fills its own run of rows (a thread finds its request by
+// bisection in shared memory, once per 128 rows); the row of a new page's first token
+// also writes the page's table entry and tag. The page ids of new pages come from the
+// free list itself, so that no row waits for another's table entry.
+#include <algorithm>
+
 #include "mla_common.cuh"
 #include "mla_internal.h"
 
@@ -21,6 +26,8 @@ namespace {
 
 constexpr int kAllocThreads = 1024;
 constexpr int kAllocWarps = kAllocThreads / 32;
+constexpr int kWarpRows = 128;         // rows a warp fills per bisection
+constexpr int64_t kBlockRows = 4096;   // rows that are worth a block of their own
 
 struct AllocParams {
   const int32_t* seq_lens;
@@ -46,9 +53,9 @@ struct AllocParams {
 
 struct AllocShared {
   int64_t warp_sum[kAllocWarps];
-  int64_t row_end[kAllocThreads];   // rows of the chunk's requests, ends
-  int64_t page_end[kAllocThreads];  // their pages, ends
-  int32_t len[kAllocThreads];       // cached tokens; -1: refused
+  int64_t row_end[kAllocThreads];     // rows of the chunk's requests, ends
+  int64_t first_page[kAllocThreads];  // pages taken before each
+  int32_t len[kAllocThreads];         // cached tokens; -1: refused
   int32_t held[kAllocThreads];
 };
 
@@ -93,9 +100,16 @@ __device__ __forceinline__ int64_t pages_for(int64_t tokens) {
   return (tokens + kPageSize - 1) / kPageSize;
 }
 
-__global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(const AllocParams p) {
+// kFill: rows [blockIdx.x * rows_per, + rows_per) of the slot map, with the new pages that
+// begin there. kCommit: block 0 writes the per-request outputs, which may be the inputs:
+// then no other block may still read them (one block in all, or a launch of its own).
+template <bool kFill, bool kCommit>
+__global__ void __launch_bounds__(kAllocThreads)
+    kv_alloc_kernel(const AllocParams p, const int64_t rows_per) {
   __shared__ AllocShared sm;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool commit = kCommit && blockIdx.x == 0;
+  const int64_t lo = blockIdx.x * rows_per, hi = min(lo + rows_per, p.num_slots);
   const int64_t count = min(max((int64_t)p.free_count[0], (int64_t)0), p.free_capacity);
   int64_t row0 = 0, page0 = 0, taken = 0;  // rows, pages asked for and pages taken so far
   for (int b0 = 0; b0 < p.batch; b0 += kAllocThreads) {
@@ -114,63 +128,81 @@ __global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(const AllocPara
     const int64_t need = live && st == 0 ? max(pages_for(L + n) - held, (int64_t)0) : 0;
     const int64_t page_end = page0 + block_scan(need, sm.warp_sum, &pages);
     if (need > 0 && page_end > count) st = MLA_KV_ALLOC_NO_PAGES;
-    const bool grown = need > 0 && st == 0;
-    sm.row_end[tid] = row_end;
-    sm.page_end[tid] = page_end;
-    sm.len[tid] = st == 0 ? L : -1;
-    sm.held[tid] = held;
-    if (live) {
-      p.seq_lens_out[b] = st == 0 ? (int32_t)(L + n) : -1;
-      p.held_out[b] = held + (grown ? (int32_t)need : 0);
-      p.status[b] = st;
-      p.cu[b + 1] = (int32_t)min(row_end, (int64_t)0x7fffffff);
+    if constexpr (kFill) {
+      sm.row_end[tid] = row_end;
+      sm.first_page[tid] = page_end - need;
+      sm.len[tid] = st == 0 ? L : -1;
+      sm.held[tid] = held;
     }
-    // the requests that got pages are a prefix of those that asked: the page count only grows
-    int64_t got = grown ? page_end : 0;
+    if (commit) {
+      const bool grown = need > 0 && st == 0;
+      if (live) {
+        p.seq_lens_out[b] = st == 0 ? (int32_t)(L + n) : -1;
+        p.held_out[b] = held + (grown ? (int32_t)need : 0);
+        p.status[b] = st;
+        p.cu[b + 1] = (int32_t)min(row_end, (int64_t)0x7fffffff);
+      }
+      // the requests that got pages come before those that got none: the sum only grows
+      int64_t got = grown ? page_end : 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) got = max(got, __shfl_xor_sync(0xffffffffu, got, o));
-    if ((tid & 31) == 0) sm.warp_sum[tid >> 5] = got;
-    __syncthreads();
-    for (int w = 0; w < kAllocWarps; ++w) taken = max(taken, sm.warp_sum[w]);
-    const int nb = min(kAllocThreads, p.batch - b0);
-    // pages: from page0 up to what was taken
-    for (int64_t x = page0 + tid; x < min(page0 + pages, taken); x += kAllocThreads) {
-      const int i = first_after(sm.page_end, nb, x);
-      const int64_t k = x - (i > 0 ? sm.page_end[i - 1] : page0);
-      const int64_t at = (int64_t)(b0 + i) * p.max_pages + sm.held[i] + k;
-      const int32_t page = p.free_pages[count - 1 - x];
-      p.block_table[at] = page;
-      if (p.page_tags != nullptr && page >= 0 && page < p.num_pages) {
-        const uint32_t tag = p.page_tags[page] + 1;
-        p.page_tags[page] = tag;
-        p.expected_tags[at] = tag;
-      }
+      for (int o = 16; o > 0; o >>= 1) got = max(got, __shfl_xor_sync(0xffffffffu, got, o));
+      if (lane == 0) sm.warp_sum[warp] = got;
     }
-    // slots: pages that the request held already come from its row, the new ones from the
-    // free list, so that no thread waits for another's table entry
-    for (int64_t x = row0 + tid; x < min(row0 + rows, p.num_slots); x += kAllocThreads) {
-      const int i = first_after(sm.row_end, nb, x);
-      int64_t slot = -1;
-      if (sm.len[i] >= 0) {
-        const int64_t pos = sm.len[i] + x - (i > 0 ? sm.row_end[i - 1] : row0);
-        const int64_t j = pos / kPageSize;
-        const int32_t page =
-            j < sm.held[i]
-                ? p.block_table[(int64_t)(b0 + i) * p.max_pages + j]
-                : p.free_pages[count - 1 - (i > 0 ? sm.page_end[i - 1] : page0) - (j - sm.held[i])];
-        if (page >= 0 && page < p.num_pages) slot = (int64_t)page * kPageSize + pos % kPageSize;
+    __syncthreads();
+    if (commit)
+      for (int w = 0; w < kAllocWarps; ++w) taken = max(taken, sm.warp_sum[w]);
+    if constexpr (kFill) {
+      const int nb = min(kAllocThreads, p.batch - b0);
+      const int64_t x_end = min(row0 + rows, hi);
+      // (first row of this block's run in the chunk: a multiple of 128 rows into the run)
+      for (int64_t x0 = lo + (int64_t)warp * kWarpRows; x0 < x_end; x0 += kAllocWarps * kWarpRows) {
+        if (x0 + kWarpRows <= row0) continue;
+        int i = first_after(sm.row_end, nb, max(x0, row0));
+#pragma unroll
+        for (int k = 0; k < kWarpRows; k += 32) {
+          const int64_t x = x0 + k + lane;
+          if (x < row0 || x >= x_end) continue;
+          while (sm.row_end[i] <= x) ++i;
+          int64_t slot = -1;
+          const int len = sm.len[i], held_i = sm.held[i];
+          if (len >= 0) {
+            const int64_t pos = len + x - (i > 0 ? sm.row_end[i - 1] : row0);
+            const int j = (int)(pos / kPageSize), off = (int)(pos % kPageSize);
+            const int64_t at = (int64_t)(b0 + i) * p.max_pages + j;
+            const bool fresh = j >= held_i;
+            const int32_t page =
+                fresh ? p.free_pages[count - 1 - sm.first_page[i] - (j - held_i)] : p.block_table[at];
+            const bool in_cache = page >= 0 && page < p.num_pages;
+            if (in_cache) slot = (int64_t)page * kPageSize + off;
+            if (fresh && off == 0) {  // a page held before covers every cached token
+              p.block_table[at] = page;
+              if (p.page_tags != nullptr && in_cache) {
+                const uint32_t tag = p.page_tags[page] + 1;
+                p.page_tags[page] = tag;
+                p.expected_tags[at] = tag;
+              }
+            }
+          }
+          p.slots[x] = (int32_t)slot;
+        }
       }
-      p.slots[x] = (int32_t)slot;
     }
     row0 += rows;
     page0 += pages;
     __syncthreads();
   }
-  for (int64_t x = row0 + tid; x < p.num_slots; x += kAllocThreads) p.slots[x] = -1;
-  if (tid == 0) {
+  if constexpr (kFill)
+    for (int64_t x = max(row0, lo) + tid; x < hi; x += kAllocThreads) p.slots[x] = -1;
+  if (commit && tid == 0) {
     p.cu[0] = 0;
     p.free_count_out[0] = (int32_t)(count - taken);
   }
+}
+
+// Whether n int32 at a share memory with m int32 at b.
+bool overlap(const void* a, int64_t n, const void* b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4 * (uintptr_t)m && y < x + 4 * (uintptr_t)n;
 }
 
 }  // namespace
@@ -208,6 +240,26 @@ extern "C" mla_status mla_kv_alloc(const int32_t* seq_lens, const int32_t* new_t
                       free_count, free_capacity, num_pages,    block_table,  max_pages,
                       page_tags, expected_tags, seq_lens_out,  pages_held_out, free_count_out,
                       cu_tokens, slot_mapping,  num_slots,     request_status};
-  kv_alloc_kernel<<<1, kAllocThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int sms = device_sm_count();
+  if (sms <= 0) return MLA_ERR_CUDA;
+  int64_t blocks = std::min<int64_t>((num_slots + kBlockRows - 1) / kBlockRows, sms);
+  blocks = std::max<int64_t>(blocks, 1);
+  const int64_t rows_per =
+      ((num_slots + blocks - 1) / blocks + kWarpRows - 1) / kWarpRows * kWarpRows;
+  // Several blocks read the per-request inputs while block 0 writes its outputs: where
+  // one of those shares memory with an input, they get a launch of their own.
+  const void* ins[4] = {seq_lens, new_tokens, pages_held, free_count};
+  const void* outs[5] = {seq_lens_out, pages_held_out, free_count_out, cu_tokens, request_status};
+  bool apart = true;
+  for (int i = 0; i < 4; ++i)
+    for (int o = 0; o < 5; ++o)
+      apart = apart && !overlap(ins[i], i == 3 ? 1 : batch, outs[o], o == 2 ? 1 : batch + (o == 3));
+  if (blocks == 1 || apart) {
+    kv_alloc_kernel<true, true><<<(unsigned)blocks, kAllocThreads, 0, s>>>(p, rows_per);
+  } else {
+    kv_alloc_kernel<true, false><<<(unsigned)blocks, kAllocThreads, 0, s>>>(p, rows_per);
+    kv_alloc_kernel<false, true><<<1, kAllocThreads, 0, s>>>(p, rows_per);
+  }
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
