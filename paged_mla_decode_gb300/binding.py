@@ -62,9 +62,8 @@ class MlaError(RuntimeError):
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libmla.so once and declare the argument types of every entry point."""
     global _lib
-    if _lib is not None:
-        return _lib
-    _lib = open_library(path)
+    if _lib is None:
+        _lib = open_library(path)
     return _lib
 
 
@@ -133,13 +132,17 @@ def status_string(status: int) -> str:
 
 
 def _ptr(t) -> int:
-    return 0 if t is None else int(t.data_ptr())
+    return 0 if t is None else t.data_ptr()
 
 
 def _stream(stream) -> int:
+    """The stream's handle; the current stream of the current device by default.
+
+    (Read without a Stream object, which costs as much host time as a kernel launch.)
+    """
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return int(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(status: int, where: str):
@@ -291,11 +294,21 @@ def mla_kv_check(page_tags: torch.Tensor, block_table: torch.Tensor,
     _check(st, "mla_kv_check")
 
 
-def _int32(device: torch.device, *tensors) -> None:
-    """Each tensor is a contiguous int32 (or, for tags and status words, uint32) one on `device`."""
+_I32, _U32 = torch.int32, torch.uint32
+
+
+def _int32(device: int, *tensors) -> None:
+    """Each tensor is a contiguous int32 (for tags and status words also uint32) one on `device`."""
     for t in tensors:
-        assert t.dtype == torch.int32 or t.dtype == torch.uint32
-        assert t.is_contiguous() and t.device == device
+        assert t.dtype is _I32 or t.dtype is _U32
+        assert t.is_contiguous() and t.get_device() == device
+
+
+def _device_of(t: torch.Tensor) -> int:
+    """The tensor's CUDA device, which must be the current one (the library launches there)."""
+    device = t.get_device()
+    assert t.is_cuda and device == torch.cuda.current_device()
+    return device
 
 
 def mla_kv_gather(kv_pages: torch.Tensor, kv_scale: float, block_table: torch.Tensor,
@@ -309,8 +322,8 @@ def mla_kv_gather(kv_pages: torch.Tensor, kv_scale: float, block_table: torch.Te
     ``cu_tokens[batch]`` on are left as they were. ``kv_pages`` as in
     :func:`kv_dtype_code`.
     """
-    dtype, device = kv_dtype_code(kv_pages), kv_pages.device
-    assert kv_pages.is_cuda and block_table.dim() == 2
+    dtype, device = kv_dtype_code(kv_pages), _device_of(kv_pages)
+    assert block_table.dim() == 2
     batch, max_pages = block_table.shape
     rows = latent.shape[0]
     _int32(device, block_table, cu_tokens)
@@ -321,11 +334,12 @@ def mla_kv_gather(kv_pages: torch.Tensor, kv_scale: float, block_table: torch.Te
     assert latent.dtype == torch.bfloat16 and rope.dtype == torch.bfloat16
     assert latent.shape == (rows, 512) and rope.shape == (rows, 64)
     assert latent.is_contiguous() and rope.is_contiguous()
-    assert latent.device == device and rope.device == device
-    st = load_library().mla_kv_gather(_ptr(kv_pages), kv_pages.shape[0], _page_size(kv_pages),
-                                      dtype, kv_scale, _ptr(block_table), max_pages, _ptr(starts),
-                                      _ptr(cu_tokens), batch, rows, _ptr(latent), _ptr(rope),
-                                      _stream(stream))
+    assert latent.get_device() == device and rope.get_device() == device
+    st = load_library().mla_kv_gather(kv_pages.data_ptr(), kv_pages.shape[0],
+                                      _page_size(kv_pages), dtype, kv_scale,
+                                      block_table.data_ptr(), max_pages, _ptr(starts),
+                                      cu_tokens.data_ptr(), batch, rows, latent.data_ptr(),
+                                      rope.data_ptr(), _stream(stream))
     _check(st, "mla_kv_gather")
 
 
@@ -347,8 +361,8 @@ def mla_kv_alloc(seq_lens: torch.Tensor, new_tokens: torch.Tensor, pages_held: t
     input) and ``request_status`` (MLA_KV_ALLOC_* bits; a refused request gets
     length -1 and slots -1).
     """
-    device = block_table.device
-    assert block_table.is_cuda and block_table.dim() == 2
+    device = _device_of(block_table)
+    assert block_table.dim() == 2
     batch, max_pages = block_table.shape
     _int32(device, seq_lens, new_tokens, pages_held, free_pages, free_count, block_table,
            seq_lens_out, pages_held_out, free_count_out, cu_tokens, slot_mapping, request_status)
@@ -362,11 +376,12 @@ def mla_kv_alloc(seq_lens: torch.Tensor, new_tokens: torch.Tensor, pages_held: t
         _int32(device, page_tags, expected_tags)
         assert page_tags.numel() == num_pages and expected_tags.shape == block_table.shape
     st = load_library().mla_kv_alloc(
-        _ptr(seq_lens), _ptr(new_tokens), batch, 64, _ptr(pages_held), _ptr(free_pages),
-        _ptr(free_count), free_pages.numel(), num_pages, _ptr(block_table), max_pages,
-        _ptr(page_tags), _ptr(expected_tags), _ptr(seq_lens_out), _ptr(pages_held_out),
-        _ptr(free_count_out), _ptr(cu_tokens), _ptr(slot_mapping), slot_mapping.numel(),
-        _ptr(request_status), _stream(stream))
+        seq_lens.data_ptr(), new_tokens.data_ptr(), batch, 64, pages_held.data_ptr(),
+        free_pages.data_ptr(), free_count.data_ptr(), free_pages.numel(), num_pages,
+        block_table.data_ptr(), max_pages, _ptr(page_tags), _ptr(expected_tags),
+        seq_lens_out.data_ptr(), pages_held_out.data_ptr(), free_count_out.data_ptr(),
+        cu_tokens.data_ptr(), slot_mapping.data_ptr(), slot_mapping.numel(),
+        request_status.data_ptr(), _stream(stream))
     _check(st, "mla_kv_alloc")
 
 
@@ -396,8 +411,8 @@ def mla_verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | No
     ``num_accepted [batch]`` and, given ``seq_lens``, ``seq_lens_out``: the
     lengths without the rejected drafts (may be ``seq_lens`` itself).
     """
-    assert target_probs.is_cuda and target_probs.dim() == 3
-    device = target_probs.device
+    assert target_probs.dim() == 3
+    device = _device_of(target_probs)
     batch, rows, vocab = target_probs.shape
     drafts = rows - 1
     assert target_probs.dtype in (torch.float32, torch.bfloat16)
@@ -405,13 +420,14 @@ def mla_verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | No
     target_stride = _row_stride(target_probs) if batch > 0 else vocab
     draft_stride = vocab
     if draft_probs is not None:
-        assert draft_probs.dtype == target_probs.dtype and draft_probs.device == device
+        assert draft_probs.dtype == target_probs.dtype
+        assert draft_probs.get_device() == device
         assert draft_probs.shape == (batch, drafts, vocab)
         if batch > 0 and drafts > 0:
             draft_stride = _row_stride(draft_probs)
     assert draft_tokens.shape == (batch, drafts) and out_tokens.shape == (batch, rows)
     assert uniforms.dtype == torch.float32 and uniforms.shape == (batch, rows)
-    assert uniforms.is_contiguous() and uniforms.device == device
+    assert uniforms.is_contiguous() and uniforms.get_device() == device
     assert num_accepted.numel() == batch
     _int32(device, draft_tokens, out_tokens, num_accepted)
     assert seq_lens_out is None or seq_lens is not None
@@ -420,9 +436,10 @@ def mla_verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | No
             _int32(device, t)
             assert t.numel() == batch
     st = load_library().mla_verify_drafts(
-        _ptr(target_probs), target_stride, _ptr(draft_probs), draft_stride, dtype,
-        _ptr(draft_tokens), _ptr(uniforms), _ptr(num_drafts), _ptr(seq_lens), batch, drafts, vocab,
-        _ptr(out_tokens), _ptr(num_accepted), _ptr(seq_lens_out), _stream(stream))
+        target_probs.data_ptr(), target_stride, _ptr(draft_probs), draft_stride, dtype,
+        draft_tokens.data_ptr(), uniforms.data_ptr(), _ptr(num_drafts), _ptr(seq_lens), batch,
+        drafts, vocab, out_tokens.data_ptr(), num_accepted.data_ptr(), _ptr(seq_lens_out),
+        _stream(stream))
     _check(st, "mla_verify_drafts")
 
 

@@ -24,9 +24,8 @@
 namespace mla {
 namespace {
 
-constexpr int kAllocThreads = 1024;
+constexpr int kAllocThreads = 1024;    // at most; a step's few rows take fewer
 constexpr int kAllocWarps = kAllocThreads / 32;
-constexpr int kWarpRows = 128;         // rows a warp fills per bisection
 constexpr int64_t kBlockRows = 4096;   // rows that are worth a block of their own
 
 struct AllocParams {
@@ -51,39 +50,42 @@ struct AllocParams {
   uint32_t* status;
 };
 
+// Inclusive running sums of two values over the block's threads, in place; every thread
+// also gets the totals.
+struct Pair {
+  int64_t x, y;
+};
+__device__ __forceinline__ Pair block_scan(Pair& v, Pair* warp_sum, int warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t a = __shfl_up_sync(0xffffffffu, v.x, o), b = __shfl_up_sync(0xffffffffu, v.y, o);
+    if (lane >= o) v.x += a, v.y += b;
+  }
+  if (lane == 31) warp_sum[warp] = v;
+  __syncthreads();
+  // every warp scans the warps' sums
+  Pair s = lane < warps ? warp_sum[lane] : Pair{0, 0};
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t a = __shfl_up_sync(0xffffffffu, s.x, o), b = __shfl_up_sync(0xffffffffu, s.y, o);
+    if (lane >= o) s.x += a, s.y += b;
+  }
+  const int64_t px = __shfl_sync(0xffffffffu, s.x, max(warp - 1, 0));
+  const int64_t py = __shfl_sync(0xffffffffu, s.y, max(warp - 1, 0));
+  if (warp > 0) v.x += px, v.y += py;
+  const Pair total{__shfl_sync(0xffffffffu, s.x, 31), __shfl_sync(0xffffffffu, s.y, 31)};
+  __syncthreads();  // the sums are no longer read
+  return total;
+}
+
 struct AllocShared {
-  int64_t warp_sum[kAllocWarps];
+  Pair warp_sum[kAllocWarps];
   int64_t row_end[kAllocThreads];     // rows of the chunk's requests, ends
   int64_t first_page[kAllocThreads];  // pages taken before each
   int32_t len[kAllocThreads];         // cached tokens; -1: refused
   int32_t held[kAllocThreads];
 };
-
-// Inclusive running sum over the block's threads; every thread gets its own and the total.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sum, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  if (lane == 31) warp_sum[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t s = lane < kAllocWarps ? warp_sum[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += u;
-    }
-    if (lane < kAllocWarps) warp_sum[lane] = s;
-  }
-  __syncthreads();
-  if (warp > 0) v += warp_sum[warp - 1];
-  *total = warp_sum[kAllocWarps - 1];
-  __syncthreads();
-  return v;
-}
 
 // First i < n with end[i] > x (n if there is none).
 __device__ __forceinline__ int first_after(const int64_t* end, int n, int64_t x) {
@@ -105,28 +107,35 @@ __device__ __forceinline__ int64_t pages_for(int64_t tokens) {
 // then no other block may still read them (one block in all, or a launch of its own).
 template <bool kFill, bool kCommit>
 __global__ void __launch_bounds__(kAllocThreads)
-    kv_alloc_kernel(const AllocParams p, const int64_t rows_per) {
+    kv_alloc_kernel(const AllocParams p, const int64_t rows_per, const int warp_rows) {
   __shared__ AllocShared sm;
+  const int threads = blockDim.x, warps = threads >> 5;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool commit = kCommit && blockIdx.x == 0;
   const int64_t lo = blockIdx.x * rows_per, hi = min(lo + rows_per, p.num_slots);
   const int64_t count = min(max((int64_t)p.free_count[0], (int64_t)0), p.free_capacity);
   int64_t row0 = 0, page0 = 0, taken = 0;  // rows, pages asked for and pages taken so far
-  for (int b0 = 0; b0 < p.batch; b0 += kAllocThreads) {
+  for (int b0 = 0; b0 < p.batch; b0 += threads) {
     const int b = b0 + tid;
     const bool live = b < p.batch;
     const int L = live ? p.seq_lens[b] : 0, held = live ? p.held[b] : 0;
     const int asked = live ? p.new_tokens[b] : 0;
     const int64_t n = max(asked, 0);
-    int64_t rows, pages;
-    const int64_t row_end = row0 + block_scan(n, sm.warp_sum, &rows);
     uint32_t st = 0;
     if (L < 0 || asked < 0 || held < 0 || held > p.max_pages || pages_for(L) > held)
       st = MLA_KV_ALLOC_BAD_LENGTH;
     else if (pages_for(L + n) > p.max_pages) st = MLA_KV_ALLOC_TABLE_FULL;
-    else if (row_end > p.num_slots) st = MLA_KV_ALLOC_SLOTS_FULL;
-    const int64_t need = live && st == 0 ? max(pages_for(L + n) - held, (int64_t)0) : 0;
-    const int64_t page_end = page0 + block_scan(need, sm.warp_sum, &pages);
+    int64_t need = live && st == 0 ? max(pages_for(L + n) - held, (int64_t)0) : 0;
+    Pair ends{n, need};  // rows and pages up to and with this request
+    Pair sums = block_scan(ends, sm.warp_sum, warps);
+    const int64_t rows = sums.x, row_end = row0 + ends.x;
+    if (row0 + rows > p.num_slots) {  // some request's rows do not fit: it asks for no page
+      if (st == 0 && row_end > p.num_slots) st = MLA_KV_ALLOC_SLOTS_FULL;
+      if (st != 0) need = 0;
+      ends = Pair{0, need};
+      sums = block_scan(ends, sm.warp_sum, warps);
+    }
+    const int64_t pages = sums.y, page_end = page0 + ends.y;
     if (need > 0 && page_end > count) st = MLA_KV_ALLOC_NO_PAGES;
     if constexpr (kFill) {
       sm.row_end[tid] = row_end;
@@ -146,20 +155,18 @@ __global__ void __launch_bounds__(kAllocThreads)
       int64_t got = grown ? page_end : 0;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) got = max(got, __shfl_xor_sync(0xffffffffu, got, o));
-      if (lane == 0) sm.warp_sum[warp] = got;
+      if (lane == 0) sm.warp_sum[warp].x = got;
     }
     __syncthreads();
     if (commit)
-      for (int w = 0; w < kAllocWarps; ++w) taken = max(taken, sm.warp_sum[w]);
+      for (int w = 0; w < warps; ++w) taken = max(taken, sm.warp_sum[w].x);
     if constexpr (kFill) {
-      const int nb = min(kAllocThreads, p.batch - b0);
+      const int nb = min(threads, p.batch - b0);
       const int64_t x_end = min(row0 + rows, hi);
-      // (first row of this block's run in the chunk: a multiple of 128 rows into the run)
-      for (int64_t x0 = lo + (int64_t)warp * kWarpRows; x0 < x_end; x0 += kAllocWarps * kWarpRows) {
-        if (x0 + kWarpRows <= row0) continue;
+      for (int64_t x0 = lo + (int64_t)warp * warp_rows; x0 < x_end; x0 += warps * warp_rows) {
+        if (x0 + warp_rows <= row0) continue;  // (rows of an earlier chunk)
         int i = first_after(sm.row_end, nb, max(x0, row0));
-#pragma unroll
-        for (int k = 0; k < kWarpRows; k += 32) {
+        for (int k = 0; k < warp_rows; k += 32) {
           const int64_t x = x0 + k + lane;
           if (x < row0 || x >= x_end) continue;
           while (sm.row_end[i] <= x) ++i;
@@ -192,7 +199,7 @@ __global__ void __launch_bounds__(kAllocThreads)
     __syncthreads();
   }
   if constexpr (kFill)
-    for (int64_t x = max(row0, lo) + tid; x < hi; x += kAllocThreads) p.slots[x] = -1;
+    for (int64_t x = max(row0, lo) + tid; x < hi; x += threads) p.slots[x] = -1;
   if (commit && tid == 0) {
     p.cu[0] = 0;
     p.free_count_out[0] = (int32_t)(count - taken);
@@ -245,8 +252,13 @@ extern "C" mla_status mla_kv_alloc(const int32_t* seq_lens, const int32_t* new_t
   if (sms <= 0) return MLA_ERR_CUDA;
   int64_t blocks = std::min<int64_t>((num_slots + kBlockRows - 1) / kBlockRows, sms);
   blocks = std::max<int64_t>(blocks, 1);
-  const int64_t rows_per =
-      ((num_slots + blocks - 1) / blocks + kWarpRows - 1) / kWarpRows * kWarpRows;
+  // A warp bisects once per 128 rows, in a step of a few rows a request once per 32; one
+  // block has the threads that its requests and rows keep busy.
+  const int warp_rows = num_slots > kAllocThreads ? 128 : 32;
+  const int64_t rows_per = ((num_slots + blocks - 1) / blocks + warp_rows - 1) / warp_rows * warp_rows;
+  int threads = 128;
+  while (threads < kAllocThreads && (blocks > 1 || threads < std::max<int64_t>(batch, num_slots)))
+    threads *= 2;
   // Several blocks read the per-request inputs while block 0 writes its outputs: where
   // one of those shares memory with an input, they get a launch of their own.
   const void* ins[4] = {seq_lens, new_tokens, pages_held, free_count};
@@ -256,10 +268,10 @@ extern "C" mla_status mla_kv_alloc(const int32_t* seq_lens, const int32_t* new_t
     for (int o = 0; o < 5; ++o)
       apart = apart && !overlap(ins[i], i == 3 ? 1 : batch, outs[o], o == 2 ? 1 : batch + (o == 3));
   if (blocks == 1 || apart) {
-    kv_alloc_kernel<true, true><<<(unsigned)blocks, kAllocThreads, 0, s>>>(p, rows_per);
+    kv_alloc_kernel<true, true><<<(unsigned)blocks, threads, 0, s>>>(p, rows_per, warp_rows);
   } else {
-    kv_alloc_kernel<true, false><<<(unsigned)blocks, kAllocThreads, 0, s>>>(p, rows_per);
-    kv_alloc_kernel<false, true><<<1, kAllocThreads, 0, s>>>(p, rows_per);
+    kv_alloc_kernel<true, false><<<(unsigned)blocks, threads, 0, s>>>(p, rows_per, warp_rows);
+    kv_alloc_kernel<false, true><<<1, threads, 0, s>>>(p, rows_per, warp_rows);
   }
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

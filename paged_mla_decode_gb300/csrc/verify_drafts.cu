@@ -30,10 +30,16 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kVerifyThreads = 512;
-constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kUnroll = 2;  // tiles of a warp in flight: 32 KB of p and q per block, two blocks an SM
+// Two shapes of block. With few requests a block has an SM to itself and every load of a
+// run should be in flight at once; with many, four smaller blocks an SM cover each
+// other's waits (the drafts' probabilities, the cluster's barriers, the final scan).
+struct Few {
+  static constexpr int kThreads = 512, kBlocksPerSm = 1, kBytes = 128;  // in flight per row and thread
+};
+struct Many {
+  static constexpr int kThreads = 256, kBlocksPerSm = 4, kBytes = 32;
+};
 
 struct VerifyParams {
   const void* target;
@@ -53,8 +59,18 @@ struct VerifyParams {
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 // A probability within [0, 1] (NaN and negative values: 0).
-__device__ __forceinline__ float weight(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
-__device__ __forceinline__ uint64_t fixed60(float x) { return __float2ull_rz(weight(x) * 0x1p60f); }
+__device__ __forceinline__ float weight(float x) { return __saturatef(x); }
+// weight(x) in units of 2^-60, truncated: the 24-bit mantissa, shifted by the exponent
+// (a shift by 64 or more gives 0). In integer instructions, because a conversion to a
+// 64-bit integer runs at a small fraction of their rate: 84 us for 128 requests of
+// 163,840 tokens with conversions, VERIFY_NUMBER with shifts.
+__device__ __forceinline__ uint64_t fixed60(float x) {
+  const uint32_t bits = __float_as_uint(weight(x));
+  const uint64_t mantissa = (uint64_t)((bits << 8) | 0x80000000u) << 32;
+  uint64_t v;
+  asm("shr.u64 %0, %1, %2;\n" : "=l"(v) : "l"(mantissa), "r"(130u - (bits >> 23)));
+  return v;
+}
 __device__ __forceinline__ float unit(float u) { return u > 0.f ? fminf(u, 1.f - 0x1p-24f) : 0.f; }
 
 // The distribution that the next token is drawn from: p, or what a rejection leaves of it.
@@ -64,33 +80,45 @@ struct Rest {
   const T* q;  // null: none, or all of `skip`'s weight
   int skip;    // token that lost all its weight (-1: none)
 
-  __device__ __forceinline__ uint64_t of(float pi, float qi, int i) const {
-    const uint64_t a = fixed60(pi);
+  // of token i, element k of the loaded pi and qi
+  template <class W>
+  __device__ __forceinline__ uint64_t of(const W& pi, const W& qi, int k, int i) const {
+    const uint64_t a = fixed60(pi.get(k));
     if (q == nullptr) return i == skip ? 0 : a;
-    const uint64_t b = fixed60(qi);
+    const uint64_t b = fixed60(qi.get(k));
     return a > b ? a - b : 0;
   }
 };
 
-// kWide elements of a row from element i on (0 beyond `end`); 16-byte loads if kVec (then
-// the row is 16-byte aligned and i a multiple of kWide), one element otherwise.
+// kWide elements of a row from element i on (0 beyond `end`), kept as loaded; 16-byte
+// loads if kVec (then the row is 16-byte aligned and i a multiple of kWide), one element
+// otherwise.
 template <class T, bool kVec>
 struct Wide {
   static constexpr int kWide = kVec ? 16 / (int)sizeof(T) : 1;
-  static __device__ __forceinline__ void load(const T* row, int i, int end, float (&x)[kWide]) {
-    if (kVec && i + kWide <= end) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + i));
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t w[kVec ? 4 : 1];
+
+  __device__ __forceinline__ void load(const T* row, int i, int end) {
+    if constexpr (kVec) {
+      if (i + kWide <= end) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + i));
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+      } else {
+        w[0] = w[1] = w[2] = w[3] = 0u;
 #pragma unroll
-      for (int k = 0; k < kWide; ++k) {
-        if constexpr (sizeof(T) == 4) x[k] = __uint_as_float(w[k % 4]);
-        else x[k] = __uint_as_float((k & 1) ? w[(k / 2) % 4] & 0xffff0000u : w[(k / 2) % 4] << 16);
+        for (int k = 0; k < kWide; ++k)
+          if (i + k < end) w[k * sizeof(T) / 4] |= bits(row[i + k]) << (8 * (k * sizeof(T) % 4));
       }
     } else {
-#pragma unroll
-      for (int k = 0; k < kWide; ++k) x[k] = i + k < end ? to_float(row[i + k]) : 0.f;
+      w[0] = i < end ? bits(row[i]) : 0u;
     }
   }
+  __device__ __forceinline__ float get(int k) const {
+    const uint32_t v = w[k * sizeof(T) / 4] >> (8 * (k * sizeof(T) % 4));
+    return __uint_as_float(sizeof(T) == 4 ? v : v << 16);
+  }
+  static __device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
+  static __device__ __forceinline__ uint32_t bits(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
 };
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
@@ -99,11 +127,14 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
   return v;
 }
 
-template <class T, bool kVec>
-__global__ void __launch_bounds__(kVerifyThreads, 2)
+template <class T, bool kVec, class Shape>
+__global__ void __launch_bounds__(Shape::kThreads, Shape::kBlocksPerSm)
     verify_kernel(const VerifyParams p, const int run) {
   using W = Wide<T, kVec>;
+  constexpr int kVerifyThreads = Shape::kThreads, kVerifyWarps = kVerifyThreads / 32;
   constexpr int kTile = 32 * W::kWide;  // elements a warp takes at a time
+  // tiles of a warp in flight (one element of 4 or 2 bytes a load: 8 at most)
+  constexpr int kUnroll = kVec ? Shape::kBytes / 16 : 8;
   __shared__ uint64_t s_warp[kVerifyWarps];  // sums of the warps' runs
   __shared__ uint64_t s_block[2];            // of the block's, by pass; read by the cluster
   __shared__ uint64_t s_scan[kVerifyWarps];
@@ -128,6 +159,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2)
   const T* target = static_cast<const T*>(p.target) + (int64_t)b * (K + 1) * p.target_stride;
   const T* draft = p.draft ? static_cast<const T*>(p.draft) + (int64_t)b * K * p.draft_stride : nullptr;
   const float* u = p.uniforms + (int64_t)b * (K + 1);
+  const float u_sample = u[K];  // read ahead
   const int32_t* tokens = p.tokens + (int64_t)b * K;
   if (warp == 0) {
     bool ok = false;
@@ -158,18 +190,18 @@ __global__ void __launch_bounds__(kVerifyThreads, 2)
   for (int pass = 0; pass < 2; ++pass) {
     uint64_t sum = 0;
     for (int i0 = lo; i0 < hi; i0 += kUnroll * kTile) {
-      float pi[kUnroll][W::kWide], qi[kUnroll][W::kWide];
+      W pi[kUnroll], qi[kUnroll];
 #pragma unroll
       for (int t = 0; t < kUnroll; ++t) {
         const int i = i0 + t * kTile + lane * W::kWide;
-        W::load(rest.p, i, hi, pi[t]);
-        if (rest.q != nullptr) W::load(rest.q, i, hi, qi[t]);
+        pi[t].load(rest.p, i, hi);
+        if (rest.q != nullptr) qi[t].load(rest.q, i, hi);
       }
 #pragma unroll
       for (int t = 0; t < kUnroll; ++t)
 #pragma unroll
         for (int k = 0; k < W::kWide; ++k)
-          sum += rest.of(pi[t][k], qi[t][k], i0 + t * kTile + lane * W::kWide + k);
+          sum += rest.of(pi[t], qi[t], k, i0 + t * kTile + lane * W::kWide + k);
     }
     sum = warp_sum(sum);
     __syncthreads();  // (the last pass's sums are no longer read)
@@ -180,20 +212,17 @@ __global__ void __launch_bounds__(kVerifyThreads, 2)
       if (lane == 0) s_block[pass] = all;
     }
     cluster.sync();
-    total = before = 0;
-    for (int r = 0; r < ranks; ++r) {
-      const uint64_t v = *cluster.map_shared_rank(&s_block[pass], r);
-      total += v;
-      if (r < rank) before += v;
-    }
+    // lane r reads block r's sum
+    const uint64_t v = lane < ranks ? *cluster.map_shared_rank(&s_block[pass], lane) : 0;
+    total = warp_sum(v);
+    before = warp_sum(lane < rank ? v : 0);
     if (total > 0 || !rejected) break;
     rest.q = nullptr;  // a rejection that leaves nothing: the target's own distribution
     rest.skip = -1;
   }
-  // no block leaves while another may still read its sums, and every block has read the
-  // length that block 0 may overwrite
-  cluster.sync();
-  if (rank == 0) {
+  // no block leaves while another may still read its sums: arrive here, wait at the end
+  cluster.barrier_arrive();
+  if (rank == 0) {  // (every block has read the length that may be overwritten here)
     for (int i = tid; i <= K; i += kVerifyThreads)
       if (i != a) out[i] = i < a ? tokens[i] : -1;
     if (tid == 0) {
@@ -203,20 +232,23 @@ __global__ void __launch_bounds__(kVerifyThreads, 2)
     }
   }
   // the border: the first token whose running sum exceeds u * total, in integers
-  const uint64_t at = __umul64hi(__float2ull_rz(unit(u[K]) * 0x1p64f), total);
+  const uint64_t at = __umul64hi(__float2ull_rz(unit(u_sample) * 0x1p64f), total);
   int w = 0;
   while (w < kVerifyWarps && before + s_warp[w] <= at) before += s_warp[w++];
-  if (total == 0 || at < before || w == kVerifyWarps) return;  // in another block's run
+  if (total == 0 || at < before || w == kVerifyWarps) {  // in another block's run
+    cluster.barrier_wait();
+    return;
+  }
   const int run_lo = (int)min((int64_t)(rank * kVerifyWarps + w) * run, (int64_t)V);
   const int run_hi = (int)min((int64_t)run_lo + run, (int64_t)V);
   for (int i0 = run_lo; i0 < run_hi; i0 += kVerifyThreads * W::kWide) {
     const int i = i0 + tid * W::kWide;
-    float pi[W::kWide], qi[W::kWide];
-    W::load(rest.p, i, run_hi, pi);
-    if (rest.q != nullptr) W::load(rest.q, i, run_hi, qi);
+    W pi, qi;
+    pi.load(rest.p, i, run_hi);
+    if (rest.q != nullptr) qi.load(rest.q, i, run_hi);
     uint64_t mine = 0;
 #pragma unroll
-    for (int k = 0; k < W::kWide; ++k) mine += rest.of(pi[k], qi[k], i + k);
+    for (int k = 0; k < W::kWide; ++k) mine += rest.of(pi, qi, k, i + k);
     uint64_t c = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -232,7 +264,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2)
       int k = 0;
 #pragma unroll
       for (int j = 0; j < W::kWide; ++j) {
-        const uint64_t v = rest.of(pi[j], qi[j], i + j);
+        const uint64_t v = rest.of(pi, qi, j, i + j);
         if (upto + v <= at) {
           upto += v;
           k = j + 1;
@@ -250,22 +282,22 @@ __global__ void __launch_bounds__(kVerifyThreads, 2)
     if (at < before) break;
   }
   if (tid == 0) out[a] = s_token;
+  cluster.barrier_wait();
 }
 
 // Blocks per request: as many as keep 2,048 tokens each, so that few requests still
-// spread over many SMs. On 131,072 tokens and one request VERIFY_NUMBERS
+// spread over many SMs.
 int cluster_blocks(int vocab) {
   int c = 1;
   while (c < kMaxCluster && vocab >= 2 * c * 2048) c *= 2;
   return c;
 }
 
-template <class T, bool kVec>
-cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream) {
-  const int ranks = cluster_blocks(p.vocab);
+template <class T, bool kVec, class Shape>
+cudaError_t launch_verify(const VerifyParams& p, int ranks, cudaStream_t stream) {
   constexpr int kTile = 32 * Wide<T, kVec>::kWide;
-  const int warps = ranks * kVerifyWarps;
-  const int run = (int)(((int64_t)p.vocab + (int64_t)warps * kTile - 1) / ((int64_t)warps * kTile)) * kTile;
+  const int64_t share = (int64_t)ranks * (Shape::kThreads / 32) * kTile;
+  const int run = (int)((p.vocab + share - 1) / share) * kTile;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ranks;
@@ -273,20 +305,26 @@ cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.batch * ranks));
-  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.blockDim = dim3(Shape::kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_kernel<T, kVec>, p, run);
+  return cudaLaunchKernelEx(&cfg, verify_kernel<T, kVec, Shape>, p, run);
 }
 
 template <class T>
 cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream) {
+  const int ranks = cluster_blocks(p.vocab), sms = device_sm_count();
+  // (19 requests of 131,072 tokens, 152 blocks: 16.6 us, 14.5 with the other shape)
+  const bool few = 2 * (int64_t)p.batch * ranks <= sms;
   // 16-byte loads where every row starts on a 16-byte boundary
   const uintptr_t at = reinterpret_cast<uintptr_t>(p.target) | reinterpret_cast<uintptr_t>(p.draft);
   const int64_t strides = (p.target_stride | (p.draft ? p.draft_stride : 0)) * (int64_t)sizeof(T);
-  return ((at | (uintptr_t)strides) & 15u) == 0 ? launch_verify<T, true>(p, stream)
-                                                : launch_verify<T, false>(p, stream);
+  if (((at | (uintptr_t)strides) & 15u) == 0)
+    return few ? launch_verify<T, true, Few>(p, ranks, stream)
+               : launch_verify<T, true, Many>(p, ranks, stream);
+  return few ? launch_verify<T, false, Few>(p, ranks, stream)
+             : launch_verify<T, false, Many>(p, ranks, stream);
 }
 
 }  // namespace
