@@ -100,7 +100,12 @@ __global__ void kv_append_bf16_kernel(const __nv_bfloat16* __restrict__ latent,
 
 // One thread quantises one block of 32 elements (64 bytes of bf16 in, 16 bytes of codes
 // out); 18 threads cover a token. The threads of blocks 2i and 2i + 1 are neighbours in a
-// warp (18 is even) and share an exponent byte.
+// warp (18 is even) and share an exponent byte. 1,152 bytes read and 297 written per
+// token: DRAM bound if an element costs few instructions, so the largest magnitude is
+// found on bf16 pairs and the codes come from the hardware's conversion of x * inverse
+// (kMultiply: exact, see E2m1Steps); by three comparisons with the thresholds where the
+// scale has no such multiplier. NUMBERS
+template <bool kMultiply>
 __global__ void kv_append_e2m1_kernel(const __nv_bfloat16* __restrict__ latent,
                                       const __nv_bfloat16* __restrict__ rope,
                                       const int32_t* __restrict__ slots, int64_t num_tokens,
@@ -128,33 +133,48 @@ __global__ void kv_append_e2m1_kernel(const __nv_bfloat16* __restrict__ latent,
       raw[4 * i + 3] = v.w;
     }
   }
-  // largest magnitude by its bits (their order is the values'; a NaN comes out on top)
-  uint32_t top = 0;
+  // largest magnitude (NaN if there is one)
+  __nv_bfloat162 most = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&raw[0]));
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    top = max(top, max(raw[i] & 0x7fffu, (raw[i] >> 16) & 0x7fffu));
-  const bool nan = top > 0x7f80u;
+  for (int i = 1; i < 16; ++i)
+    most = __hmax2_nan(most, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i])));
+  const float amax = __bfloat162float(__hmax_nan(__low2bfloat16(most), __high2bfloat16(most)));
+  const bool nan = isnan(amax);
   // smallest e with amax <= steps.top * 2^e: the difference of the two numbers' bits in
   // units of a binade, rounded up; stored as n = e + 8 in 0..14
-  const int diff = (int)(top << 16) - __float_as_int(steps.top);
+  const int diff = __float_as_int(amax) - __float_as_int(steps.top);
   const int n = nan ? kE2m1NanExp : min(max(((diff + 0x7fffff) >> 23) + 8, 0), 14);
   const float down = __int_as_float((127 + 8 - min(n, 14)) << 23);  // 2^-e
   uint32_t words[4];
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     uint32_t word = 0;
+    if constexpr (kMultiply) {
+      const float by = steps.inverse * down;
+      uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t bits = (i & 1) ? raw[4 * w + i / 2] >> 16 : raw[4 * w + i / 2] & 0xffffu;
-      const float y = __uint_as_float((bits & 0x7fffu) << 16) * down;
-      // three comparisons find the number of thresholds at or below y
-      const bool c4 = y >= steps.step[3];
-      const bool c2 = y >= (c4 ? steps.step[5] : steps.step[1]);
-      const float last = c4 ? (c2 ? steps.step[6] : steps.step[4])
-                            : (c2 ? steps.step[2] : steps.step[0]);
-      const uint32_t code = (c4 ? 4u : 0u) | (c2 ? 2u : 0u) | (y >= last ? 1u : 0u) |
-                            ((bits >> 12) & 8u);
-      word |= code << (4 * i);
+      for (int i = 0; i < 4; ++i) {
+        const float2 x =
+            __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[4 * w + i]));
+        asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n cvt.u32.u8 %0, t;\n}\n"
+            : "=r"(c[i])
+            : "f"(x.x * by), "f"(x.y * by));
+      }
+      word = c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t bits = (i & 1) ? raw[4 * w + i / 2] >> 16 : raw[4 * w + i / 2] & 0xffffu;
+        const float y = __uint_as_float((bits & 0x7fffu) << 16) * down;
+        // three comparisons find the number of thresholds at or below y
+        const bool c4 = y >= steps.step[3];
+        const bool c2 = y >= (c4 ? steps.step[5] : steps.step[1]);
+        const float last = c4 ? (c2 ? steps.step[6] : steps.step[4])
+                              : (c2 ? steps.step[2] : steps.step[0]);
+        const uint32_t code = (c4 ? 4u : 0u) | (c2 ? 2u : 0u) | (y >= last ? 1u : 0u) |
+                              ((bits >> 12) & 8u);
+        word |= code << (4 * i);
+      }
     }
     words[w] = nan ? 0u : word;
   }
@@ -201,10 +221,11 @@ extern "C" mla_status mla_kv_append(const void* latent, const void* rope,
         static_cast<const __nv_bfloat16*>(latent), static_cast<const __nv_bfloat16*>(rope),
         slot_mapping, num_tokens, static_cast<uint8_t*>(kv_pages), num_slots, kv_scale);
   } else if (kv_dtype == MLA_KV_E2M1) {
-    kv_append_e2m1_kernel<<<(unsigned)grid, block, 0, s>>>(
+    const E2m1Steps steps = e2m1_steps(kv_scale);
+    const auto kernel = steps.inverse > 0.f ? kv_append_e2m1_kernel<true> : kv_append_e2m1_kernel<false>;
+    kernel<<<(unsigned)grid, block, 0, s>>>(
         static_cast<const __nv_bfloat16*>(latent), static_cast<const __nv_bfloat16*>(rope),
-        slot_mapping, num_tokens, static_cast<uint8_t*>(kv_pages), num_slots,
-        e2m1_steps(kv_scale));
+        slot_mapping, num_tokens, static_cast<uint8_t*>(kv_pages), num_slots, steps);
   } else {
     kv_append_bf16_kernel<<<(unsigned)grid, block, 0, s>>>(
         static_cast<const __nv_bfloat16*>(latent), static_cast<const __nv_bfloat16*>(rope),

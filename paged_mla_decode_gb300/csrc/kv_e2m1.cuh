@@ -15,7 +15,9 @@
 // expands to e4m3 codes exactly, and the tensor-core path of the e4m3 cache applies.
 #pragma once
 
+#include <math.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "mla_common.cuh"
 
@@ -46,9 +48,16 @@ __host__ __device__ constexpr int e2m1_exp_offset(int block, int token) {
 // The products (27 significant bits at most) are formed exactly in double; the nearest
 // float32 on the right side of each decides every float32 y as the product would.
 // s must lie in [2^-100, 2^100], so that no threshold over- or underflows.
+//
+// `inverse` (0 if there is none): a float32 r for which the hardware's rounding of
+// fl(y * r) to e2m1 agrees with the thresholds for every bf16 y. A product is rounded to
+// 24 bits, so this is a property of the bf16 numbers on either side of each threshold,
+// checked here for 1/s and its neighbours up to two units away. Of the 2^23 mantissas of
+// s only 1.875 has none (its midpoints are exact ties of bf16 numbers, and no r hits all).
 struct E2m1Steps {
   float step[7];
   float top;
+  float inverse;
 };
 inline float e2m1_round_down(double d) {
   const float f = (float)d;
@@ -59,13 +68,31 @@ inline float e2m1_round_up(double d) {
   return (double)f < d ? nextafterf(f, INFINITY) : f;
 }
 inline E2m1Steps e2m1_steps(float s) {
-  const double mid[7] = {0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0};
+  const float mid[7] = {0.25f, 0.75f, 1.25f, 1.75f, 2.5f, 3.5f, 5.0f};
   E2m1Steps r;
+  float above[7], below[7];  // the bf16 numbers on either side of each threshold
   for (int i = 0; i < 7; ++i) {
-    const double t = mid[i] * (double)s;
+    const double t = (double)mid[i] * (double)s;
     r.step[i] = (i & 1) ? e2m1_round_up(t) : nextafterf(e2m1_round_down(t), INFINITY);
+    uint32_t bits;
+    memcpy(&bits, &r.step[i], 4);
+    bits = (bits + 0xffffu) & 0xffff0000u;
+    memcpy(&above[i], &bits, 4);
+    bits -= 0x10000u;
+    memcpy(&below[i], &bits, 4);
   }
   r.top = e2m1_round_down(7.0 * (double)s);
+  r.inverse = 0.f;
+  for (int k = 0; k < 5 && r.inverse == 0.f; ++k) {
+    float c = 1.0f / s;
+    for (int n = 0; n < (k + 1) / 2; ++n) c = nextafterf(c, (k & 1) ? INFINITY : 0.f);
+    bool ok = true;
+    for (int i = 0; i < 7; ++i) {
+      const float a = above[i] * c, b = below[i] * c;
+      ok = ok && ((i & 1) ? a >= mid[i] && b < mid[i] : a > mid[i] && b <= mid[i]);
+    }
+    if (ok) r.inverse = c;
+  }
   return r;
 }
 inline bool e2m1_scale_ok(float s) { return s >= 0x1p-100f && s <= 0x1p100f; }

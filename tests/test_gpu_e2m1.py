@@ -44,7 +44,8 @@ def test_append_random_tokens(cuda_device, n, scale):
     _check_append(wl.f32_to_bf16_bits(x), slots, pages, scale, cuda_device)
 
 
-@pytest.mark.parametrize("scale", [SCALE, 1.0, float(np.float32(1.0 / 3.0)), float(np.float32(0.7)), 2.0 ** -100])
+@pytest.mark.parametrize("scale", [SCALE, 1.0, float(np.float32(1.0 / 3.0)), float(np.float32(0.7)), 2.0 ** -100,
+                                   1.875, 1.875 * 2.0 ** -8, 1.5, 0.1875])
 def test_append_every_bf16(cuda_device, scale):
     """All 65,536 bf16 values, neighbours sharing blocks: ties, near ties (an e2m1 midpoint
     times the default scale is within one float32 ulp of bf16 values), subnormals,
