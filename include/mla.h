@@ -392,7 +392,7 @@ MLA_API mla_status mla_kv_alloc(const int32_t* seq_lens, const int32_t* new_toke
  *
  * Arithmetic: probabilities are taken within [0, 1] (NaN as 0), uniforms within
  * [0, 1 - 2^-24] (NaN as 0). The acceptance test is exact; weights are summed as
- * integers in units of 2^-60 (a probability below 2^-37 is truncated to them),
+ * integers in units of 2^-60 (a probability below 2^-37 is rounded to them),
  * so the result does not depend on the order of the sum. A row's probabilities
  * must sum to less than 16.
  *

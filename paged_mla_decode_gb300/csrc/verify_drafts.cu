@@ -7,14 +7,16 @@
 // drawn from max(p_j - q_j, 0), normalised; if all are kept, from p of the position after
 // the last one.
 //
-// Arithmetic. A probability becomes a 64-bit integer in units of 2^-60 (exact for a
-// float32 of 2^-37 and above, truncated below), so that sums are exact, do not depend on
-// the order of addition, and the sampled index is the smallest i with
-// sum_{k <= i} w_k > u * sum w, decided in integers. The acceptance test compares
-// u * q < p in double, where the product is exact.
+// Arithmetic. A probability becomes an integer in units of 2^-60 (exact for a float32 of
+// 2^-37 and above, rounded below), so that sums are exact, do not depend on the order of
+// addition, and the sampled index is the smallest i with sum_{k <= i} w_k > u * sum w,
+// decided in integers. The acceptance test compares u * q < p in double, where the
+// product is exact.
 //
-// One row of p (and one of q after a rejection) is read: DRAM bound for many requests,
-// latency bound for few. So a request is worked by a cluster of up to eight blocks, each
+// One row of p (and one of q after a rejection) is read: bound by DRAM and by the 20
+// instructions that a pair of probabilities takes for many requests (4.7 TB/s with 512),
+// by latency for few (10 us: the drafts' probabilities, the run, the cluster's exchange,
+// the final scan, one after the other). So a request is worked by a cluster of up to eight blocks, each
 // summing a run of the vocabulary; the blocks exchange their sums through distributed
 // shared memory, and the one whose run holds the border scans the 1/16 of it (a warp's
 // run) that does, with all its threads at once.
@@ -35,10 +37,10 @@ constexpr int kMaxCluster = 8;
 // run should be in flight at once; with many, four smaller blocks an SM cover each
 // other's waits (the drafts' probabilities, the cluster's barriers, the final scan).
 struct Few {
-  static constexpr int kThreads = 512, kBlocksPerSm = 1, kBytes = 128;  // in flight per row and thread
+  static constexpr int kThreads = 512, kBlocksPerSm = 1, kLoads = 8;  // in flight per row and thread
 };
 struct Many {
-  static constexpr int kThreads = 256, kBlocksPerSm = 4, kBytes = 32;
+  static constexpr int kThreads = 256, kBlocksPerSm = 4, kLoads = 4;
 };
 
 struct VerifyParams {
@@ -60,16 +62,31 @@ __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 // A probability within [0, 1] (NaN and negative values: 0).
 __device__ __forceinline__ float weight(float x) { return __saturatef(x); }
-// weight(x) in units of 2^-60, truncated: the 24-bit mantissa, shifted by the exponent
-// (a shift by 64 or more gives 0). In integer instructions, because a conversion to a
-// 64-bit integer runs at a small fraction of their rate: 84 us for 128 requests of
-// 163,840 tokens with conversions, VERIFY_NUMBER with shifts.
-__device__ __forceinline__ uint64_t fixed60(float x) {
-  const uint32_t bits = __float_as_uint(weight(x));
-  const uint64_t mantissa = (uint64_t)((bits << 8) | 0x80000000u) << 32;
-  uint64_t v;
-  asm("shr.u64 %0, %1, %2;\n" : "=l"(v) : "l"(mantissa), "r"(130u - (bits >> 23)));
-  return v;
+// weight(x) in units of 2^-60 as three slices of 20 bits, s[0] 2^40 + s[1] 2^20 + s[2].
+// Adding 8 to x leaves x rounded to 2^-20 in the low bits of the float32 sum; what the
+// rounding left over is exact, and 1.5 * 2^-17 and 1.5 * 2^-37 do the same for it with
+// 2^-40 and 2^-60 (signed: the low bits of a sum count from those of its constant, so the
+// slices of a difference are differences of the sums as integers). Six additions on the
+// full-rate pipe per number. For 128 requests of 163,840 tokens conversions to a 64-bit
+// integer took 84 us, shifts by the exponent 41, this 36 (122 MB read).
+struct Slices {
+  int32_t s[3];
+};
+__device__ __forceinline__ Slices slices(float w) {
+  constexpr float kA = 8.f, kB = 0x1.8p-17f, kC = 0x1.8p-37f;
+  constexpr float kBC = kB + kC;  // exact: 21 bits
+  Slices r;
+  const float a = w + kA;
+  const float rest = w - (a - kA);
+  const float b = rest + kB;
+  r.s[0] = __float_as_int(a);
+  r.s[1] = __float_as_int(b);
+  r.s[2] = __float_as_int(rest - (b - kBC));  // (rest - slice 1) + kC, rounded once
+  return r;
+}
+__device__ __forceinline__ uint64_t joined(const Slices& w) {
+  return ((uint64_t)(int64_t)w.s[0] << 40) + ((uint64_t)(int64_t)w.s[1] << 20) +
+         (uint64_t)(int64_t)w.s[2];
 }
 __device__ __forceinline__ float unit(float u) { return u > 0.f ? fminf(u, 1.f - 0x1p-24f) : 0.f; }
 
@@ -79,16 +96,23 @@ struct Rest {
   const T* p;
   const T* q;  // null: none, or all of `skip`'s weight
   int skip;    // token that lost all its weight (-1: none)
-
-  // of token i, element k of the loaded pi and qi
-  template <class W>
-  __device__ __forceinline__ uint64_t of(const W& pi, const W& qi, int k, int i) const {
-    const uint64_t a = fixed60(pi.get(k));
-    if (q == nullptr) return i == skip ? 0 : a;
-    const uint64_t b = fixed60(qi.get(k));
-    return a > b ? a - b : 0;
-  }
 };
+// Adds a token's weight: max(x - y, 0) with a q row (kPair), x without.
+template <bool kPair>
+__device__ __forceinline__ void add_weight(Slices& to, float x, float y) {
+  const Slices a = slices(weight(x));
+  if constexpr (kPair) {
+    const Slices b = slices(weight(y));
+    if (weight(x) > weight(y)) {
+#pragma unroll
+      for (int j = 0; j < 3; ++j) to.s[j] += a.s[j] - b.s[j];
+    }
+  } else {
+    const Slices zero = slices(0.f);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) to.s[j] += a.s[j] - zero.s[j];
+  }
+}
 
 // kWide elements of a row from element i on (0 beyond `end`), kept as loaded; 16-byte
 // loads if kVec (then the row is 16-byte aligned and i a multiple of kWide), one element
@@ -121,6 +145,39 @@ struct Wide {
   static __device__ __forceinline__ uint32_t bits(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
 };
 
+// Sum of a lane's share of elements lo .. hi - 1 of the row (kUnroll tiles in flight).
+template <class T, bool kVec, int kUnroll, bool kPair>
+__device__ __forceinline__ uint64_t run_sum(const Rest<T>& rest, int lo, int hi, int lane) {
+  using W = Wide<T, kVec>;
+  constexpr int kTile = 32 * W::kWide;  // elements a warp takes at a time
+  static_assert(kUnroll * W::kWide <= 64, "20-bit slices of 64 elements stay within 32 bits");
+  uint64_t sum = 0;
+  for (int i0 = lo; i0 < hi; i0 += kUnroll * kTile) {
+    W pi[kUnroll], qi[kPair ? kUnroll : 1];
+#pragma unroll
+    for (int t = 0; t < kUnroll; ++t) {
+      const int i = i0 + t * kTile + lane * W::kWide;
+      pi[t].load(rest.p, i, hi);
+      if constexpr (kPair) qi[t].load(rest.q, i, hi);
+    }
+    Slices part{{0, 0, 0}};
+#pragma unroll
+    for (int t = 0; t < kUnroll; ++t)
+#pragma unroll
+      for (int k = 0; k < W::kWide; ++k)
+        add_weight<kPair>(part, pi[t].get(k), kPair ? qi[kPair ? t : 0].get(k) : 0.f);
+    sum += joined(part);
+  }
+  return sum;
+}
+
+template <class T>
+__device__ __forceinline__ uint64_t weight_of(const T* row, int i) {
+  Slices one{{0, 0, 0}};
+  add_weight<false>(one, to_float(row[i]), 0.f);
+  return joined(one);
+}
+
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -132,9 +189,8 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kBlocksPerSm)
     verify_kernel(const VerifyParams p, const int run) {
   using W = Wide<T, kVec>;
   constexpr int kVerifyThreads = Shape::kThreads, kVerifyWarps = kVerifyThreads / 32;
-  constexpr int kTile = 32 * W::kWide;  // elements a warp takes at a time
-  // tiles of a warp in flight (one element of 4 or 2 bytes a load: 8 at most)
-  constexpr int kUnroll = kVec ? Shape::kBytes / 16 : 8;
+  // tiles of a warp in flight (bf16: twice the elements a load, half the loads)
+  constexpr int kUnroll = kVec ? Shape::kLoads * (int)sizeof(T) / 4 : 8;
   __shared__ uint64_t s_warp[kVerifyWarps];  // sums of the warps' runs
   __shared__ uint64_t s_block[2];            // of the block's, by pass; read by the cluster
   __shared__ uint64_t s_scan[kVerifyWarps];
@@ -143,8 +199,31 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kBlocksPerSm)
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / ranks, K = p.max_drafts, V = p.vocab;
+  // everything that hangs on no other load first: one draft a lane
   const int drafts = p.num_drafts ? p.num_drafts[b] : K;
   const int L = p.seq_lens ? p.seq_lens[b] : 0;
+  const T* target = static_cast<const T*>(p.target) + (int64_t)b * (K + 1) * p.target_stride;
+  const T* draft = p.draft ? static_cast<const T*>(p.draft) + (int64_t)b * K * p.draft_stride : nullptr;
+  const float* u = p.uniforms + (int64_t)b * (K + 1);
+  const int32_t* tokens = p.tokens + (int64_t)b * K;
+  const float u_sample = u[K];
+  if (warp == 0) {
+    bool ok = false;
+    if (lane < K) {
+      const int x = tokens[lane];
+      const float v = unit(u[lane]);
+      if (x >= 0 && x < V) {
+        const float px = weight(to_float(target[lane * p.target_stride + x]));
+        const float qx = draft ? weight(to_float(draft[lane * p.draft_stride + x])) : 1.f;
+        ok = lane < drafts && (double)v * (double)qx < (double)px;
+      }
+    }
+    const int kept = __ffs(~__ballot_sync(0xffffffffu, ok)) - 1;  // K <= 31: some lane is false
+    if (lane == 0) {
+      s_row = kept;
+      s_token = -1;
+    }
+  }
   int32_t* out = p.out_tokens + (int64_t)b * (K + 1);
   if (drafts < 0 || drafts > K || L < 0) {  // left out: nothing of it changes the length
     if (rank == 0) {
@@ -155,27 +234,6 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kBlocksPerSm)
       }
     }
     return;
-  }
-  const T* target = static_cast<const T*>(p.target) + (int64_t)b * (K + 1) * p.target_stride;
-  const T* draft = p.draft ? static_cast<const T*>(p.draft) + (int64_t)b * K * p.draft_stride : nullptr;
-  const float* u = p.uniforms + (int64_t)b * (K + 1);
-  const float u_sample = u[K];  // read ahead
-  const int32_t* tokens = p.tokens + (int64_t)b * K;
-  if (warp == 0) {
-    bool ok = false;
-    if (lane < drafts) {
-      const int x = tokens[lane];
-      if (x >= 0 && x < V) {
-        const float px = weight(to_float(target[lane * p.target_stride + x]));
-        const float qx = draft ? weight(to_float(draft[lane * p.draft_stride + x])) : 1.f;
-        ok = (double)unit(u[lane]) * (double)qx < (double)px;
-      }
-    }
-    const int kept = __ffs(~__ballot_sync(0xffffffffu, ok)) - 1;  // K <= 31: some lane is false
-    if (lane == 0) {
-      s_row = kept;
-      s_token = -1;
-    }
   }
   __syncthreads();
   const int a = s_row;
@@ -188,21 +246,9 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kBlocksPerSm)
   const int hi = (int)min((int64_t)lo + run, (int64_t)V);
   uint64_t total = 0, before = 0;  // of all blocks; of those before this one
   for (int pass = 0; pass < 2; ++pass) {
-    uint64_t sum = 0;
-    for (int i0 = lo; i0 < hi; i0 += kUnroll * kTile) {
-      W pi[kUnroll], qi[kUnroll];
-#pragma unroll
-      for (int t = 0; t < kUnroll; ++t) {
-        const int i = i0 + t * kTile + lane * W::kWide;
-        pi[t].load(rest.p, i, hi);
-        if (rest.q != nullptr) qi[t].load(rest.q, i, hi);
-      }
-#pragma unroll
-      for (int t = 0; t < kUnroll; ++t)
-#pragma unroll
-        for (int k = 0; k < W::kWide; ++k)
-          sum += rest.of(pi[t], qi[t], k, i0 + t * kTile + lane * W::kWide + k);
-    }
+    uint64_t sum = rest.q != nullptr ? run_sum<T, kVec, kUnroll, true>(rest, lo, hi, lane)
+                                     : run_sum<T, kVec, kUnroll, false>(rest, lo, hi, lane);
+    if (rest.skip >= lo && rest.skip < hi && lane == 0) sum -= weight_of(rest.p, rest.skip);
     sum = warp_sum(sum);
     __syncthreads();  // (the last pass's sums are no longer read)
     if (lane == 0) s_warp[warp] = sum;
@@ -246,9 +292,15 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kBlocksPerSm)
     W pi, qi;
     pi.load(rest.p, i, run_hi);
     if (rest.q != nullptr) qi.load(rest.q, i, run_hi);
-    uint64_t mine = 0;
+    uint64_t mine = 0, each[W::kWide];
 #pragma unroll
-    for (int k = 0; k < W::kWide; ++k) mine += rest.of(pi, qi, k, i + k);
+    for (int k = 0; k < W::kWide; ++k) {
+      Slices one{{0, 0, 0}};
+      if (rest.q != nullptr) add_weight<true>(one, pi.get(k), qi.get(k));
+      else if (i + k != rest.skip) add_weight<false>(one, pi.get(k), 0.f);
+      each[k] = joined(one);
+      mine += each[k];
+    }
     uint64_t c = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -264,9 +316,8 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kBlocksPerSm)
       int k = 0;
 #pragma unroll
       for (int j = 0; j < W::kWide; ++j) {
-        const uint64_t v = rest.of(pi, qi, j, i + j);
-        if (upto + v <= at) {
-          upto += v;
+        if (upto + each[j] <= at) {
+          upto += each[j];
           k = j + 1;
         } else {
           upto = ~0ull;  // past the border: every later test fails
@@ -286,7 +337,8 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kBlocksPerSm)
 }
 
 // Blocks per request: as many as keep 2,048 tokens each, so that few requests still
-// spread over many SMs.
+// spread over many SMs. Fewer blocks with many requests (one wave of them) were no faster:
+// 128 requests of 163,840 tokens 36.3 us with four, 35.7 with eight; 512 120 and 104.
 int cluster_blocks(int vocab) {
   int c = 1;
   while (c < kMaxCluster && vocab >= 2 * c * 2048) c *= 2;
@@ -314,7 +366,7 @@ cudaError_t launch_verify(const VerifyParams& p, int ranks, cudaStream_t stream)
 
 template <class T>
 cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream) {
-  const int ranks = cluster_blocks(p.vocab), sms = device_sm_count();
+  const int sms = device_sm_count(), ranks = cluster_blocks(p.vocab);
   // (19 requests of 131,072 tokens, 152 blocks: 16.6 us, 14.5 with the other shape)
   const bool few = 2 * (int64_t)p.batch * ranks <= sms;
   // 16-byte loads where every row starts on a 16-byte boundary
