@@ -915,13 +915,17 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(BAR_S_EMPTY + (int)(j & 1)));
         float s[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s[i] = (__uint_as_float(shi[i]) + __uint_as_float(slo[i])) * qmul;
+        if (nvis < kPageSize) {  // (only a row's last page, or a bad page id, hides tokens)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (16 * c16 + i >= nvis) s[i] = -INFINITY;
+        }
         float tm = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const bool vis = 16 * c16 + i < nvis;
-          s[i] = vis ? (__uint_as_float(shi[i]) + __uint_as_float(slo[i])) * qmul : -INFINITY;
-          tm = fmaxf(tm, s[i]);
-        }
+        for (int i = 0; i < 16; ++i) tm = fmaxf(tm, s[i]);
         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
         if (lane < 16) pmax_s[(int)(j & 1) * 128 + g * 64 + h] = tm;
         // P buffer j % 3 was read by PV(j - 3); waiting for it also makes the
