@@ -23,15 +23,16 @@
 // serve trillions of tokens ...", section "First, understand the workload").
 //
 // A 4-bit cache (kv_e2m1.cuh) takes the same path (kE2m1): its pages land in a second,
-// smaller ring as stored, four expander warps rewrite each as the swizzled e4m3 page
+// smaller ring as stored, six expander warps rewrite each as the swizzled e4m3 page
 // that the contractions read (a table lookup, exact), and everything after that is
-// the e4m3 kernel. It trades one ring slot for the raw pages (kRing 4 + 2 raw). What
-// bounds it is shared-memory bandwidth: a page's MMAs read 140 KB of operands (V twice,
+// the e4m3 kernel. It trades one ring slot for the raw pages (kRing 4 + 2 raw). 31
+// requests of 60k-140k tokens with 64 heads (307 pages a CTA) take 438 us, 413 without
+// the expansion, 368 from an e4m3 cache, whose softmax has more registers. What is left
+// is shared-memory bandwidth above all: a page's MMAs read 140 KB of operands (V twice,
 // for P's two terms), the P buffers and page copies move 35 KB, the expansion reads and
-// writes another 55 KB: 1,800 cycles at 128 B a cycle, of the 2,330 a page takes
-// (31 requests of 60k-140k tokens, 64 heads: 488 us, 307 pages a CTA).
+// writes another 55 KB: 1,800 cycles at 128 B a cycle, of some 2,300 that a page takes.
 //
-// Warp roles (416 threads; 544 with the expanders):
+// Warp roles (416 threads; 608 with the expanders):
 //   warps 0-7  q loading, softmax and epilogue. Row t of A and S is (head
 //              16*(t/32) + t%16, part (t/16)%2), part 0 = hi, 1 = lo. Warp w reads
 //              TMEM lanes 32*(w%4) .. +31; thread (w, lane) handles head
@@ -45,7 +46,9 @@
 //              (128-byte swizzled latent blocks, 64-byte swizzled rope block).
 //   warps 9-10 issue QK of even / odd pages (lane 0); warp 9 allocates TMEM.
 //   warps 11-12 issue PV of even / odd pages (lane 0).
-//   warps 13-16 (4-bit cache only) expand raw pages into the ring, one per scheduler.
+//   warps 13-18 (4-bit cache only) expand raw pages into the ring. More than 20 warps
+//              would leave a thread 80 registers, with which the softmax takes twice as
+//              long; up to 20 it has 96.
 // A thread that issues MMAs stalls for a while after each batch (until the
 // tensor pipe's queue has room), so two issuers per contraction keep the pipe
 // fed: one issues while the other waits.
@@ -88,7 +91,7 @@ constexpr int kTmaWarp = kSmWarps;                   // 8
 constexpr int kQkWarp0 = kSmWarps + 1;               // 9: also allocates TMEM
 constexpr int kPvWarp0 = kSmWarps + 3;               // 11
 constexpr int kExpWarp0 = kSmWarps + 5;              // 13: expanders of a 4-bit cache
-constexpr int kExpWarps = 4;
+constexpr int kExpWarps = 6;
 constexpr int kPageBytes = kPageSize * kDEntry;      // 36864
 constexpr int kLatBlock = kPageSize * 128;           // 8192: 64 rows x 128 dims
 constexpr int kRopeOff = 4 * kLatBlock;              // rope block within a page slot
@@ -124,7 +127,7 @@ constexpr int kTableAhead = 32;  // pages described (block-table read started) b
 // Shared memory map (offsets from a 1024-aligned base) and barriers.
 template <bool kE2m1>
 struct Map {
-  static constexpr int kThreads = 32 * (kE2m1 ? kExpWarp0 + kExpWarps : kSmWarps + 5);  // 544, 416
+  static constexpr int kThreads = 32 * (kE2m1 ? kExpWarp0 + kExpWarps : kSmWarps + 5);  // 608, 416
   static constexpr int kRing = kE2m1 ? 4 : 5;          // e4m3 pages in flight
   static constexpr int kRawRing = kE2m1 ? 2 : 0;       // 4-bit pages in flight
   static constexpr int kOffPages = 0;
@@ -341,16 +344,12 @@ __device__ const uint64_t kE2m1Lut[16] = {
     e2m1_as_e4m3(8),  e2m1_as_e4m3(9),  e2m1_as_e4m3(10), e2m1_as_e4m3(11),
     e2m1_as_e4m3(12), e2m1_as_e4m3(13), e2m1_as_e4m3(14), e2m1_as_e4m3(15)};
 
-// One expander warp's share of a page: of every 128-dim block the quarter g (blocks g,
-// 4 + g, 8 + g, 12 + g), two tokens (lane, lane + 32) a thread, and a quarter of the two
-// rope blocks. Alone on an SM it is bound by the ALU pipe (a warp instruction per two
-// cycles; 32 of the 50 that 32 elements take convert), so there is one expander per
-// scheduler, the exponents are read once, the next blocks' loads and table rows are in
-// flight while a block is written, and a thread's place in a row is a constant: 974
-// cycles a page. Only two blocks are unrolled: the roles' loops share the instruction
-// cache (all nine unrolled: 510 us on the 31 requests above). Three warps with 128
-// registers a thread instead of four with 96 took 493 us, five warpgroups with registers
-// moved to the softmax (setmaxnreg) 515.
+// One expander warp's share of a page: blocks 3e .. 3e + 2 of every token, two tokens
+// (lane, lane + 32) a thread. Beside the other roles a warp gets an instruction every four
+// to five cycles, whatever its code, so six warps share the page (31 requests as above:
+// 438 us; four with nine blocks a thread 485, three with twelve 493). The next block's
+// loads and table rows are in flight while a block is written. Not unrolled: the roles'
+// loops share the instruction cache (457 us unrolled).
 struct ExpandUnit {
   uint4 codes;
   uint2 row;  // of the expansion table
@@ -375,52 +374,48 @@ __device__ __forceinline__ void expand_write(const ExpandUnit& u, uint32_t at) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(at ^ 16u), "r"(c2.x), "r"(c2.y),
                "r"(c3.x), "r"(c3.y) : "memory");
 }
-__device__ __forceinline__ void expand_page(uint32_t raw, uint32_t page, uint32_t lut, int g,
+__device__ __forceinline__ void expand_page(uint32_t raw, uint32_t page, uint32_t lut, int e,
                                             int lane) {
-  const int rt = lane + 32 * (g & 1);  // rope: block 16 + g / 2 of token rt
-  uint32_t exps[2], rope_exps;         // four bytes each, this quarter's nibble the lowest
+  constexpr int kPer = kE2m1Blocks / kExpWarps;  // 3
+  const int b0 = kPer * e;
+  uint32_t exps[2];  // the blocks' nibbles, the first lowest
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    uint32_t b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      asm volatile("ld.shared.u8 %0, [%1];\n"
-                   : "=r"(b[i])
-                   : "r"(raw + e2m1_exp_offset(4 * i + g, lane + 32 * k)));
-    exps[k] = (b[0] + b[1] * 0x100u + b[2] * 0x10000u + b[3] * 0x1000000u) >> (4 * (g & 1));
+    uint32_t x, y;
+    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(x) : "r"(raw + e2m1_exp_offset(b0, lane + 32 * k)));
+    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(y) : "r"(raw + e2m1_exp_offset(b0 + 2, lane + 32 * k)));
+    exps[k] = (x + (y << 8)) >> (4 * (b0 & 1));
   }
-  asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(rope_exps) : "r"(raw + e2m1_exp_offset(16, rt)));
-  uint32_t code_at = raw + e2m1_code_offset(g, lane);
-  uint32_t at = page + lane * 128 + (((uint32_t)g << 5) ^ ((uint32_t)(lane & 7) << 4));
+  uint32_t code_at = raw + e2m1_code_offset(b0, lane);
+  const uint32_t lat = page + lane * 128, lat_sw = (uint32_t)(lane & 7) << 4;
+  const uint32_t rope = page + kRopeOff + lane * 64, rope_sw = (uint32_t)((lane >> 1) & 3) << 4;
   auto load = [&](ExpandUnit (&u)[2]) {
     expand_load(u[0], code_at, lut, exps[0]);
     expand_load(u[1], code_at + e2m1_code_offset(0, 32), lut, exps[1]);
-    exps[0] >>= 8;
-    exps[1] >>= 8;
-    code_at += e2m1_code_offset(4, 0);
+    exps[0] >>= 4;
+    exps[1] >>= 4;
+    code_at += e2m1_code_offset(1, 0);
   };
-  auto write = [&](const ExpandUnit (&u)[2]) {
+  auto write = [&](const ExpandUnit (&u)[2], int b) {
+    const bool is_rope = b >= kDLatent / kE2m1Block;
+    const uint32_t c = ((uint32_t)b & 3u) << 5;
+    const uint32_t at = is_rope ? rope + (c ^ rope_sw) : lat + (uint32_t)(b >> 2) * kLatBlock + (c ^ lat_sw);
     expand_write(u[0], at);
-    expand_write(u[1], at + 32 * 128);  // 32 rows on: the same swizzle
-    at += kLatBlock;
+    expand_write(u[1], at + (is_rope ? 32u * 64u : 32u * 128u));
   };
-  ExpandUnit even[2], odd[2];
-  load(even);
+  ExpandUnit cur[2];
+  load(cur);
 #pragma unroll 1
-  for (int i = 0; i < 4; i += 2) {
-    load(odd);
-    write(even);
-    if (i == 0) load(even);
-    else expand_load(even[0], raw + e2m1_code_offset(16 + (g >> 1), rt), lut, rope_exps >> (4 * (g >> 1)));
-    write(odd);
+  for (int i = 0; i < kPer; ++i) {
+    const ExpandUnit now[2] = {cur[0], cur[1]};
+    if (i + 1 < kPer) load(cur);
+    write(now, b0 + i);
   }
-  expand_write(even[0], page + kRopeOff + rt * 64 +
-                            (((uint32_t)(g >> 1) << 5) ^ ((uint32_t)((rt >> 1) & 3) << 4)));
 }
 
 // kGrouped: the grouped decode (GroupPlan): this CTA's shared-prefix range, then
 // its suffix range; otherwise mla_decode's single plan (Plan).
-// kE2m1: a 4-bit cache, expanded to e4m3 pages by four more warps; otherwise e4m3.
+// kE2m1: a 4-bit cache, expanded to e4m3 pages by six more warps; otherwise e4m3.
 template <bool kGrouped, bool kE2m1>
 __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
     decode_fp8_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap lat_map,
@@ -659,7 +654,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
       }
       __syncwarp();
     } else if (kE2m1 && warp >= kExpWarp0) {
-      // =================== expanders of a 4-bit cache (4 warps) ===================
+      // =================== expanders of a 4-bit cache (6 warps) ===================
       if constexpr (kE2m1) {
         bool ok = true;
         for (int64_t j = 0; j < npages; ++j) {
