@@ -105,6 +105,77 @@ combine_pieces_kernel(const int32_t* __restrict__ row_base, const int32_t* __res
   if (!ok && threadIdx.x == 0) atomicOr(status, MLA_DEVICE_ERR_TIMEOUT);
 }
 
+// The same merge where rows have few pieces: one warp per unit. A block per unit spends a
+// barrier sequence and a staging area on a piece or two there; here lane l keeps dims
+// 4l .. 4l + 3 of the unit's 128, and the weights of 32 pieces at a time (one a lane).
+// A whole decode call of 256 rows of 8 pages, 64 heads (65,536 units of 1.6 pieces), takes
+// 87 us with it and 178 with the blocks; 128 rows of 32 pages 81 and 140. The blocks' bulk
+// copies win for a row of many pieces, so the rule asks for 2.5 per row on average: with
+// 64 rows, one of 100k tokens and the others of one page, the two are even (117, 123 us);
+// with 32 such rows the blocks are ahead (125, 110).
+constexpr int kWarpMergeWarps = 8;
+constexpr int kWarpMergeLoads = 4;  // pieces whose loads are in flight (8: 95 us, 16: 168 on the 256 rows)
+__global__ void __launch_bounds__(32 * kWarpMergeWarps)
+combine_warps_kernel(const int32_t* __restrict__ row_base, const int32_t* __restrict__ row_np,
+                     const int32_t* __restrict__ piece_err, const float* __restrict__ part_lse,
+                     const float* __restrict__ part_out, int heads, int64_t units,
+                     __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = (int64_t)blockIdx.x * kWarpMergeWarps + (threadIdx.x >> 5);
+  if (unit >= units) return;
+  const int quarter = (int)(unit % kMergeQuarters);
+  const int64_t rh = unit / kMergeQuarters;
+  const int r = (int)(rh / heads), h = (int)(rh - (int64_t)r * heads);
+  const int np = __ldcg(row_np + r), base = __ldcg(row_base + r);
+  float m = -INFINITY, l_own = -INFINITY;
+  int bad = 0;
+  for (int s = lane; s < np; s += 32) {
+    const float l = __ldcg(part_lse + (int64_t)(base + s) * heads + h);
+    if (s == lane) l_own = l;
+    m = fmaxf(m, l);
+    bad |= __ldcg(piece_err + base + s);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const bool empty = np <= 0 || __any_sync(0xffffffffu, bad != 0) || !(m > -INFINITY);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float total = 0.f;
+  if (!empty) {
+    const float* src = part_out + ((int64_t)base * heads + h) * kDLatent + 128 * quarter + 4 * lane;
+    const int64_t step = (int64_t)heads * kDLatent;
+    for (int s0 = 0; s0 < np; s0 += 32) {
+      if (s0 > 0)
+        l_own = s0 + lane < np ? __ldcg(part_lse + (int64_t)(base + s0 + lane) * heads + h) : -INFINITY;
+      const float w_own = l_own > -INFINITY ? fast_exp2((l_own - m) * kLog2e) : 0.f;
+      const int n = min(32, np - s0);
+      for (int k0 = 0; k0 < n; k0 += kWarpMergeLoads) {
+        float4 v[kWarpMergeLoads];
+#pragma unroll
+        for (int k = 0; k < kWarpMergeLoads; ++k)
+          if (k0 + k < n) v[k] = __ldcg(reinterpret_cast<const float4*>(src + (s0 + k0 + k) * step));
+#pragma unroll
+        for (int k = 0; k < kWarpMergeLoads; ++k) {
+          if (k0 + k >= n) break;
+          const float w = __shfl_sync(0xffffffffu, w_own, k0 + k);
+          if (w == 0.f) continue;  // an empty piece: its slice may hold anything
+          acc.x += w * v[k].x; acc.y += w * v[k].y; acc.z += w * v[k].z; acc.w += w * v[k].w;
+          total += w;
+        }
+      }
+    }
+  }
+  const float inv = empty ? 0.f : 1.0f / total;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  uint2 packed;
+  packed.x = *reinterpret_cast<const uint32_t*>(&lo);
+  packed.y = *reinterpret_cast<const uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(out + rh * kDLatent + 128 * quarter + 4 * lane) = packed;
+  if (quarter == 0 && lane == 0) lse[rh] = empty ? -INFINITY : m + logf(total);
+}
+
 // Standalone merge: part_out [S][rows][512], part_lse [S][rows]; one block per row.
 __global__ void __launch_bounds__(kCombineThreads)
 combine_dense_kernel(const float* __restrict__ part_out, const float* __restrict__ part_lse,
@@ -121,7 +192,21 @@ combine_dense_kernel(const float* __restrict__ part_out, const float* __restrict
 cudaError_t launch_combine_pieces(const DecodeWorkspace& ws, int rows, int heads,
                                   int max_pieces_per_row, __nv_bfloat16* out, float* lse,
                                   cudaStream_t stream) {
-  const unsigned blocks = (unsigned)((int64_t)rows * heads * kMergeQuarters);
+  const int64_t units = (int64_t)rows * heads * kMergeQuarters;
+  const unsigned blocks = (unsigned)units;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  if ((int64_t)rows * 5 >= 2 * (int64_t)max_pieces_per_row) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((units + kWarpMergeWarps - 1) / kWarpMergeWarps));
+    cfg.blockDim = dim3(32 * kWarpMergeWarps);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, combine_warps_kernel, (const int32_t*)ws.row_base,
+                              (const int32_t*)ws.row_np, (const int32_t*)ws.piece_err,
+                              (const float*)ws.part_lse, (const float*)ws.part_out, heads, units,
+                              out, lse);
+  }
 
   static std::atomic<int> configured[64];
   int dev = 0;
@@ -139,7 +224,6 @@ cudaError_t launch_combine_pieces(const DecodeWorkspace& ws, int rows, int heads
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = (size_t)stage * kMergeSliceBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, combine_pieces_kernel, (const int32_t*)ws.row_base,
