@@ -394,7 +394,7 @@ MLA_API mla_status mla_kv_alloc(const int32_t* seq_lens, const int32_t* new_toke
  * [0, 1 - 2^-24] (NaN as 0). The acceptance test is exact; weights are summed as
  * integers in units of 2^-60 (a probability below 2^-37 is rounded to them),
  * so the result does not depend on the order of the sum. A row's probabilities
- * must sum to less than 16.
+ * must sum to less than 16 (beyond it the sums wrap: some token, or -1).
  *
  * target_probs  device, [batch][max_drafts + 1] rows of `vocab` probabilities,
  *               target_stride >= vocab elements apart

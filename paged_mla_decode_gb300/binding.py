@@ -173,15 +173,38 @@ def _page_size(kv_pages: torch.Tensor) -> int:
     return 64 if kv_pages.dim() == 2 else int(kv_pages.shape[1])
 
 
+_I32, _U32 = torch.int32, torch.uint32
+
+
+def _int32(device: int, *tensors) -> None:
+    """Each tensor is a contiguous int32 (for tags and status words also uint32) one on `device`."""
+    for t in tensors:
+        assert t.dtype is _I32 or t.dtype is _U32
+        assert t.is_contiguous() and t.get_device() == device
+
+
+def _device_of(t: torch.Tensor) -> int:
+    """The tensor's CUDA device, which must be the current one (the library launches there)."""
+    device = t.get_device()
+    assert t.is_cuda and device == torch.cuda.current_device()
+    return device
+
+
+def _same_device(device: int, *tensors) -> None:
+    """Each tensor is contiguous and on `device`: its pointer is all the library gets."""
+    for t in tensors:
+        assert t.is_contiguous() and t.get_device() == device
+
+
 def mla_kv_append(latent: torch.Tensor, rope: torch.Tensor, slot_mapping: torch.Tensor,
                   kv_pages: torch.Tensor, kv_scale: float, stream=None) -> None:
     """Write tokens' 512 latent + 64 rope elements into their cache slots."""
     num_tokens = int(slot_mapping.numel())
     assert latent.dtype == torch.bfloat16 and rope.dtype == torch.bfloat16
     assert slot_mapping.dtype == torch.int32
-    assert latent.is_contiguous() and rope.is_contiguous()
     assert latent.shape == (num_tokens, 512) and rope.shape == (num_tokens, 64)
     dtype = kv_dtype_code(kv_pages)
+    _same_device(_device_of(kv_pages), latent, rope, slot_mapping)
     st = load_library().mla_kv_append(_ptr(latent), _ptr(rope), _ptr(slot_mapping), num_tokens,
                                       _ptr(kv_pages), int(kv_pages.shape[0]),
                                       _page_size(kv_pages), dtype,
@@ -211,6 +234,7 @@ def mla_decode(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tenso
     assert out.dtype == torch.bfloat16 and tuple(out.shape) == (batch, nq, heads, 512)
     assert lse.dtype == torch.float32 and tuple(lse.shape) == (batch, nq, heads)
     dtype = kv_dtype_code(kv_pages)
+    _same_device(_device_of(kv_pages), q, block_table, seq_lens, out, lse, workspace)
     lib = load_library()
     fn = lib.mla_decode_f16_operands if f16_operands else lib.mla_decode
     st = fn(
@@ -242,6 +266,7 @@ def mla_decode_grouped(q: torch.Tensor, kv_pages: torch.Tensor, block_table: tor
     assert out.dtype == torch.bfloat16 and tuple(out.shape) == (batch, nq, heads, 512)
     assert lse.dtype == torch.float32 and tuple(lse.shape) == (batch, nq, heads)
     dtype = kv_dtype_code(kv_pages)
+    _same_device(_device_of(kv_pages), q, block_table, seq_lens, out, lse, workspace)
     st = load_library().mla_decode_grouped(
         _ptr(q), _ptr(kv_pages), int(kv_pages.shape[0]), _page_size(kv_pages),
         dtype, _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
@@ -292,23 +317,6 @@ def mla_kv_check(page_tags: torch.Tensor, block_table: torch.Tensor,
                                      _ptr(request_status), _ptr(checked_seq_lens),
                                      _stream(stream))
     _check(st, "mla_kv_check")
-
-
-_I32, _U32 = torch.int32, torch.uint32
-
-
-def _int32(device: int, *tensors) -> None:
-    """Each tensor is a contiguous int32 (for tags and status words also uint32) one on `device`."""
-    for t in tensors:
-        assert t.dtype is _I32 or t.dtype is _U32
-        assert t.is_contiguous() and t.get_device() == device
-
-
-def _device_of(t: torch.Tensor) -> int:
-    """The tensor's CUDA device, which must be the current one (the library launches there)."""
-    device = t.get_device()
-    assert t.is_cuda and device == torch.cuda.current_device()
-    return device
 
 
 def mla_kv_gather(kv_pages: torch.Tensor, kv_scale: float, block_table: torch.Tensor,
@@ -464,6 +472,7 @@ def mla_decode_static_scratch(q: torch.Tensor, kv_pages: torch.Tensor,
     assert out.dtype == torch.bfloat16 and tuple(out.shape) == (batch, nq, heads, 512)
     assert lse.dtype == torch.float32 and tuple(lse.shape) == (batch, nq, heads)
     dtype = kv_dtype_code(kv_pages)
+    _same_device(_device_of(kv_pages), q, block_table, seq_lens, out, lse)
     if device_status is not None:
         assert device_status.dtype == torch.int32 and device_status.numel() >= 1
     st = load_library().mla_decode_static_scratch(

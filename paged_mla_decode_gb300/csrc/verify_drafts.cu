@@ -237,6 +237,8 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kBlocksPerSm)
   }
   __syncthreads();
   const int a = s_row;
+  // -1 unless some block finds the border; that block's store comes after the barrier below
+  if (rank == 0 && tid == 0) out[a] = -1;
   const bool rejected = a < drafts;
   Rest<T> rest{target + a * p.target_stride,
                rejected && draft ? draft + a * p.draft_stride : nullptr,
@@ -272,7 +274,6 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kBlocksPerSm)
     for (int i = tid; i <= K; i += kVerifyThreads)
       if (i != a) out[i] = i < a ? tokens[i] : -1;
     if (tid == 0) {
-      if (total == 0) out[a] = -1;
       p.accepted[b] = a;
       if (p.seq_lens_out) p.seq_lens_out[b] = L - (drafts - a);
     }

@@ -103,6 +103,12 @@ def test_binding_refuses_what_the_library_cannot_see():
                              i32(1))
     with pytest.raises(AssertionError):
         binding.mla_verify_drafts(torch.zeros(1, 2, 5), None, i32(1, 1), torch.zeros(1, 2), i32(1, 2), i32(1))
+    bf = lambda *s: torch.zeros(s).bfloat16()  # noqa: E731
+    with pytest.raises(AssertionError):
+        binding.mla_kv_append(bf(3, 512), bf(3, 64), i32(3), page, 1.0)
+    with pytest.raises(AssertionError):
+        binding.mla_decode(bf(1, 1, 16, 576), page, i32(1, 2), i32(1), 0.1, 1.0, bf(1, 1, 16, 512), torch.zeros(1, 1, 16),
+                           torch.zeros(9, dtype=torch.uint8))
     probs = torch.zeros(2, 3, 10)
     assert binding._row_stride(probs) == 10 and binding._row_stride(probs[..., :7]) == 10
     assert binding._row_stride(probs[:, :1]) == 30
