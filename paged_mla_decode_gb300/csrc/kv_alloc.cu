@@ -50,45 +50,50 @@ struct AllocParams {
   uint32_t* status;
 };
 
-// Inclusive running sums of two values over the block's threads, in place; every thread
-// also gets the totals.
+// Running sums saturate at 2^31 - 1, past every row and page there can be: sums of
+// non-negative numbers that saturate are still associative, and 32 bits suffice.
+constexpr uint32_t kMost = 0x7fffffffu;
 struct Pair {
-  int64_t x, y;
+  uint32_t x, y;
 };
-__device__ __forceinline__ Pair block_scan(Pair& v, Pair* warp_sum, int warps) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ Pair plus(Pair a, Pair b) {
+  return Pair{min(a.x + b.x, kMost), min(a.y + b.y, kMost)};
+}
+__device__ __forceinline__ Pair warp_scan(Pair v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t a = __shfl_up_sync(0xffffffffu, v.x, o), b = __shfl_up_sync(0xffffffffu, v.y, o);
-    if (lane >= o) v.x += a, v.y += b;
+    const Pair u{__shfl_up_sync(0xffffffffu, v.x, o), __shfl_up_sync(0xffffffffu, v.y, o)};
+    if (lane >= o) v = plus(v, u);
   }
+  return v;
+}
+// Inclusive running sums over the block's threads, in place; returns the totals.
+__device__ __forceinline__ Pair block_scan(Pair& v, Pair* warp_sum, int warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_scan(v, lane);
   if (lane == 31) warp_sum[warp] = v;
   __syncthreads();
   // every warp scans the warps' sums
-  Pair s = lane < warps ? warp_sum[lane] : Pair{0, 0};
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t a = __shfl_up_sync(0xffffffffu, s.x, o), b = __shfl_up_sync(0xffffffffu, s.y, o);
-    if (lane >= o) s.x += a, s.y += b;
-  }
-  const int64_t px = __shfl_sync(0xffffffffu, s.x, max(warp - 1, 0));
-  const int64_t py = __shfl_sync(0xffffffffu, s.y, max(warp - 1, 0));
-  if (warp > 0) v.x += px, v.y += py;
+  const Pair s = warp_scan(lane < warps ? warp_sum[lane] : Pair{0, 0}, lane);
+  const int last = max(warp - 1, 0);
+  const Pair before{__shfl_sync(0xffffffffu, s.x, last), __shfl_sync(0xffffffffu, s.y, last)};
+  if (warp > 0) v = plus(v, before);
   const Pair total{__shfl_sync(0xffffffffu, s.x, 31), __shfl_sync(0xffffffffu, s.y, 31)};
   __syncthreads();  // the sums are no longer read
   return total;
 }
 
+// What the rows of a chunk's requests need.
 struct AllocShared {
   Pair warp_sum[kAllocWarps];
-  int64_t row_end[kAllocThreads];     // rows of the chunk's requests, ends
-  int64_t first_page[kAllocThreads];  // pages taken before each
-  int32_t len[kAllocThreads];         // cached tokens; -1: refused
-  int32_t held[kAllocThreads];
+  int32_t row_end[kAllocThreads];  // rows up to and with the request
+  int32_t shift[kAllocThreads];    // token of row x = x + shift
+  int32_t held[kAllocThreads];     // -1: refused
+  int32_t fresh[kAllocThreads];    // page held + k = free_pages[fresh - k]
 };
 
 // First i < n with end[i] > x (n if there is none).
-__device__ __forceinline__ int first_after(const int64_t* end, int n, int64_t x) {
+__device__ __forceinline__ int first_after(const int32_t* end, int n, int32_t x) {
   int lo = 0, hi = n;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -98,111 +103,133 @@ __device__ __forceinline__ int first_after(const int64_t* end, int n, int64_t x)
   return lo;
 }
 
-__device__ __forceinline__ int64_t pages_for(int64_t tokens) {
-  return (tokens + kPageSize - 1) / kPageSize;
+__device__ __forceinline__ int32_t pages_for(uint32_t tokens) {
+  return (int32_t)(tokens / kPageSize + (tokens % kPageSize != 0));
 }
 
-// kFill: rows [blockIdx.x * rows_per, + rows_per) of the slot map, with the new pages that
-// begin there. kCommit: block 0 writes the per-request outputs, which may be the inputs:
+// kFill: rows [blockIdx.x * rows_per, + rows_per) of the slot map (kRows a thread at a
+// time), with the new pages that begin there. kCommit: block 0 writes the per-request outputs, which may be the inputs:
 // then no other block may still read them (one block in all, or a launch of its own).
-template <bool kFill, bool kCommit>
+template <bool kFill, bool kCommit, int kRows>
 __global__ void __launch_bounds__(kAllocThreads)
-    kv_alloc_kernel(const AllocParams p, const int64_t rows_per, const int warp_rows) {
+    kv_alloc_kernel(const AllocParams p, const int64_t rows_per) {
+  constexpr int kWarpRows = 32 * kRows;  // rows a warp fills per bisection
   __shared__ AllocShared sm;
   const int threads = blockDim.x, warps = threads >> 5;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool commit = kCommit && blockIdx.x == 0;
-  const int64_t lo = blockIdx.x * rows_per, hi = min(lo + rows_per, p.num_slots);
-  const int64_t count = min(max((int64_t)p.free_count[0], (int64_t)0), p.free_capacity);
-  int64_t row0 = 0, page0 = 0, taken = 0;  // rows, pages asked for and pages taken so far
+  const int32_t lo = (int32_t)min((int64_t)blockIdx.x * rows_per, p.num_slots);
+  const int32_t hi = (int32_t)min((int64_t)lo + rows_per, p.num_slots);
+  const int32_t count = min(max(p.free_count[0], 0), (int32_t)p.free_capacity);
+  Pair done{0, 0};    // rows, and pages asked for, of the requests so far
+  uint32_t taken = 0;  // pages taken so far
   for (int b0 = 0; b0 < p.batch; b0 += threads) {
     const int b = b0 + tid;
     const bool live = b < p.batch;
-    const int L = live ? p.seq_lens[b] : 0, held = live ? p.held[b] : 0;
-    const int asked = live ? p.new_tokens[b] : 0;
-    const int64_t n = max(asked, 0);
+    const int32_t L = live ? p.seq_lens[b] : 0, held = live ? p.held[b] : 0;
+    const int32_t asked = live ? p.new_tokens[b] : 0;
+    const uint32_t n = (uint32_t)max(asked, 0);
+    const int32_t fits = pages_for((uint32_t)L + n);
     uint32_t st = 0;
-    if (L < 0 || asked < 0 || held < 0 || held > p.max_pages || pages_for(L) > held)
+    if (L < 0 || asked < 0 || held < 0 || held > p.max_pages || pages_for((uint32_t)L) > held)
       st = MLA_KV_ALLOC_BAD_LENGTH;
-    else if (pages_for(L + n) > p.max_pages) st = MLA_KV_ALLOC_TABLE_FULL;
-    int64_t need = live && st == 0 ? max(pages_for(L + n) - held, (int64_t)0) : 0;
+    else if (fits > p.max_pages) st = MLA_KV_ALLOC_TABLE_FULL;
+    uint32_t need = live && st == 0 ? (uint32_t)max(fits - held, 0) : 0u;
     Pair ends{n, need};  // rows and pages up to and with this request
     Pair sums = block_scan(ends, sm.warp_sum, warps);
-    const int64_t rows = sums.x, row_end = row0 + ends.x;
-    if (row0 + rows > p.num_slots) {  // some request's rows do not fit: it asks for no page
-      if (st == 0 && row_end > p.num_slots) st = MLA_KV_ALLOC_SLOTS_FULL;
+    const Pair now = plus(done, sums);
+    const uint32_t row_end = plus(done, ends).x, row_all = now.x;
+    if (now.x > (uint32_t)p.num_slots) {  // some request's rows do not fit: it asks for no page
+      if (st == 0 && row_end > (uint32_t)p.num_slots) st = MLA_KV_ALLOC_SLOTS_FULL;
       if (st != 0) need = 0;
       ends = Pair{0, need};
       sums = block_scan(ends, sm.warp_sum, warps);
     }
-    const int64_t pages = sums.y, page_end = page0 + ends.y;
-    if (need > 0 && page_end > count) st = MLA_KV_ALLOC_NO_PAGES;
+    const uint32_t page_end = plus(done, ends).y;
+    if (need > 0 && page_end > (uint32_t)count) st = MLA_KV_ALLOC_NO_PAGES;
     if constexpr (kFill) {
-      sm.row_end[tid] = row_end;
-      sm.first_page[tid] = page_end - need;
-      sm.len[tid] = st == 0 ? L : -1;
-      sm.held[tid] = held;
+      sm.row_end[tid] = (int32_t)row_end;
+      sm.shift[tid] = (int32_t)((uint32_t)L - (row_end - n));
+      sm.held[tid] = st == 0 ? held : -1;
+      sm.fresh[tid] = (int32_t)((uint32_t)count - 1u - (page_end - need));
     }
     if (commit) {
       const bool grown = need > 0 && st == 0;
       if (live) {
-        p.seq_lens_out[b] = st == 0 ? (int32_t)(L + n) : -1;
+        p.seq_lens_out[b] = st == 0 ? (int32_t)((uint32_t)L + n) : -1;
         p.held_out[b] = held + (grown ? (int32_t)need : 0);
         p.status[b] = st;
-        p.cu[b + 1] = (int32_t)min(row_end, (int64_t)0x7fffffff);
+        p.cu[b + 1] = (int32_t)row_end;
       }
       // the requests that got pages come before those that got none: the sum only grows
-      int64_t got = grown ? page_end : 0;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) got = max(got, __shfl_xor_sync(0xffffffffu, got, o));
+      const uint32_t got = __reduce_max_sync(0xffffffffu, grown ? page_end : 0u);
       if (lane == 0) sm.warp_sum[warp].x = got;
     }
     __syncthreads();
     if (commit)
-      for (int w = 0; w < warps; ++w) taken = max(taken, sm.warp_sum[w].x);
+      taken = max(taken, __reduce_max_sync(0xffffffffu, lane < warps ? sm.warp_sum[lane].x : 0u));
     if constexpr (kFill) {
       const int nb = min(threads, p.batch - b0);
-      const int64_t x_end = min(row0 + rows, hi);
-      for (int64_t x0 = lo + (int64_t)warp * warp_rows; x0 < x_end; x0 += warps * warp_rows) {
-        if (x0 + warp_rows <= row0) continue;  // (rows of an earlier chunk)
-        int i = first_after(sm.row_end, nb, max(x0, row0));
-        for (int k = 0; k < warp_rows; k += 32) {
-          const int64_t x = x0 + k + lane;
-          if (x < row0 || x >= x_end) continue;
-          while (sm.row_end[i] <= x) ++i;
-          int64_t slot = -1;
-          const int len = sm.len[i], held_i = sm.held[i];
-          if (len >= 0) {
-            const int64_t pos = len + x - (i > 0 ? sm.row_end[i - 1] : row0);
-            const int j = (int)(pos / kPageSize), off = (int)(pos % kPageSize);
-            const int64_t at = (int64_t)(b0 + i) * p.max_pages + j;
-            const bool fresh = j >= held_i;
-            const int32_t page =
-                fresh ? p.free_pages[count - 1 - sm.first_page[i] - (j - held_i)] : p.block_table[at];
-            const bool in_cache = page >= 0 && page < p.num_pages;
-            if (in_cache) slot = (int64_t)page * kPageSize + off;
-            if (fresh && off == 0) {  // a page held before covers every cached token
-              p.block_table[at] = page;
-              if (p.page_tags != nullptr && in_cache) {
-                const uint32_t tag = p.page_tags[page] + 1;
-                p.page_tags[page] = tag;
-                p.expected_tags[at] = tag;
-              }
-            }
+      const int32_t from = (int32_t)done.x, to = min((int32_t)row_all, hi);
+      for (int32_t x0 = lo + warp * kWarpRows; x0 < to; x0 += warps * kWarpRows) {
+        if (x0 + kWarpRows <= from) continue;  // (rows of an earlier chunk)
+        int i = first_after(sm.row_end, nb, max(x0, from));
+        // most runs lie in one request: its data is then read once
+        const bool whole = i < nb && sm.row_end[i] >= min(x0 + kWarpRows, to);
+        int32_t held_i = whole ? sm.held[i] : -1, shift = sm.shift[i % kAllocThreads];
+        int32_t fresh = sm.fresh[i % kAllocThreads];
+        // all of a thread's page ids are asked for before the first is used, then all tags
+        int32_t page[kRows], off[kRows];
+        int64_t at[kRows];  // block-table entry of a new page's first token, else -1
+        uint32_t tag[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          const int32_t x = x0 + 32 * k + lane;
+          page[k] = -1;
+          off[k] = 0;
+          at[k] = -1;
+          if (x < from || x >= to) continue;
+          if (!whole) {
+            while (sm.row_end[i] <= x) ++i;
+            held_i = sm.held[i];
+            shift = sm.shift[i];
+            fresh = sm.fresh[i];
           }
-          p.slots[x] = (int32_t)slot;
+          if (held_i < 0) continue;
+          const int32_t pos = x + shift, j = pos / kPageSize;
+          const int64_t entry = (int64_t)(b0 + i) * p.max_pages + j;
+          off[k] = pos % kPageSize;
+          page[k] = j < held_i ? p.block_table[entry] : p.free_pages[fresh - (j - held_i)];
+          // (a page held before covers every cached token: a new one starts at its token 0)
+          if (j >= held_i && off[k] == 0) at[k] = entry;
         }
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          const bool in_cache = page[k] >= 0 && page[k] < (int32_t)p.num_pages;
+          if (at[k] >= 0) {
+            p.block_table[at[k]] = page[k];
+            if (p.page_tags == nullptr || !in_cache) at[k] = -1;
+            else tag[k] = p.page_tags[page[k]] + 1;
+          }
+          const int32_t x = x0 + 32 * k + lane;
+          if (x >= from && x < to) p.slots[x] = in_cache ? page[k] * kPageSize + off[k] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kRows; ++k)
+          if (at[k] >= 0) {
+            p.page_tags[page[k]] = tag[k];
+            p.expected_tags[at[k]] = tag[k];
+          }
       }
     }
-    row0 += rows;
-    page0 += pages;
+    done = Pair{row_all, plus(done, sums).y};
     __syncthreads();
   }
   if constexpr (kFill)
-    for (int64_t x = max(row0, lo) + tid; x < hi; x += threads) p.slots[x] = -1;
+    for (int32_t x = max((int32_t)done.x, lo) + tid; x < hi; x += threads) p.slots[x] = -1;
   if (commit && tid == 0) {
     p.cu[0] = 0;
-    p.free_count_out[0] = (int32_t)(count - taken);
+    p.free_count_out[0] = count - (int32_t)taken;
   }
 }
 
@@ -228,7 +255,8 @@ extern "C" mla_status mla_kv_alloc(const int32_t* seq_lens, const int32_t* new_t
   if (batch < 0 || free_capacity < 0 || num_pages < 0 || max_pages < 1 || num_slots < 0)
     return MLA_ERR_INVALID_ARG;
   if (page_size != kPageSize) return MLA_ERR_UNSUPPORTED;
-  if (num_pages > 0x7fffffff / kPageSize || num_slots > 0x7fffffffLL ||
+  if (num_pages > 0x7fffffff / kPageSize || num_slots > 0x7fff0000LL ||
+      free_capacity > 0x7fff0000LL ||  // (sums and runs of rows end below 2^31)
       max_pages > 0x7fffffff / kPageSize)
     return MLA_ERR_UNSUPPORTED;
   if (!free_count || !free_count_out || !cu_tokens) return MLA_ERR_INVALID_ARG;
@@ -254,7 +282,8 @@ extern "C" mla_status mla_kv_alloc(const int32_t* seq_lens, const int32_t* new_t
   blocks = std::max<int64_t>(blocks, 1);
   // A warp bisects once per 128 rows, in a step of a few rows a request once per 32; one
   // block has the threads that its requests and rows keep busy.
-  const int warp_rows = num_slots > kAllocThreads ? 128 : 32;
+  const bool many = num_slots > kAllocThreads;
+  const int warp_rows = many ? 128 : 32;
   const int64_t rows_per = ((num_slots + blocks - 1) / blocks + warp_rows - 1) / warp_rows * warp_rows;
   int threads = 128;
   while (threads < kAllocThreads && (blocks > 1 || threads < std::max<int64_t>(batch, num_slots)))
@@ -267,11 +296,10 @@ extern "C" mla_status mla_kv_alloc(const int32_t* seq_lens, const int32_t* new_t
   for (int i = 0; i < 4; ++i)
     for (int o = 0; o < 5; ++o)
       apart = apart && !overlap(ins[i], i == 3 ? 1 : batch, outs[o], o == 2 ? 1 : batch + (o == 3));
-  if (blocks == 1 || apart) {
-    kv_alloc_kernel<true, true><<<(unsigned)blocks, threads, 0, s>>>(p, rows_per, warp_rows);
-  } else {
-    kv_alloc_kernel<true, false><<<(unsigned)blocks, threads, 0, s>>>(p, rows_per, warp_rows);
-    kv_alloc_kernel<false, true><<<1, threads, 0, s>>>(p, rows_per, warp_rows);
-  }
+  const bool at_once = blocks == 1 || apart;
+  const auto fill = at_once ? (many ? kv_alloc_kernel<true, true, 4> : kv_alloc_kernel<true, true, 1>)
+                            : kv_alloc_kernel<true, false, 4>;
+  fill<<<(unsigned)blocks, threads, 0, s>>>(p, rows_per);
+  if (!at_once) kv_alloc_kernel<false, true, 1><<<1, threads, 0, s>>>(p, rows_per);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
