@@ -1138,7 +1138,8 @@ __global__ void __launch_bounds__(kSplitThreads)
   griddep_launch_dependents();
   __shared__ unsigned s_amax[kSplitHeads];
   const int tid = threadIdx.x;
-  const int hl = tid / kQOpChunks, u = tid - hl * kQOpChunks;
+  // neighbouring threads take neighbouring heads: their codes lie beside each other
+  const int hl = tid % kSplitHeads, u = tid / kSplitHeads;
   const int groups = (heads + kSplitHeads - 1) / kSplitHeads;
   const int64_t row = blockIdx.x / groups;
   const int h = (int)(blockIdx.x - row * groups) * kSplitHeads + hl;
