@@ -23,16 +23,16 @@
 // serve trillions of tokens ...", section "First, understand the workload").
 //
 // A 4-bit cache (kv_e2m1.cuh) takes the same path (kE2m1): its pages land in a second,
-// smaller ring as stored, six expander warps rewrite each as the swizzled e4m3 page
+// smaller ring as stored, seven expander warps rewrite each as the swizzled e4m3 page
 // that the contractions read (a table lookup, exact), and everything after that is
 // the e4m3 kernel. It trades one ring slot for the raw pages (kRing 4 + 2 raw). 31
-// requests of 60k-140k tokens with 64 heads (307 pages a CTA) take 438 us, 413 without
-// the expansion, 368 from an e4m3 cache, whose softmax has more registers. What is left
+// requests of 60k-140k tokens with 64 heads (307 pages a CTA) take 429 us, 413 without
+// the expansion, 366 from an e4m3 cache, whose softmax has more registers. What is left
 // is shared-memory bandwidth above all: a page's MMAs read 140 KB of operands (V twice,
 // for P's two terms), the P buffers and page copies move 35 KB, the expansion reads and
 // writes another 55 KB: 1,800 cycles at 128 B a cycle, of some 2,300 that a page takes.
 //
-// Warp roles (416 threads; 608 with the expanders):
+// Warp roles (416 threads; 640 with the expanders):
 //   warps 0-7  q loading, softmax and epilogue. Row t of A and S is (head
 //              16*(t/32) + t%16, part (t/16)%2), part 0 = hi, 1 = lo. Warp w reads
 //              TMEM lanes 32*(w%4) .. +31; thread (w, lane) handles head
@@ -46,7 +46,7 @@
 //              (128-byte swizzled latent blocks, 64-byte swizzled rope block).
 //   warps 9-10 issue QK of even / odd pages (lane 0); warp 9 allocates TMEM.
 //   warps 11-12 issue PV of even / odd pages (lane 0).
-//   warps 13-18 (4-bit cache only) expand raw pages into the ring. More than 20 warps
+//   warps 13-19 (4-bit cache only) expand raw pages into the ring. More than 20 warps
 //              would leave a thread 80 registers, with which the softmax takes twice as
 //              long; up to 20 it has 96.
 // A thread that issues MMAs stalls for a while after each batch (until the
@@ -91,7 +91,7 @@ constexpr int kTmaWarp = kSmWarps;                   // 8
 constexpr int kQkWarp0 = kSmWarps + 1;               // 9: also allocates TMEM
 constexpr int kPvWarp0 = kSmWarps + 3;               // 11
 constexpr int kExpWarp0 = kSmWarps + 5;              // 13: expanders of a 4-bit cache
-constexpr int kExpWarps = 6;
+constexpr int kExpWarps = 7;
 constexpr int kPageBytes = kPageSize * kDEntry;      // 36864
 constexpr int kLatBlock = kPageSize * 128;           // 8192: 64 rows x 128 dims
 constexpr int kRopeOff = 4 * kLatBlock;              // rope block within a page slot
@@ -127,7 +127,7 @@ constexpr int kTableAhead = 32;  // pages described (block-table read started) b
 // Shared memory map (offsets from a 1024-aligned base) and barriers.
 template <bool kE2m1>
 struct Map {
-  static constexpr int kThreads = 32 * (kE2m1 ? kExpWarp0 + kExpWarps : kSmWarps + 5);  // 608, 416
+  static constexpr int kThreads = 32 * (kE2m1 ? kExpWarp0 + kExpWarps : kSmWarps + 5);  // 640, 416
   static constexpr int kRing = kE2m1 ? 4 : 5;          // e4m3 pages in flight
   static constexpr int kRawRing = kE2m1 ? 2 : 0;       // 4-bit pages in flight
   static constexpr int kOffPages = 0;
@@ -344,12 +344,13 @@ __device__ const uint64_t kE2m1Lut[16] = {
     e2m1_as_e4m3(8),  e2m1_as_e4m3(9),  e2m1_as_e4m3(10), e2m1_as_e4m3(11),
     e2m1_as_e4m3(12), e2m1_as_e4m3(13), e2m1_as_e4m3(14), e2m1_as_e4m3(15)};
 
-// One expander warp's share of a page: blocks 3e .. 3e + 2 of every token, two tokens
-// (lane, lane + 32) a thread. Beside the other roles a warp gets an instruction every four
-// to five cycles, whatever its code, so six warps share the page (31 requests as above:
-// 438 us; four with nine blocks a thread 485, three with twelve 493). The next block's
-// loads and table rows are in flight while a block is written. Not unrolled: the roles'
-// loops share the instruction cache (457 us unrolled).
+// One expander warp's share of a page: three blocks of every token (warps e = 0..3) or two
+// (e = 4..6), two tokens (lane, lane + 32) a thread. Beside the other roles a warp gets an
+// instruction every four to six cycles whatever its code, so seven warps share the page,
+// and the three schedulers with two of them have five blocks each, the one with one warp
+// three. 31 requests as above: 429 us; six warps 439, four 485, three 493. The loop is
+// short because the roles' loops share the instruction cache: unrolled 457, with the next
+// block's loads in flight (a register copy more) 432.
 struct ExpandUnit {
   uint4 codes;
   uint2 row;  // of the expansion table
@@ -376,14 +377,14 @@ __device__ __forceinline__ void expand_write(const ExpandUnit& u, uint32_t at) {
 }
 __device__ __forceinline__ void expand_page(uint32_t raw, uint32_t page, uint32_t lut, int e,
                                             int lane) {
-  constexpr int kPer = kE2m1Blocks / kExpWarps;  // 3
-  const int b0 = kPer * e;
+  const int b0 = e < 4 ? 3 * e : 4 + 2 * e, blocks = e < 4 ? 3 : 2;
   uint32_t exps[2];  // the blocks' nibbles, the first lowest
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    uint32_t x, y;
-    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(x) : "r"(raw + e2m1_exp_offset(b0, lane + 32 * k)));
-    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(y) : "r"(raw + e2m1_exp_offset(b0 + 2, lane + 32 * k)));
+    const uint32_t at = raw + e2m1_exp_offset(b0, lane + 32 * k);
+    uint32_t x, y = 0;
+    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(x) : "r"(at));
+    if ((b0 & 1) + blocks > 2) asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(y) : "r"(at + kPageSize));
     exps[k] = (x + (y << 8)) >> (4 * (b0 & 1));
   }
   uint32_t code_at = raw + e2m1_code_offset(b0, lane);
@@ -403,19 +404,17 @@ __device__ __forceinline__ void expand_page(uint32_t raw, uint32_t page, uint32_
     expand_write(u[0], at);
     expand_write(u[1], at + (is_rope ? 32u * 64u : 32u * 128u));
   };
-  ExpandUnit cur[2];
-  load(cur);
 #pragma unroll 1
-  for (int i = 0; i < kPer; ++i) {
-    const ExpandUnit now[2] = {cur[0], cur[1]};
-    if (i + 1 < kPer) load(cur);
-    write(now, b0 + i);
+  for (int i = 0; i < blocks; ++i) {
+    ExpandUnit u[2];
+    load(u);
+    write(u, b0 + i);
   }
 }
 
 // kGrouped: the grouped decode (GroupPlan): this CTA's shared-prefix range, then
 // its suffix range; otherwise mla_decode's single plan (Plan).
-// kE2m1: a 4-bit cache, expanded to e4m3 pages by six more warps; otherwise e4m3.
+// kE2m1: a 4-bit cache, expanded to e4m3 pages by seven more warps; otherwise e4m3.
 template <bool kGrouped, bool kE2m1>
 __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
     decode_fp8_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap lat_map,
@@ -654,7 +653,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
       }
       __syncwarp();
     } else if (kE2m1 && warp >= kExpWarp0) {
-      // =================== expanders of a 4-bit cache (6 warps) ===================
+      // =================== expanders of a 4-bit cache (7 warps) ===================
       if constexpr (kE2m1) {
         bool ok = true;
         for (int64_t j = 0; j < npages; ++j) {
