@@ -120,20 +120,6 @@ __host__ __device__ constexpr uint64_t e2m1_as_e4m3(int n) {
   return row;
 }
 
-// For n = 3 .. 14 every magnitude but 0 is a normal e4m3 number times 2^(n - 8), and its
-// code is linear in n: the table row (bytes 0, 8n - 16, 8n - 8, 8n - 4 | 8n, 8n + 4,
-// 8n + 8, 8n + 12) costs two multiply-adds instead of a shared-memory read.
-__device__ __forceinline__ void e2m1_linear_row(uint32_t n, uint32_t& lo, uint32_t& hi) {
-  lo = n * 0x08080800u - 0x04081000u;
-  hi = n * 0x08080808u + 0x0c080400u;
-}
-// Whether the low nibbles of all four bytes lie in 3 .. 14: n + 13 carries into bit 4
-// from n = 3 on, n + 1 at n = 15 only.
-__device__ __forceinline__ bool e2m1_all_linear(uint32_t nibbles) {
-  const uint32_t m = nibbles & 0x0f0f0f0fu;
-  return ((m + 0x0d0d0d0du) & ~(m + 0x01010101u) & 0x10101010u) == 0x10101010u;
-}
-
 // Eight e2m1 codes (nibble i = element i) -> eight e4m3 codes, given the block's table
 // row (lo: magnitudes 0..3, hi: 4..7): nine instructions. A byte permute looks up four
 // magnitudes at once; the signs are the top bits of w's bytes (odd elements) and of
