@@ -78,17 +78,128 @@ __device__ __forceinline__ void merge_row(const float* __restrict__ out_base, in
   if (tid == 0) *lse_out = empty ? -INFINITY : m + logf(total);
 }
 
-// Merge of mla_decode's pieces: one block of kMergeThreads per unit (row, head,
-// quarter of the 512 dims), see merge_unit.
-__global__ void __launch_bounds__(kMergeThreads)
-combine_pieces_kernel(const int32_t* __restrict__ row_base, const int32_t* __restrict__ row_np,
-                      const int32_t* __restrict__ piece_err, const float* __restrict__ part_lse,
-                      const float* __restrict__ part_out, int heads,
-                      __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
-                      unsigned* __restrict__ status, int stage_pieces) {
-  // launched as a dependent of the decode kernel: its partials are visible after this
-  griddep_wait();
-  griddep_launch_dependents();
+// ---- merge of a decode's pieces ----
+// Units are (row, head, quarter of the 512 dims). With few rows each may have many pieces,
+// and every unit is merged by a block (merge_unit: the slices staged by bulk copies).
+// Otherwise only the rows of more than kFewPieces pieces are, of which there are at most
+// `many_rows` (every CTA's range cuts one row at most), and the other units take a warp
+// each: a block would spend its barriers and its staging on a few pieces there. The grid
+// then starts with the blocks of the rows of many pieces; each looks for its row in the
+// row table and leaves if there is none. A decode call of 256 rows of 8 pages, 64 heads,
+// takes 84 us, with a block per unit throughout 178; 48 rows of one page 28 and 42; one
+// row of 100k tokens among 31 of one page 101 and 110. For the few rows the first kernel
+// stays: it has 32 registers a thread, the second 52 (8 rows of 20k tokens 47 us, 53).
+constexpr int kFewPieces = 16;
+constexpr int kWarpMergeLoads = 4;  // pieces whose loads are in flight (8: 95 us, 16: 168 on the 256 rows)
+
+struct MergeParams {
+  const int32_t* row_base;
+  const int32_t* row_np;
+  const int32_t* piece_err;
+  const float* part_lse;
+  const float* part_out;
+  int rows, heads;
+  int64_t units;
+  unsigned many_blocks;  // blocks for rows of many pieces, before the others
+  __nv_bfloat16* out;
+  float* lse;
+  unsigned* status;
+  int stage_pieces;
+};
+
+// Row number k (from 0) among those of more than kFewPieces pieces; -1 if there are fewer.
+// All threads of the block call it; 128 rows a warp at a time.
+__device__ __forceinline__ int find_row_of_many(const MergeParams& p, int k) {
+  __shared__ int s_count[kMergeWarps];
+  __shared__ int s_found;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) s_found = -1;
+  for (int r0 = 0; r0 < p.rows; r0 += 128 * kMergeWarps) {
+    unsigned many[4];
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = r0 + 128 * warp + 32 * j + lane;
+      many[j] = __ballot_sync(0xffffffffu, r < p.rows && __ldcg(p.row_np + min(r, p.rows - 1)) > kFewPieces);
+      count += __popc(many[j]);
+    }
+    if (lane == 0) s_count[warp] = count;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < kMergeWarps; ++w) {
+      if (w < warp) before += s_count[w];
+      all += s_count[w];
+    }
+    int left = k - before;
+    if (left >= 0 && left < count && lane == 0) {
+      for (int j = 0; j < 4; ++j) {
+        const int n = __popc(many[j]);
+        if (left < n) {
+          s_found = r0 + 128 * warp + 32 * j + (int)__fns(many[j], 0, left + 1);
+          break;
+        }
+        left -= n;
+      }
+    }
+    __syncthreads();
+    if (s_found >= 0 || k < all) break;
+    k -= all;
+  }
+  return s_found;
+}
+
+// One unit by one warp: lane l keeps dims 4l .. 4l + 3 of its 128, and the weight of one of
+// 32 pieces at a time.
+__device__ __forceinline__ void merge_unit_by_warp(const MergeParams& p, int64_t unit, int lane) {
+  const int quarter = (int)(unit % kMergeQuarters);
+  const int64_t rh = unit / kMergeQuarters;
+  const int r = (int)(rh / p.heads), h = (int)(rh - (int64_t)r * p.heads);
+  const int np = __ldcg(p.row_np + r), base = __ldcg(p.row_base + r);
+  if (np > kFewPieces) return;  // another block's
+  float l_own = -INFINITY;
+  int bad = 0;
+  if (lane < np) {
+    l_own = __ldcg(p.part_lse + (int64_t)(base + lane) * p.heads + h);
+    bad = __ldcg(p.piece_err + base + lane);
+  }
+  float m = l_own;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const bool empty = np <= 0 || __any_sync(0xffffffffu, bad != 0) || !(m > -INFINITY);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float total = 0.f;
+  if (!empty) {
+    const float* src =
+        p.part_out + ((int64_t)base * p.heads + h) * kDLatent + 128 * quarter + 4 * lane;
+    const int64_t step = (int64_t)p.heads * kDLatent;
+    const float w_own = l_own > -INFINITY ? fast_exp2((l_own - m) * kLog2e) : 0.f;
+    for (int k0 = 0; k0 < np; k0 += kWarpMergeLoads) {
+      float4 v[kWarpMergeLoads];
+#pragma unroll
+      for (int k = 0; k < kWarpMergeLoads; ++k)
+        if (k0 + k < np) v[k] = __ldcg(reinterpret_cast<const float4*>(src + (k0 + k) * step));
+#pragma unroll
+      for (int k = 0; k < kWarpMergeLoads; ++k) {
+        if (k0 + k >= np) break;
+        const float w = __shfl_sync(0xffffffffu, w_own, k0 + k);
+        if (w == 0.f) continue;  // an empty piece: its slice may hold anything
+        acc.x += w * v[k].x; acc.y += w * v[k].y; acc.z += w * v[k].z; acc.w += w * v[k].w;
+        total += w;
+      }
+    }
+  }
+  const float inv = empty ? 0.f : 1.0f / total;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  uint2 packed;
+  packed.x = *reinterpret_cast<const uint32_t*>(&lo);
+  packed.y = *reinterpret_cast<const uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(p.out + rh * kDLatent + 128 * quarter + 4 * lane) = packed;
+  if (quarter == 0 && lane == 0) p.lse[rh] = empty ? -INFINITY : m + logf(total);
+}
+
+// Unit `unit` by the whole block.
+__device__ __forceinline__ void merge_unit_by_block(const MergeParams& p, int64_t unit) {
   extern __shared__ float4 stage[];                 // [stage_pieces][32] float4
   __shared__ __align__(8) uint64_t mbar;
   __shared__ MergeShared sm;
@@ -99,81 +210,32 @@ combine_pieces_kernel(const int32_t* __restrict__ row_base, const int32_t* __res
   }
   uint32_t phase = 0;
   const bool ok = merge_unit(
-      blockIdx.x, heads, row_base, row_np, piece_err, part_lse, part_out, out, lse, stage_pieces,
-      stage, sm, mb, phase, (int)threadIdx.x, [] { __syncthreads(); },
+      unit, p.heads, p.row_base, p.row_np, p.piece_err, p.part_lse, p.part_out, p.out, p.lse,
+      p.stage_pieces, stage, sm, mb, phase, (int)threadIdx.x, [] { __syncthreads(); },
       [](bool pred) { return __syncthreads_or(pred ? 1 : 0) != 0; });
-  if (!ok && threadIdx.x == 0) atomicOr(status, MLA_DEVICE_ERR_TIMEOUT);
+  if (!ok && threadIdx.x == 0) atomicOr(p.status, MLA_DEVICE_ERR_TIMEOUT);
 }
 
-// The same merge where rows have few pieces: one warp per unit. A block per unit spends a
-// barrier sequence and a staging area on a piece or two there; here lane l keeps dims
-// 4l .. 4l + 3 of the unit's 128, and the weights of 32 pieces at a time (one a lane).
-// A whole decode call of 256 rows of 8 pages, 64 heads (65,536 units of 1.6 pieces), takes
-// 87 us with it and 178 with the blocks; 128 rows of 32 pages 81 and 140. The blocks' bulk
-// copies win for a row of many pieces, so the rule asks for 2.5 per row on average: with
-// 64 rows, one of 100k tokens and the others of one page, the two are even (117, 123 us);
-// with 32 such rows the blocks are ahead (125, 110).
-constexpr int kWarpMergeWarps = 8;
-constexpr int kWarpMergeLoads = 4;  // pieces whose loads are in flight (8: 95 us, 16: 168 on the 256 rows)
-__global__ void __launch_bounds__(32 * kWarpMergeWarps)
-combine_warps_kernel(const int32_t* __restrict__ row_base, const int32_t* __restrict__ row_np,
-                     const int32_t* __restrict__ piece_err, const float* __restrict__ part_lse,
-                     const float* __restrict__ part_out, int heads, int64_t units,
-                     __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+// Both are launched as dependents of the decode kernel: its partials are visible after
+// griddep_wait.
+__global__ void __launch_bounds__(kMergeThreads) combine_pieces_kernel(const MergeParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * kWarpMergeWarps + (threadIdx.x >> 5);
-  if (unit >= units) return;
-  const int quarter = (int)(unit % kMergeQuarters);
-  const int64_t rh = unit / kMergeQuarters;
-  const int r = (int)(rh / heads), h = (int)(rh - (int64_t)r * heads);
-  const int np = __ldcg(row_np + r), base = __ldcg(row_base + r);
-  float m = -INFINITY, l_own = -INFINITY;
-  int bad = 0;
-  for (int s = lane; s < np; s += 32) {
-    const float l = __ldcg(part_lse + (int64_t)(base + s) * heads + h);
-    if (s == lane) l_own = l;
-    m = fmaxf(m, l);
-    bad |= __ldcg(piece_err + base + s);
+  merge_unit_by_block(p, blockIdx.x);
+}
+
+__global__ void __launch_bounds__(kMergeThreads) combine_rows_kernel(const MergeParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  if (blockIdx.x >= p.many_blocks) {
+    const int64_t unit =
+        (int64_t)(blockIdx.x - p.many_blocks) * kMergeWarps + (threadIdx.x >> 5);
+    if (unit < p.units) merge_unit_by_warp(p, unit, threadIdx.x & 31);
+    return;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const bool empty = np <= 0 || __any_sync(0xffffffffu, bad != 0) || !(m > -INFINITY);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float total = 0.f;
-  if (!empty) {
-    const float* src = part_out + ((int64_t)base * heads + h) * kDLatent + 128 * quarter + 4 * lane;
-    const int64_t step = (int64_t)heads * kDLatent;
-    for (int s0 = 0; s0 < np; s0 += 32) {
-      if (s0 > 0)
-        l_own = s0 + lane < np ? __ldcg(part_lse + (int64_t)(base + s0 + lane) * heads + h) : -INFINITY;
-      const float w_own = l_own > -INFINITY ? fast_exp2((l_own - m) * kLog2e) : 0.f;
-      const int n = min(32, np - s0);
-      for (int k0 = 0; k0 < n; k0 += kWarpMergeLoads) {
-        float4 v[kWarpMergeLoads];
-#pragma unroll
-        for (int k = 0; k < kWarpMergeLoads; ++k)
-          if (k0 + k < n) v[k] = __ldcg(reinterpret_cast<const float4*>(src + (s0 + k0 + k) * step));
-#pragma unroll
-        for (int k = 0; k < kWarpMergeLoads; ++k) {
-          if (k0 + k >= n) break;
-          const float w = __shfl_sync(0xffffffffu, w_own, k0 + k);
-          if (w == 0.f) continue;  // an empty piece: its slice may hold anything
-          acc.x += w * v[k].x; acc.y += w * v[k].y; acc.z += w * v[k].z; acc.w += w * v[k].w;
-          total += w;
-        }
-      }
-    }
-  }
-  const float inv = empty ? 0.f : 1.0f / total;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  uint2 packed;
-  packed.x = *reinterpret_cast<const uint32_t*>(&lo);
-  packed.y = *reinterpret_cast<const uint32_t*>(&hi);
-  *reinterpret_cast<uint2*>(out + rh * kDLatent + 128 * quarter + 4 * lane) = packed;
-  if (quarter == 0 && lane == 0) lse[rh] = empty ? -INFINITY : m + logf(total);
+  const unsigned per_row = (unsigned)p.heads * kMergeQuarters;
+  const int row = find_row_of_many(p, (int)(blockIdx.x / per_row));
+  if (row >= 0) merge_unit_by_block(p, (int64_t)row * per_row + blockIdx.x % per_row);
 }
 
 // Standalone merge: part_out [S][rows][512], part_lse [S][rows]; one block per row.
@@ -189,47 +251,50 @@ combine_dense_kernel(const float* __restrict__ part_out, const float* __restrict
 
 }  // namespace
 
-cudaError_t launch_combine_pieces(const DecodeWorkspace& ws, int rows, int heads,
+cudaError_t launch_combine_pieces(const DecodeWorkspace& ws, int rows, int heads, int passes,
                                   int max_pieces_per_row, __nv_bfloat16* out, float* lse,
                                   cudaStream_t stream) {
-  const int64_t units = (int64_t)rows * heads * kMergeQuarters;
-  const unsigned blocks = (unsigned)units;
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
-  if ((int64_t)rows * 5 >= 2 * (int64_t)max_pieces_per_row) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((units + kWarpMergeWarps - 1) / kWarpMergeWarps));
-    cfg.blockDim = dim3(32 * kWarpMergeWarps);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, combine_warps_kernel, (const int32_t*)ws.row_base,
-                              (const int32_t*)ws.row_np, (const int32_t*)ws.piece_err,
-                              (const float*)ws.part_lse, (const float*)ws.part_out, heads, units,
-                              out, lse);
-  }
-
   static std::atomic<int> configured[64];
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && !configured[dev].load()) {
-    cudaError_t e = cudaFuncSetAttribute(combine_pieces_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kMergeStagePieces * (int)kMergeSliceBytes);
-    if (e != cudaSuccess) return e;
-    configured[dev].store(1);
+  if (dev < 0 || dev >= 64 || !configured[dev].load()) {
+    for (const auto kernel : {combine_pieces_kernel, combine_rows_kernel}) {
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           kMergeStagePieces * (int)kMergeSliceBytes);
+      if (e != cudaSuccess) return e;
+    }
+    if (dev >= 0 && dev < 64) configured[dev].store(1);
   }
-  const int stage = merge_stage_pieces(max_pieces_per_row, rows);
+  MergeParams p;
+  p.row_base = ws.row_base;
+  p.row_np = ws.row_np;
+  p.piece_err = ws.piece_err;
+  p.part_lse = ws.part_lse;
+  p.part_out = ws.part_out;
+  p.rows = rows;
+  p.heads = heads;
+  p.units = (int64_t)rows * heads * kMergeQuarters;
+  // a row of more than kFewPieces pieces is cut at least kFewPieces times (kFewPieces - 1
+  // if its prefix and suffix pieces count together), by max_pieces_per_row CTAs a pass
+  const int64_t many_rows = (int64_t)passes * max_pieces_per_row / (kFewPieces - 1);
+  const bool few_rows = rows <= many_rows;
+  p.many_blocks = few_rows ? 0u : (unsigned)(many_rows * heads * kMergeQuarters);
+  p.out = out;
+  p.lse = lse;
+  p.status = ws.status;
+  p.stage_pieces = merge_stage_pieces(max_pieces_per_row, rows);
+  const int64_t blocks =
+      few_rows ? p.units : p.many_blocks + (p.units + kMergeWarps - 1) / kMergeWarps;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
+  cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kMergeThreads);
-  cfg.dynamicSmemBytes = (size_t)stage * kMergeSliceBytes;
+  cfg.dynamicSmemBytes = (size_t)p.stage_pieces * kMergeSliceBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_pieces_kernel, (const int32_t*)ws.row_base,
-                            (const int32_t*)ws.row_np, (const int32_t*)ws.piece_err,
-                            (const float*)ws.part_lse, (const float*)ws.part_out, heads, out,
-                            lse, ws.status, stage);
+  return cudaLaunchKernelEx(&cfg, few_rows ? combine_pieces_kernel : combine_rows_kernel, p);
 }
 
 }  // namespace mla

@@ -117,8 +117,8 @@ mla_status decode_impl(const void* q, const void* kv_pages, int64_t num_pages, i
   cudaError_t e = (p.bf16 || f16_operands) ? launch_decode_tensor_core(p, s)
                                             : launch_decode_fp8(p, s);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
-  e = launch_combine_pieces(p.ws, (int)rows, num_heads, G, static_cast<__nv_bfloat16*>(out), lse,
-                            s);
+  e = launch_combine_pieces(p.ws, (int)rows, num_heads, grouped ? 2 : 1, G,
+                            static_cast<__nv_bfloat16*>(out), lse, s);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 }  // namespace
