@@ -275,7 +275,9 @@ cudaError_t launch_combine_pieces(const DecodeWorkspace& ws, int rows, int heads
   p.heads = heads;
   p.units = (int64_t)rows * heads * kMergeQuarters;
   // a row of more than kFewPieces pieces is cut at least kFewPieces times (kFewPieces - 1
-  // if its prefix and suffix pieces count together), by max_pieces_per_row CTAs a pass
+  // if its prefix and suffix pieces count together), and the ranges of a pass's CTAs make
+  // fewer cuts than there are CTAs (G of them, which is also the most pieces that a row can
+  // have; F forks of one prefix are cut by G / F workers each)
   const int64_t many_rows = (int64_t)passes * max_pieces_per_row / (kFewPieces - 1);
   const bool few_rows = rows <= many_rows;
   p.many_blocks = few_rows ? 0u : (unsigned)(many_rows * heads * kMergeQuarters);

@@ -5,8 +5,8 @@
 // partial attention outputs over disjoint pieces of a sequence carry their
 // log-sum-exp statistics and are merged with online softmax:
 //   lse = ln sum_s exp(lse_s),  out = sum_s exp(lse_s - lse) * out_s.
-// The merge kernel that follows a decode kernel (combine.cu) runs one unit per
-// block.
+// The merge that follows a decode kernel (combine.cu) runs one unit per block
+// this way, in calls of many rows only those of many pieces.
 #pragma once
 
 #include "mla_common.cuh"
