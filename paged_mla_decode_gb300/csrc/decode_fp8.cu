@@ -26,9 +26,9 @@
 // smaller ring as stored, seven expander warps rewrite each as the swizzled e4m3 page
 // that the contractions read (a table lookup, exact), and everything after that is
 // the e4m3 kernel. It trades one ring slot for the raw pages (kRing 4 + 2 raw). 31
-// requests of 60k-140k tokens with 64 heads (307 pages a CTA) take 429 us, 413 without
-// the expansion, 366 from an e4m3 cache, whose softmax has more registers. What is left
-// is shared-memory bandwidth above all: a page's MMAs read 140 KB of operands (V twice,
+// requests of 60k-140k tokens with 64 heads (307 pages a CTA) take 418 us, some 16 less
+// without the expansion, 357 from an e4m3 cache, whose softmax has more registers. What is
+// left is shared-memory bandwidth above all: a page's MMAs read 140 KB of operands (V twice,
 // for P's two terms), the P buffers and page copies move 35 KB, the expansion reads and
 // writes another 55 KB: 1,800 cycles at 128 B a cycle, of some 2,300 that a page takes.
 //
@@ -348,9 +348,9 @@ __device__ const uint64_t kE2m1Lut[16] = {
 // (e = 4..6), two tokens (lane, lane + 32) a thread. Beside the other roles a warp gets an
 // instruction every four to six cycles whatever its code, so seven warps share the page,
 // and the three schedulers with two of them have five blocks each, the one with one warp
-// three. 31 requests as above: 429 us; six warps 439, four 485, three 493. The loop is
-// short because the roles' loops share the instruction cache: unrolled 457, with the next
-// block's loads in flight (a register copy more) 432.
+// three. 31 requests as above, with a merge that took 11 us more: 429 us; six warps 439,
+// four 485, three 493. The loop is short because the roles' loops share the instruction
+// cache: unrolled 457, with the next block's loads in flight (a register copy more) 432.
 struct ExpandUnit {
   uint4 codes;
   uint2 row;  // of the expansion table
