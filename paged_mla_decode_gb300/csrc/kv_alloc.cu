@@ -12,10 +12,10 @@
 //
 // Two running sums over the batch and 4 bytes written per new token: latency bound for a
 // step's few tokens, then bound by the slots' stores. Every block scans the requests, in
-// chunks of its size, and fills its own run of rows (a thread finds its request by
-// bisection in shared memory, once per 128 rows); the row of a new page's first token
-// also writes the page's table entry and tag. The page ids of new pages come from the
-// free list itself, so that no row waits for another's table entry.
+// chunks of its size, and fills its own run of rows, a warp a run of them at a time: it
+// finds their request by bisection in shared memory, and the row of a new page's first
+// token also writes the page's table entry and tag. The page ids of new pages come from
+// the free list itself, so that no row waits for another's table entry.
 #include <algorithm>
 
 #include "mla_common.cuh"
@@ -27,6 +27,14 @@ namespace {
 constexpr int kAllocThreads = 1024;    // at most; a step's few rows take fewer
 constexpr int kAllocWarps = kAllocThreads / 32;
 constexpr int64_t kBlockRows = 4096;   // rows that are worth a block of their own
+// Rows that a warp fills at a time, with one search for their request: 32 in a step of few
+// rows, 128 in larger calls, and 512 where requests are long (4,096 rows each on average):
+// there most runs have one or two requests, and the warp looks their pages up at once. 32
+// requests of 60k-140k new tokens take 10.3 us so (16.5 with 128 rows a time, each row its
+// own lookup), 512 of 100-5,000 13.9 (12.3), 256 of four 15 (8.2); between 1,000 and 4,000
+// rows a request the two are even.
+constexpr int kFewRows = 32, kManyRows = 128, kPageRows = 512;
+constexpr int64_t kRowsPerRequest = 4096;
 
 struct AllocParams {
   const int32_t* seq_lens;
@@ -107,13 +115,100 @@ __device__ __forceinline__ int32_t pages_for(uint32_t tokens) {
   return (int32_t)(tokens / kPageSize + (tokens % kPageSize != 0));
 }
 
-// kFill: rows [blockIdx.x * rows_per, + rows_per) of the slot map (kRows a thread at a
-// time), with the new pages that begin there. kCommit: block 0 writes the per-request outputs, which may be the inputs:
-// then no other block may still read them (one block in all, or a launch of its own).
-template <bool kFill, bool kCommit, int kRows>
+// Rows x0 + [0, kPageRows) of the slot map, as far as they lie in begin .. end - 1, which belong to
+// requests i and i + 1 of the chunk that starts at request b0. They lie in 11 pages at most:
+// lane k looks up the k-th and enters it where it is new, and the rows take its id from there.
+__device__ __forceinline__ void fill_by_page(const AllocParams& p, const AllocShared& sm, int b0, int i,
+                                             int32_t x0, int32_t begin, int32_t end, int lane) {
+  const int32_t cut = min(sm.row_end[i], end);  // where the second request's rows begin
+  int32_t page = -1, shift[2] = {0, 0}, base[2] = {0, 0};  // lane of position x: x / 64 + base
+  int64_t at = -1;  // block-table entry of a new page whose first token is here, else -1
+  int lanes = 0;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int32_t from = s ? cut : begin, to = s ? end : cut;
+    if (from >= to) continue;
+    const int32_t held = sm.held[i + s];
+    shift[s] = held < 0 ? -from : sm.shift[i + s];
+    const int32_t first = (from + shift[s]) / kPageSize;
+    base[s] = lanes - first;
+    const int32_t j = lane - base[s];
+    if (held >= 0 && j >= first && j <= (to - 1 + shift[s]) / kPageSize) {
+      const int64_t entry = (int64_t)(b0 + i + s) * p.max_pages + j;
+      page = j < held ? p.block_table[entry] : p.free_pages[sm.fresh[i + s] - (j - held)];
+      if (j >= held && j * kPageSize >= from + shift[s]) at = entry;
+    }
+    lanes += (to - 1 + shift[s]) / kPageSize - first + 1;
+  }
+  if (at >= 0) p.block_table[at] = page;
+  if (page < 0 || page >= (int32_t)p.num_pages) page = -1;
+  if (at >= 0 && page >= 0 && p.page_tags != nullptr) {
+    const uint32_t tag = p.page_tags[page] + 1;
+    p.page_tags[page] = tag;
+    p.expected_tags[at] = tag;
+  }
+#pragma unroll
+  for (int k = 0; k < kPageRows / 32; ++k) {
+    const int32_t x = x0 + 32 * k + lane;
+    const int s = x >= cut;
+    const int32_t pos = (int32_t)((uint32_t)x + (uint32_t)(s ? shift[1] : shift[0]));
+    const int32_t id = __shfl_sync(0xffffffffu, page, pos / kPageSize + (s ? base[1] : base[0]));
+    if (x >= begin && x < end) p.slots[x] = id >= 0 ? id * kPageSize + pos % kPageSize : -1;
+  }
+}
+
+// Rows x0 + [0, 32 * kRows) likewise, of requests i and on; a row looks its page up itself.
+template <int kRows>
+__device__ __forceinline__ void fill_by_row(const AllocParams& p, const AllocShared& sm, int b0, int i,
+                                            int32_t x0, int32_t begin, int32_t end, int lane) {
+  // all of a thread's page ids are asked for before the first is used, then all tags
+  int32_t page[kRows], off[kRows];
+  int64_t at[kRows];  // block-table entry of a new page's first token, else -1
+  uint32_t tag[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int32_t x = x0 + 32 * k + lane;
+    page[k] = -1;
+    off[k] = 0;
+    at[k] = -1;
+    if (x < begin || x >= end) continue;
+    while (sm.row_end[i] <= x) ++i;
+    const int32_t held = sm.held[i];
+    if (held < 0) continue;
+    const int32_t pos = x + sm.shift[i], j = pos / kPageSize;
+    const int64_t entry = (int64_t)(b0 + i) * p.max_pages + j;
+    off[k] = pos % kPageSize;
+    page[k] = j < held ? p.block_table[entry] : p.free_pages[sm.fresh[i] - (j - held)];
+    // (a page held before covers every cached token: a new one starts at its token 0)
+    if (j >= held && off[k] == 0) at[k] = entry;
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const bool in_cache = page[k] >= 0 && page[k] < (int32_t)p.num_pages;
+    if (at[k] >= 0) {
+      p.block_table[at[k]] = page[k];
+      if (p.page_tags == nullptr || !in_cache) at[k] = -1;
+      else tag[k] = p.page_tags[page[k]] + 1;
+    }
+    const int32_t x = x0 + 32 * k + lane;
+    if (x >= begin && x < end) p.slots[x] = in_cache ? page[k] * kPageSize + off[k] : -1;
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k)
+    if (at[k] >= 0) {
+      p.page_tags[page[k]] = tag[k];
+      p.expected_tags[at[k]] = tag[k];
+    }
+}
+
+// kRows > 0: rows [blockIdx.x * rows_per, + rows_per) of the slot map, kRows a warp at a
+// time, with the new pages that begin there. kCommit: block 0 writes the per-request
+// outputs, which may be the inputs: then no other block may still read them (one block in
+// all, or a launch of its own).
+template <int kRows, bool kCommit>
 __global__ void __launch_bounds__(kAllocThreads)
     kv_alloc_kernel(const AllocParams p, const int64_t rows_per) {
-  constexpr int kWarpRows = 32 * kRows;  // rows a warp fills per bisection
+  constexpr bool kFill = kRows > 0;
   __shared__ AllocShared sm;
   const int threads = blockDim.x, warps = threads >> 5;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -171,55 +266,22 @@ __global__ void __launch_bounds__(kAllocThreads)
     if constexpr (kFill) {
       const int nb = min(threads, p.batch - b0);
       const int32_t from = (int32_t)done.x, to = min((int32_t)row_all, hi);
-      for (int32_t x0 = lo + warp * kWarpRows; x0 < to; x0 += warps * kWarpRows) {
-        if (x0 + kWarpRows <= from) continue;  // (rows of an earlier chunk)
-        int i = first_after(sm.row_end, nb, max(x0, from));
-        // most runs lie in one request: its data is then read once
-        const bool whole = i < nb && sm.row_end[i] >= min(x0 + kWarpRows, to);
-        int32_t held_i = whole ? sm.held[i] : -1, shift = sm.shift[i % kAllocThreads];
-        int32_t fresh = sm.fresh[i % kAllocThreads];
-        // all of a thread's page ids are asked for before the first is used, then all tags
-        int32_t page[kRows], off[kRows];
-        int64_t at[kRows];  // block-table entry of a new page's first token, else -1
-        uint32_t tag[kRows];
-#pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-          const int32_t x = x0 + 32 * k + lane;
-          page[k] = -1;
-          off[k] = 0;
-          at[k] = -1;
-          if (x < from || x >= to) continue;
-          if (!whole) {
-            while (sm.row_end[i] <= x) ++i;
-            held_i = sm.held[i];
-            shift = sm.shift[i];
-            fresh = sm.fresh[i];
+      for (int32_t x0 = lo + warp * kRows; x0 < to; x0 += warps * kRows) {
+        if (x0 + kRows <= from) continue;  // (rows of an earlier chunk)
+        const int32_t begin = max(x0, from), end = min(x0 + kRows, to);
+        const int i = first_after(sm.row_end, nb, begin);
+        if constexpr (kRows == kPageRows) {
+          if (i + 2 >= nb || sm.row_end[i + 1] >= end) {
+            fill_by_page(p, sm, b0, i, x0, begin, end, lane);
+          } else {
+            for (int32_t x = x0; x < end; x += kManyRows)
+              if (x + kManyRows > begin)
+                fill_by_row<kManyRows / 32>(p, sm, b0, x <= begin ? i : first_after(sm.row_end, nb, x), x,
+                                            begin, end, lane);
           }
-          if (held_i < 0) continue;
-          const int32_t pos = x + shift, j = pos / kPageSize;
-          const int64_t entry = (int64_t)(b0 + i) * p.max_pages + j;
-          off[k] = pos % kPageSize;
-          page[k] = j < held_i ? p.block_table[entry] : p.free_pages[fresh - (j - held_i)];
-          // (a page held before covers every cached token: a new one starts at its token 0)
-          if (j >= held_i && off[k] == 0) at[k] = entry;
+        } else {
+          fill_by_row<kRows / 32>(p, sm, b0, i, x0, begin, end, lane);
         }
-#pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-          const bool in_cache = page[k] >= 0 && page[k] < (int32_t)p.num_pages;
-          if (at[k] >= 0) {
-            p.block_table[at[k]] = page[k];
-            if (p.page_tags == nullptr || !in_cache) at[k] = -1;
-            else tag[k] = p.page_tags[page[k]] + 1;
-          }
-          const int32_t x = x0 + 32 * k + lane;
-          if (x >= from && x < to) p.slots[x] = in_cache ? page[k] * kPageSize + off[k] : -1;
-        }
-#pragma unroll
-        for (int k = 0; k < kRows; ++k)
-          if (at[k] >= 0) {
-            p.page_tags[page[k]] = tag[k];
-            p.expected_tags[at[k]] = tag[k];
-          }
       }
     }
     done = Pair{row_all, plus(done, sums).y};
@@ -280,10 +342,9 @@ extern "C" mla_status mla_kv_alloc(const int32_t* seq_lens, const int32_t* new_t
   if (sms <= 0) return MLA_ERR_CUDA;
   int64_t blocks = std::min<int64_t>((num_slots + kBlockRows - 1) / kBlockRows, sms);
   blocks = std::max<int64_t>(blocks, 1);
-  // A warp bisects once per 128 rows, in a step of a few rows a request once per 32; one
-  // block has the threads that its requests and rows keep busy.
-  const bool many = num_slots > kAllocThreads;
-  const int warp_rows = many ? 128 : 32;
+  const int warp_rows = num_slots <= kAllocThreads ? kFewRows
+                        : num_slots >= kRowsPerRequest * batch ? kPageRows
+                                                               : kManyRows;
   const int64_t rows_per = ((num_slots + blocks - 1) / blocks + warp_rows - 1) / warp_rows * warp_rows;
   int threads = 128;
   while (threads < kAllocThreads && (blocks > 1 || threads < std::max<int64_t>(batch, num_slots)))
@@ -297,9 +358,12 @@ extern "C" mla_status mla_kv_alloc(const int32_t* seq_lens, const int32_t* new_t
     for (int o = 0; o < 5; ++o)
       apart = apart && !overlap(ins[i], i == 3 ? 1 : batch, outs[o], o == 2 ? 1 : batch + (o == 3));
   const bool at_once = blocks == 1 || apart;
-  const auto fill = at_once ? (many ? kv_alloc_kernel<true, true, 4> : kv_alloc_kernel<true, true, 1>)
-                            : kv_alloc_kernel<true, false, 4>;
+  const auto fill =
+      warp_rows == kFewRows ? kv_alloc_kernel<kFewRows, true>
+      : warp_rows == kManyRows
+          ? (at_once ? kv_alloc_kernel<kManyRows, true> : kv_alloc_kernel<kManyRows, false>)
+          : (at_once ? kv_alloc_kernel<kPageRows, true> : kv_alloc_kernel<kPageRows, false>);
   fill<<<(unsigned)blocks, threads, 0, s>>>(p, rows_per);
-  if (!at_once) kv_alloc_kernel<false, true, 1><<<1, threads, 0, s>>>(p, rows_per);
+  if (!at_once) kv_alloc_kernel<0, true><<<1, threads, 0, s>>>(p, rows_per);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
