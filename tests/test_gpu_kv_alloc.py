@@ -102,6 +102,20 @@ def test_refusals_and_bad_requests(cuda_device, B, new, num_slots, width):
     _same(d, want)
 
 
+@pytest.mark.parametrize("B,new,num_slots,bad", [(2, 30000, None, 0), (6, 30000, None, 3), (9, 20000, 70000, 2),
+                                                 (3, 13000, None, 1)])
+def test_long_requests(cuda_device, B, new, num_slots, bad):
+    """Runs of rows within one or two long requests, some of them refused, with bad free pages."""
+    c = _inputs(B + new, B, 3000, new, num_slots=num_slots, bad=bad)
+    c["free"][::9] = -1
+    c["free"][4::11] = c["pages"]
+    d = _device(c, cuda_device)
+    _call(c, d)
+    want = _oracle(c)
+    assert len(want["slot_mapping"]) >= 4096 * B and (want["slot_mapping"] >= 0).any()
+    _same(d, want)
+
+
 @pytest.mark.parametrize("count", [-5, 0, 10 ** 6])
 def test_free_count_is_clamped_to_the_list(cuda_device, count):
     c = _inputs(3, 5, 100, 200)
