@@ -139,6 +139,7 @@ struct Map {
   static constexpr int kOffPmax = kOffLinv + 256;                   // float [2 pages][2 halves][64]
   static constexpr int kOffLsum = kOffPmax + 1024;                  // float [2 halves][64]
   static constexpr int kOffLut = kOffLsum + 512;                    // uint64 [16] (4-bit cache)
+  static_assert(kOffLut % 128 == 0, "a row's address is the table's | 8n");
   static constexpr int kOffFlags = kOffLut + (kE2m1 ? 128 : 0);     // int [4]
   static constexpr int kOffPlan = kOffFlags + 16;                   // int64 [6]
   static constexpr int kOffDesc = kOffPlan + 48;                    // PageDesc [kDescRing]
@@ -356,13 +357,13 @@ struct ExpandUnit {
   uint2 row;  // of the expansion table
 };
 __device__ __forceinline__ void expand_load(ExpandUnit& u, uint32_t code_at, uint32_t lut,
-                                            uint32_t n) {
+                                            uint32_t n8) {
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(u.codes.x), "=r"(u.codes.y), "=r"(u.codes.z), "=r"(u.codes.w)
                : "r"(code_at));
   asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n"
                : "=r"(u.row.x), "=r"(u.row.y)
-               : "r"(lut + 8 * (n & 15u)));
+               : "r"(lut | (n8 & 0x78u)));
 }
 // Chunks c and c + 1 of a row (c even): the swizzle makes them each other's neighbour.
 __device__ __forceinline__ void expand_write(const ExpandUnit& u, uint32_t at) {
@@ -375,40 +376,55 @@ __device__ __forceinline__ void expand_write(const ExpandUnit& u, uint32_t at) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(at ^ 16u), "r"(c2.x), "r"(c2.y),
                "r"(c3.x), "r"(c3.y) : "memory");
 }
-__device__ __forceinline__ void expand_page(uint32_t raw, uint32_t page, uint32_t lut, int e,
-                                            int lane) {
-  const int b0 = e < 4 ? 3 * e : 4 + 2 * e, blocks = e < 4 ? 3 : 2;
-  uint32_t exps[2];  // the blocks' nibbles, the first lowest
+// What stays the same from page to page, as offsets in shared memory.
+struct Expander {
+  uint32_t codes, exps;  // the first block's, in raw page 0
+  uint32_t to, sw;       // this token's row in page slot 0 and its swizzle
+  uint32_t next;         // bytes from it to the row of token lane + 32
+  uint32_t first;        // 32 * the first block
+  int blocks, shift;
+};
+template <class M>
+__device__ __forceinline__ Expander expander(int e, int lane) {
+  static_assert(kExpWarps == 7 && kDLatent / kE2m1Block == 16, "the last warp has the rope blocks");
+  const int b0 = e < 4 ? 3 * e : 4 + 2 * e;
+  const bool rope = e == kExpWarps - 1;
+  Expander x;
+  x.blocks = e < 4 ? 3 : 2;
+  x.shift = 4 * (b0 & 1);
+  x.first = 32u * b0;
+  x.codes = M::kOffRaw + e2m1_code_offset(b0, lane);
+  x.exps = M::kOffRaw + e2m1_exp_offset(b0, lane);
+  x.to = M::kOffPages + (rope ? lane * 64 : lane * 128);  // (b0 = 16 adds the latent blocks)
+  x.sw = (rope ? (lane >> 1) & 3 : lane & 7) << 4;
+  x.next = rope ? 32 * 64 : 32 * 128;
+  return x;
+}
+__device__ __forceinline__ void expand_page(const Expander& x, uint32_t raw, uint32_t page,
+                                            uint32_t lut) {
+  uint32_t n8[2];  // the blocks' nibbles, the first at bit 3
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const uint32_t at = raw + e2m1_exp_offset(b0, lane + 32 * k);
-    uint32_t x, y = 0;
-    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(x) : "r"(at));
-    if ((b0 & 1) + blocks > 2) asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(y) : "r"(at + kPageSize));
-    exps[k] = (x + (y << 8)) >> (4 * (b0 & 1));
+    const uint32_t at = raw + x.exps + 32 * k;
+    uint32_t u, v = 0;
+    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(u) : "r"(at));
+    if ((x.shift >> 2) + x.blocks > 2) asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(v) : "r"(at + kPageSize));
+    n8[k] = (8u * u + 2048u * v) >> x.shift;
   }
-  uint32_t code_at = raw + e2m1_code_offset(b0, lane);
-  const uint32_t lat = page + lane * 128, lat_sw = (uint32_t)(lane & 7) << 4;
-  const uint32_t rope = page + kRopeOff + lane * 64, rope_sw = (uint32_t)((lane >> 1) & 3) << 4;
-  auto load = [&](ExpandUnit (&u)[2]) {
-    expand_load(u[0], code_at, lut, exps[0]);
-    expand_load(u[1], code_at + e2m1_code_offset(0, 32), lut, exps[1]);
-    exps[0] >>= 4;
-    exps[1] >>= 4;
-    code_at += e2m1_code_offset(1, 0);
-  };
-  auto write = [&](const ExpandUnit (&u)[2], int b) {
-    const bool is_rope = b >= kDLatent / kE2m1Block;
-    const uint32_t c = ((uint32_t)b & 3u) << 5;
-    const uint32_t at = is_rope ? rope + (c ^ rope_sw) : lat + (uint32_t)(b >> 2) * kLatBlock + (c ^ lat_sw);
-    expand_write(u[0], at);
-    expand_write(u[1], at + (is_rope ? 32u * 64u : 32u * 128u));
-  };
+  uint32_t code_at = raw + x.codes, d = x.first;
+  const uint32_t to = page + x.to;
 #pragma unroll 1
-  for (int i = 0; i < blocks; ++i) {
+  for (int i = 0; i < x.blocks; ++i) {
     ExpandUnit u[2];
-    load(u);
-    write(u, b0 + i);
+    expand_load(u[0], code_at, lut, n8[0]);
+    expand_load(u[1], code_at + e2m1_code_offset(0, 32), lut, n8[1]);
+    n8[0] >>= 4;
+    n8[1] >>= 4;
+    code_at += e2m1_code_offset(1, 0);
+    const uint32_t at = to + (d / 128) * kLatBlock + ((d & 96u) ^ x.sw);
+    d += 32;
+    expand_write(u[0], at);
+    expand_write(u[1], at + x.next);
   }
 }
 
@@ -656,20 +672,21 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
       // =================== expanders of a 4-bit cache (7 warps) ===================
       if constexpr (kE2m1) {
         bool ok = true;
-        for (int64_t j = 0; j < npages; ++j) {
-          const int rs = (int)(j % M::kRawRing), slot = (int)(j % kRing);
-          ok = tc::mbar_wait(bar(M::BAR_RAW_FULL + rs), (uint32_t)(j / M::kRawRing) & 1, kWaitNs);
+        const Expander x = expander<M>(warp - kExpWarp0, lane);
+        const uint32_t lut = sbase + M::kOffLut;
+        const uint32_t pages = (uint32_t)npages;
+        for (uint32_t j = 0; j < pages; ++j) {
+          const uint32_t rs = j % M::kRawRing, slot = j % kRing;
+          ok = tc::mbar_wait(bar(M::BAR_RAW_FULL + rs), (j / M::kRawRing) & 1, kWaitNs);
           // the page that held the slot has been read by its PV (and its QK before that)
           if (ok && j >= kRing)
-            ok = tc::mbar_wait(bar(BAR_PV_DONE + slot), ((uint32_t)(j / kRing) - 1) & 1, kWaitNs);
+            ok = tc::mbar_wait(bar(BAR_PV_DONE + slot), (j / kRing - 1) & 1, kWaitNs);
           ok = __all_sync(0xffffffffu, ok && !flags[F_ABORT]);
           if (!ok) break;
           // a bad page id brought no bytes: its tokens are masked and its value rows
           // zeroed by the softmax warps
           if (desc[j % kDescRing].flags & kDescPageOk)
-            expand_page(sbase + M::kOffRaw + rs * kE2m1PageBytes,
-                        sbase + kOffPages + slot * kPageBytes, sbase + M::kOffLut,
-                        warp - kExpWarp0, lane);
+            expand_page(x, sbase + rs * kE2m1PageBytes, sbase + slot * kPageBytes, lut);
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
