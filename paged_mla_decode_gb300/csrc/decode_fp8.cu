@@ -833,23 +833,24 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(BAR_O_EMPTY));
       }
-      for (int64_t j = 0; j < npages; ++j) {
-        // Page 0 opens the first piece, whose row the plan gives: its q is staged at
-        // once. Later pages' descriptors are read once the page has landed.
-        int row = cur0.r;
-        bool ps = j == 0;
-        // (a failed wait is acted on at this page's block barrier below; every
-        // thread reads the same descriptor word, so the piece-start decision, and
-        // with it the barriers of the q staging, is uniform either way)
-        if (!tc::mbar_wait(bar(BAR_PAGE_FULL + (int)(j % kRing)), (uint32_t)(j / kRing) & 1,
-                           kWaitNs))
-          flags[F_ABORT] = 1;
-        if (j > 0) {
-          const PageDesc d0 = desc[j % kDescRing];
-          row = min(max(d0.row, 0), p.rows - 1);  // in range even if a stopped producer never wrote it
-          ps = d0.flags & kDescPieceStart;
-        }
+      // This loop is a chain of short steps that every page goes through: what it has to
+      // know of page j is asked for at once, ahead of S, and ring positions are counted
+      // (page j is in slot `slot`, its barriers complete with parity `par`). 31 requests of
+      // 60k-140k tokens: e4m3 cache 334 us so, 358 with one question after another; 4-bit
+      // cache 395 and 417.
+      bool ps = true;  // page j starts a piece
+      uint32_t slot = 0, par = 0;
+      const uint32_t pages = (uint32_t)npages;
+      for (uint32_t j = 0; j < pages; ++j) {
+        // (a failed wait is acted on at this page's block barrier below)
         if (ps) {
+          // Page 0 opens the first piece, whose row the plan gives: its q is staged at
+          // once. Later rows are read from the descriptor once the page has landed.
+          int row = cur0.r;
+          if (j > 0) {
+            if (!tc::mbar_wait(bar(BAR_PAGE_FULL + slot), par, kWaitNs)) flags[F_ABORT] = 1;
+            row = min(max(desc[j % kDescRing].row, 0), p.rows - 1);  // in range even if a stopped producer never wrote it
+          }
           // ---- load the split q of this row into A ----
           if (piece > 0) {
             const bool got = tc::mbar_wait(bar(BAR_Q_EMPTY), (uint32_t)(piece - 1) & 1, kWaitNs);
@@ -904,8 +905,19 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
         // ---- S of this page ----
         // (a failed wait, like a stop by another role, is acted on at this page's
         // block barrier below: one barrier per page)
-        if (!tc::mbar_wait(bar(BAR_S_FULL + (int)(j & 1)), (uint32_t)(j >> 1) & 1, kWaitNs))
+        const bool s_full = tc::mbar_test(bar(BAR_S_FULL + (j & 1)), (j >> 1) & 1);
+        const bool page_full = tc::mbar_test(bar(BAR_PAGE_FULL + slot), par);  // (its descriptor is read)
+        // P buffer j % 3 was read by PV(j - 3); its end also makes the PV_DONE parity of
+        // the rescale below unambiguous
+        const uint32_t slot3 = slot >= kPBufs ? slot - kPBufs : slot + kRing - kPBufs;
+        const uint32_t par3 = slot >= kPBufs ? par : par ^ 1u;
+        const bool p_free = j < kPBufs || tc::mbar_test(bar(BAR_PV_DONE + slot3), par3);
+        bool stop = flags[F_ABORT] != 0;
+        if ((!s_full && !tc::mbar_wait_slow(bar(BAR_S_FULL + (j & 1)), (j >> 1) & 1, kWaitNs)) ||
+            (!page_full && !tc::mbar_wait(bar(BAR_PAGE_FULL + slot), par, kWaitNs))) {
           flags[F_ABORT] = 1;
+          stop = true;
+        }
         if (t == 0) MLA_STAMP(kStSmS, j);
         // page validity (tokens of a bad page id are masked and reported)
         const PageDesc d = desc[j % kDescRing];
@@ -918,13 +930,13 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
         }
         tc::fence_after_sync();
         uint32_t shi[16], slo[16];
-        const uint32_t scol = s_col((int)(j & 1)) + 32u * (uint32_t)g;
+        const uint32_t scol = s_col(j & 1) + 32u * (uint32_t)g;
         tc::tmem_ld16x2_16(tmem + lane_hi + scol, shi);
         tc::tmem_ld16x2_16(tmem + lane_lo + scol, slo);
         tc::tmem_wait_ld();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(BAR_S_EMPTY + (int)(j & 1)));
+        if (lane == 0) tc::mbar_arrive(bar(BAR_S_EMPTY + (j & 1)));
         float s[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -938,25 +950,19 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 16; ++i) tm = fmaxf(tm, s[i]);
         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
-        if (lane < 16) pmax_s[(int)(j & 1) * 128 + g * 64 + h] = tm;
-        // P buffer j % 3 was read by PV(j - 3); waiting for it also makes the
-        // PV_DONE parity of the rescale below unambiguous (PV(j - 3) is complete)
-        if (j >= kPBufs && !flags[F_ABORT]) {
-          const int64_t jp = j - kPBufs;  // the page whose PV read this P buffer
-          const bool got = tc::mbar_wait(bar(BAR_PV_DONE + (int)(jp % kRing)),
-                                         (uint32_t)(jp / kRing) & 1, kWaitNs);
-          if (!got) {
-            flags[F_ABORT] = 1;
-            atomicOr(p.ws.status, MLA_DEVICE_ERR_TIMEOUT);
-          }
+        if (lane < 16) pmax_s[(j & 1) * 128 + g * 64 + h] = tm;
+        if (!p_free && !flags[F_ABORT] && !tc::mbar_wait(bar(BAR_PV_DONE + slot3), par3, kWaitNs)) {
+          flags[F_ABORT] = 1;
+          stop = true;
+          atomicOr(p.ws.status, MLA_DEVICE_ERR_TIMEOUT);
         }
         // lazy running max: O is rescaled only when a head's page max rises more than
         // kRescaleThresh above it or falls more than kLowThresh below it; a half
         // page's max outside that band asks every thread to look closer
         const bool trig = !ps && (tm > m + kRescaleThresh || tm < m - kLowThresh);
-        const bool any = named_bar_softmax_or(trig || flags[F_ABORT] != 0);
+        const bool any = named_bar_softmax_or(trig || stop);
         if (t == 0) MLA_STAMP(kStSmBar, j);
-        const float tmax = fmaxf(tm, pmax_s[(int)(j & 1) * 128 + (1 - g) * 64 + h]);
+        const float tmax = fmaxf(tm, pmax_s[(j & 1) * 128 + (1 - g) * 64 + h]);
         if (any && named_bar_softmax_or(flags[F_ABORT] != 0)) {
           ok = false;
           break;
@@ -986,11 +992,9 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
           if (named_bar_softmax_or(grow)) {
             // bring O^T (PVs of the previous two pages done: they come from the two PV
             // warps) to the new maxima (up or down)
-            bool got = tc::mbar_wait(bar(BAR_PV_DONE + (int)((j - 1) % kRing)),
-                                     (uint32_t)((j - 1) / kRing) & 1, kWaitNs);
+            bool got = tc::mbar_wait(bar(BAR_PV_DONE + (j - 1) % kRing), ((j - 1) / kRing) & 1, kWaitNs);
             if (got && j >= 2)
-              got = tc::mbar_wait(bar(BAR_PV_DONE + (int)((j - 2) % kRing)),
-                                  (uint32_t)((j - 2) / kRing) & 1, kWaitNs);
+              got = tc::mbar_wait(bar(BAR_PV_DONE + (j - 2) % kRing), ((j - 2) / kRing) & 1, kWaitNs);
             if (named_bar_softmax_or(!got)) {
               ok = false;
               break;
@@ -1033,7 +1037,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
             lw[k] = lcode[0] | (lcode[1] << 16);
           }
           lpart += rs;
-          const uint32_t prow = sbase + kOffP + (int)(j % kPBufs) * kPBytes + h * 128;
+          const uint32_t prow = sbase + kOffP + (j % kPBufs) * kPBytes + h * 128;
           const int sw = h & 7;
           asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(prow + ((c16 ^ sw) << 4)),
                        "r"(hw[0]), "r"(hw[1]), "r"(hw[2]), "r"(hw[3]));
@@ -1044,7 +1048,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
           // value rows past the page's last token (all rows of a bad page id) become
           // zeros before PV reads them: their weights are 0, and 0 times a stale
           // NaN code would poison O (QK(j) has already read the page)
-          const uint32_t page_base = sbase + kOffPages + (int)(j % kRing) * kPageBytes;
+          const uint32_t page_base = sbase + kOffPages + slot * kPageBytes;
           for (int i = t; i < (kPageSize - nvis) * 32; i += kSmThreads) {
             const int rrow = nvis + (i >> 5), u = i & 31;
             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(
@@ -1055,7 +1059,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
         tc::fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(BAR_P_FULL + (int)(j % kPBufs)));
+        if (lane == 0) tc::mbar_arrive(bar(BAR_P_FULL + j % kPBufs));
         if (t == 0) MLA_STAMP(kStSmP, j);
         if (pe) {
           // ---- epilogue: O^T / l -> this piece's partial slot ----
@@ -1122,6 +1126,11 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
           m = -INFINITY;
           lpart = 0.f;
           ++piece;
+        }
+        ps = pe;
+        if (++slot == kRing) {
+          slot = 0;
+          par ^= 1u;
         }
       }
       if (!ok && t == 0) abort_cta();
