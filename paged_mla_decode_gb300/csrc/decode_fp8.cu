@@ -321,21 +321,29 @@ __device__ __forceinline__ bool named_bar_softmax_or(bool pred) {
   return r != 0;
 }
 
-// Two floats -> two e4m3 codes (round to nearest even, saturating); `lo` in the low byte.
-__device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
+// Four floats -> four e4m3 (e5m2) codes, round to nearest even, saturating; `a` lowest.
+__device__ __forceinline__ uint32_t e4m3x4_of(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n"
+      " cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}\n"
+      : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
 }
-__device__ __forceinline__ float2 e4m3x2_value(uint32_t codes) {
-  const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)codes);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h2));
-}
-// Two floats -> two e5m2 codes (round to nearest even, saturating); `lo` in the low byte.
-__device__ __forceinline__ uint32_t e5m2x2_of(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
+__device__ __forceinline__ uint32_t e5m2x4_of(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e5m2x2.f32 l, %2, %1;\n"
+      " cvt.rn.satfinite.e5m2x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}\n"
+      : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
+}
+// The values of four e4m3 codes (every one an f16 number).
+__device__ __forceinline__ float4 e4m3x4_value(uint32_t codes) {
+  uint32_t l, h;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, h;\n}\n" : "=r"(l), "=r"(h) : "r"(codes));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&l));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return make_float4(a.x, a.y, b.x, b.y);
 }
 
 // Rows of the expansion table by exponent nibble (e2m1_as_e4m3), copied to shared memory.
@@ -1021,20 +1029,13 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
           float rs = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint32_t hcode[2], lcode[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int i = 4 * k + 2 * e;
-              const float p0 = fast_exp2(s[i] - mu), p1 = fast_exp2(s[i + 1] - mu);
-              const uint32_t hc = e4m3x2_of(p0, p1);
-              const float2 hv = e4m3x2_value(hc);
-              const uint32_t lc = e5m2x2_of(p0 - hv.x, p1 - hv.y);
-              rs += p0 + p1;  // the exact P: lse does not carry the operand rounding
-              hcode[e] = hc;
-              lcode[e] = lc;
-            }
-            hw[k] = hcode[0] | (hcode[1] << 16);
-            lw[k] = lcode[0] | (lcode[1] << 16);
+            const float p0 = fast_exp2(s[4 * k] - mu), p1 = fast_exp2(s[4 * k + 1] - mu);
+            const float p2 = fast_exp2(s[4 * k + 2] - mu), p3 = fast_exp2(s[4 * k + 3] - mu);
+            hw[k] = e4m3x4_of(p0, p1, p2, p3);
+            const float4 hv = e4m3x4_value(hw[k]);
+            lw[k] = e5m2x4_of(p0 - hv.x, p1 - hv.y, p2 - hv.z, p3 - hv.w);
+            rs += p0 + p1;  // the exact P: lse does not carry the operand rounding
+            rs += p2 + p3;
           }
           lpart += rs;
           const uint32_t prow = sbase + kOffP + (j % kPBufs) * kPBytes + h * 128;
@@ -1205,16 +1206,11 @@ __global__ void __launch_bounds__(kSplitThreads)
   uint32_t hw[4], lw[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    uint32_t hc[2], lc[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float x0 = f[4 * k + 2 * e] * sc, x1 = f[4 * k + 2 * e + 1] * sc;
-      hc[e] = e4m3x2_of(x0, x1);
-      const float2 hv = e4m3x2_value(hc[e]);
-      lc[e] = e4m3x2_of(x0 - hv.x, x1 - hv.y);
-    }
-    hw[k] = hc[0] | (hc[1] << 16);
-    lw[k] = lc[0] | (lc[1] << 16);
+    const float x0 = f[4 * k] * sc, x1 = f[4 * k + 1] * sc;
+    const float x2 = f[4 * k + 2] * sc, x3 = f[4 * k + 3] * sc;
+    hw[k] = e4m3x4_of(x0, x1, x2, x3);
+    const float4 hv = e4m3x4_value(hw[k]);
+    lw[k] = e4m3x4_of(x0 - hv.x, x1 - hv.y, x2 - hv.z, x3 - hv.w);
   }
   const int lane_hi = 32 * (h >> 4) + (h & 15);
   uint4* dst = reinterpret_cast<uint4*>(q_op + row * kQOpRowBytes) + 128 * u;
