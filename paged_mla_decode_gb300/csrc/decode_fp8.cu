@@ -26,11 +26,12 @@
 // smaller ring as stored, seven expander warps rewrite each as the swizzled e4m3 page
 // that the contractions read (a table lookup, exact), and everything after that is
 // the e4m3 kernel. It trades one ring slot for the raw pages (kRing 4 + 2 raw). 31
-// requests of 60k-140k tokens with 64 heads (307 pages a CTA) take 418 us, some 16 less
-// without the expansion, 357 from an e4m3 cache, whose softmax has more registers. What is
-// left is shared-memory bandwidth above all: a page's MMAs read 140 KB of operands (V twice,
-// for P's two terms), the P buffers and page copies move 35 KB, the expansion reads and
-// writes another 55 KB: 1,800 cycles at 128 B a cycle, of some 2,300 that a page takes.
+// requests of 60k-140k tokens with 64 heads (307 pages a CTA) take 390 us, 330 from an
+// e4m3 cache. The difference is the expansion: without it (a probe) the kernels are even,
+// whether the pages come from L2 or not. Its 1,900 cycles a page run beside a softmax that
+// takes some 1,900 itself, on the same schedulers and the same integer pipe (61% busy),
+// with shared memory at three quarters of its rate: a page's MMAs read 140 KB of operands
+// (V twice, for P's two terms), the P buffers and page copies move 35 KB, the expansion 55.
 //
 // Warp roles (416 threads; 640 with the expanders):
 //   warps 0-7  q loading, softmax and epilogue. Row t of A and S is (head
@@ -357,9 +358,10 @@ __device__ const uint64_t kE2m1Lut[16] = {
 // (e = 4..6), two tokens (lane, lane + 32) a thread. Beside the other roles a warp gets an
 // instruction every four to six cycles whatever its code, so seven warps share the page,
 // and the three schedulers with two of them have five blocks each, the one with one warp
-// three. 31 requests as above, with a merge that took 11 us more: 429 us; six warps 439,
-// four 485, three 493. The loop is short because the roles' loops share the instruction
-// cache: unrolled 457, with the next block's loads in flight (a register copy more) 432.
+// three (six warps 2% slower, four 13%, three 15%; ten half blocks for each of the three
+// schedulers 4%). 31 requests as above: 390 us; unrolled 443, with the next block's loads
+// in flight 412, a token at a time 410: the roles' loops share the instruction cache, and
+// a shorter loop leaves a warp waiting.
 struct ExpandUnit {
   uint4 codes;
   uint2 row;  // of the expansion table
