@@ -26,7 +26,7 @@
 // smaller ring as stored, seven expander warps rewrite each as the swizzled e4m3 page
 // that the contractions read (a table lookup, exact), and everything after that is
 // the e4m3 kernel. It trades one ring slot for the raw pages (kRing 4 + 2 raw). 31
-// requests of 60k-140k tokens with 64 heads (307 pages a CTA) take 390 us, 330 from an
+// requests of 60k-140k tokens with 64 heads (307 pages a CTA) take 382 us, 327 from an
 // e4m3 cache. The difference is the expansion: without it (a probe) the kernels are even,
 // whether the pages come from L2 or not. Its 1,900 cycles a page run beside a softmax that
 // takes some 1,900 itself, on the same schedulers and the same integer pipe (61% busy),
@@ -347,6 +347,31 @@ __device__ __forceinline__ float4 e4m3x4_value(uint32_t codes) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
+// Two float operations in one instruction, each rounded as by itself. The softmax warps
+// share their schedulers with the other roles: 31 requests of 60k-140k tokens 382 us with
+// a 4-bit cache, 390 without these; e4m3 327 and 331.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, r;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 r, a, b;\n mov.b64 {%0, %1}, r;\n}\n"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, r;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 r, a, b;\n mov.b64 {%0, %1}, r;\n}\n"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c, r;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 r, a, b, c;\n mov.b64 {%0, %1}, r;\n}\n"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
 // Rows of the expansion table by exponent nibble (e2m1_as_e4m3), copied to shared memory.
 __device__ const uint64_t kE2m1Lut[16] = {
     e2m1_as_e4m3(0),  e2m1_as_e4m3(1),  e2m1_as_e4m3(2),  e2m1_as_e4m3(3),
@@ -359,9 +384,9 @@ __device__ const uint64_t kE2m1Lut[16] = {
 // instruction every four to six cycles whatever its code, so seven warps share the page,
 // and the three schedulers with two of them have five blocks each, the one with one warp
 // three (six warps 2% slower, four 13%, three 15%; ten half blocks for each of the three
-// schedulers 4%). 31 requests as above: 390 us; unrolled 443, with the next block's loads
-// in flight 412, a token at a time 410: the roles' loops share the instruction cache, and
-// a shorter loop leaves a warp waiting.
+// schedulers 4%). 31 requests as above, when they took 390 us: unrolled 443, with the next
+// block's loads in flight 412, a token at a time 410: the roles' loops share the
+// instruction cache, and a shorter loop leaves a warp waiting.
 struct ExpandUnit {
   uint4 codes;
   uint2 row;  // of the expansion table
@@ -949,8 +974,13 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
         if (lane == 0) tc::mbar_arrive(bar(BAR_S_EMPTY + (j & 1)));
         float s[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          s[i] = (__uint_as_float(shi[i]) + __uint_as_float(slo[i])) * qmul;
+        for (int i = 0; i < 16; i += 2) {
+          const float2 v = mul2(add2(make_float2(__uint_as_float(shi[i]), __uint_as_float(shi[i + 1])),
+                                     make_float2(__uint_as_float(slo[i]), __uint_as_float(slo[i + 1]))),
+                                make_float2(qmul, qmul));
+          s[i] = v.x;
+          s[i + 1] = v.y;
+        }
         if (nvis < kPageSize) {  // (only a row's last page, or a bad page id, hides tokens)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -1031,11 +1061,15 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
           float rs = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float p0 = fast_exp2(s[4 * k] - mu), p1 = fast_exp2(s[4 * k + 1] - mu);
-            const float p2 = fast_exp2(s[4 * k + 2] - mu), p3 = fast_exp2(s[4 * k + 3] - mu);
+            const float2 a = add2(make_float2(s[4 * k], s[4 * k + 1]), make_float2(-mu, -mu));
+            const float2 b = add2(make_float2(s[4 * k + 2], s[4 * k + 3]), make_float2(-mu, -mu));
+            const float p0 = fast_exp2(a.x), p1 = fast_exp2(a.y), p2 = fast_exp2(b.x), p3 = fast_exp2(b.y);
             hw[k] = e4m3x4_of(p0, p1, p2, p3);
             const float4 hv = e4m3x4_value(hw[k]);
-            lw[k] = e5m2x4_of(p0 - hv.x, p1 - hv.y, p2 - hv.z, p3 - hv.w);
+            const float2 minus = make_float2(-1.f, -1.f);
+            const float2 c = fma2(make_float2(hv.x, hv.y), minus, make_float2(p0, p1));
+            const float2 e = fma2(make_float2(hv.z, hv.w), minus, make_float2(p2, p3));
+            lw[k] = e5m2x4_of(c.x, c.y, e.x, e.y);
             rs += p0 + p1;  // the exact P: lse does not carry the operand rounding
             rs += p2 + p3;
           }
