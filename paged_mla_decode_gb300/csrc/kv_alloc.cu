@@ -269,6 +269,9 @@ __global__ void __launch_bounds__(kAllocThreads)
       for (int32_t x0 = lo + warp * kRows; x0 < to; x0 += warps * kRows) {
         if (x0 + kRows <= from) continue;  // (rows of an earlier chunk)
         const int32_t begin = max(x0, from), end = min(x0 + kRows, to);
+        // None of these rows is this chunk's: it has no rows here (none at all, or the rows
+        // before it end beyond the slot map), and no request of it would be found.
+        if (begin >= end) continue;
         const int i = first_after(sm.row_end, nb, begin);
         if constexpr (kRows == kPageRows) {
           if (i + 2 >= nb || sm.row_end[i + 1] >= end) {
