@@ -181,9 +181,9 @@ MLA_API size_t mla_decode_workspace_size(int batch, int num_queries, int num_hea
  * confined to its tokens below 2^-6 of its largest weight. Each piece of the
  * split (one per CTA) has its own maximum; pieces merge in fp32. An e2m1 cache
  * is expanded to e4m3 codes in shared memory as its pages arrive, which is
- * exact, and then takes the same arithmetic; a visible token that holds a NaN
- * block makes its rows NaN. For a bf16 cache both contractions use bf16
- * operands (kind::f16).
+ * exact, and then takes the same arithmetic. For a bf16 cache both contractions
+ * use bf16 operands (kind::f16). With every cache a NaN among a head's visible
+ * scores (from a cached NaN or from its query) makes that row NaN, out and lse.
  *
  * q           device, bf16 [batch][num_queries][num_heads][576]
  * kv_pages    device, the cache; num_pages pages of page_size (= 64) tokens

@@ -1122,11 +1122,11 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
             const float l = lsum_s[h] + lsum_s[64 + h];
             linv_s[h] = l > 0.f ? p.kv_scale / l : 0.f;
             if (h < H)
-              // (a NaN in a 4-bit page: lse = +inf, with which the merge makes the row NaN)
+              // (a NaN among the scores: lse = +inf, with which the merge makes the row NaN)
               p.ws.part_lse[(int64_t)slot * H + h] =
-                  l > 0.f                 ? (m - (float)kPOffset + log2f(l)) * kLn2
-                  : kE2m1 && !(l == 0.f) ? INFINITY
-                                          : -INFINITY;
+                  l > 0.f    ? (m - (float)kPOffset + log2f(l)) * kLn2
+                  : l == 0.f ? -INFINITY
+                             : INFINITY;
           }
           if (t == 0) p.ws.piece_err[slot] = bad;
           named_bar_softmax();

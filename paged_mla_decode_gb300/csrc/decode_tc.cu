@@ -847,9 +847,12 @@ __global__ void __maxnreg__(168)
             }
           }
           if (t < H) {
+            // (a NaN among the scores: lse = +inf, with which the merge makes the row NaN)
             const float l = l_sum[t];
             p.ws.part_lse[(int64_t)slot * H + t] =
-                l > 0.f ? (m_used[t] - (float)kPOffset + log2f(l)) * kLn2 : -INFINITY;
+                l > 0.f    ? (m_used[t] - (float)kPOffset + log2f(l)) * kLn2
+                : l == 0.f ? -INFINITY
+                           : INFINITY;
           }
           if (t == 0) p.ws.piece_err[slot] = flags[F_PIECE_BAD] ? 1 : 0;
           tc::fence_before_sync();
