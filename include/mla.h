@@ -274,6 +274,7 @@ MLA_API mla_status mla_decode_f16_operands(const void* q, const void* kv_pages, 
  *   out[r] = sum_s exp(part_lse[s][r] - lse[r]) * part_out[s][r][0:512]
  * A part with part_lse = -inf contributes nothing; if all are -inf the row
  * gets out = 0 and lse = -inf.
+ * A part with part_lse = NaN (a NaN row of mla_decode) makes the row NaN.
  *
  * part_out  device, fp32 [num_parts][num_rows][512] (normalised partials)
  * part_lse  device, fp32 [num_parts][num_rows]

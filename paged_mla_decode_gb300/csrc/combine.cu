@@ -6,6 +6,8 @@
 //   lse = ln sum_s exp(lse_s),  out = sum_s exp(lse_s - lse) * out_s.
 // A piece with lse_s = -inf (empty) contributes nothing; a row whose pieces
 // are all empty (or that is flagged bad) gets out = 0 and lse = -inf.
+// A piece with a NaN (lse_s = +inf in a decode's partials, NaN in its results)
+// makes the row NaN.
 #include <algorithm>
 #include <atomic>
 
@@ -28,9 +30,15 @@ __device__ __forceinline__ void merge_row(const float* __restrict__ out_base, in
                                           float* __restrict__ lse_out, float* s_w) {
   __shared__ float s_red[kCombineThreads / 32];
   const int tid = threadIdx.x;
+  // (a NaN lse is taken as +inf: a maximum does not pass a NaN on, and the weight
+  // exp(inf - inf) is one)
+  const auto lse_of = [&](int s) {
+    const float l = lse_base[s * lse_stride];
+    return isnan(l) ? INFINITY : l;
+  };
   float m = -INFINITY;
   if (!bad)
-    for (int s = tid; s < np; s += kCombineThreads) m = fmaxf(m, lse_base[s * lse_stride]);
+    for (int s = tid; s < np; s += kCombineThreads) m = fmaxf(m, lse_of(s));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((tid & 31) == 0) s_red[tid >> 5] = m;
@@ -43,7 +51,7 @@ __device__ __forceinline__ void merge_row(const float* __restrict__ out_base, in
   float total = 0.f;
   if (!empty) {
     for (int s = tid; s < np; s += kCombineThreads) {
-      const float l = lse_base[s * lse_stride];
+      const float l = lse_of(s);
       const float w = (l > -INFINITY) ? fast_exp2((l - m) * kLog2e) : 0.f;
       s_w[s] = w;
       total += w;
