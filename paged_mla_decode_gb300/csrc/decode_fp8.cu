@@ -1238,7 +1238,10 @@ __global__ void __launch_bounds__(kSplitThreads)
     frexpf(amax, &e);
     shift = 8 - e;  // scaled max in [2^7, 2^8)
   }
-  const float sc = ldexpf(1.0f, shift);
+  // (2^shift is no float32 number for a head below 2^-119: then in two factors, both exact)
+  const float pre = shift > 64 ? 0x1p64f : 1.0f, sc = ldexpf(1.0f, shift > 64 ? shift - 64 : shift);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] *= pre;
   uint32_t hw[4], lw[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {

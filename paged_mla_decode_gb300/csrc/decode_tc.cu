@@ -591,7 +591,9 @@ __global__ void __maxnreg__(168)
               frexpf(amax, &e);
               shift = 15 - e;  // scaled max in [2^14, 2^15)
             }
-            const float sc = ldexpf(1.0f, shift);
+            // (2^shift is no float32 number for a head below 2^-112: then in two factors)
+            const float pre = shift > 64 ? 0x1p64f : 1.0f;
+            const float sc = ldexpf(1.0f, shift > 64 ? shift - 64 : shift);
             if (h < H) {
 #pragma unroll 4
               for (int u = 0; u < 36; ++u) {
@@ -605,7 +607,7 @@ __global__ void __maxnreg__(168)
                 for (int q2 = 0; q2 < 4; ++q2) {
                   const float2 f =
                       __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[q2]));
-                  r4[q2] = pack_f2<false>(f.x * sc, f.y * sc);
+                  r4[q2] = pack_f2<false>(f.x * pre * sc, f.y * pre * sc);
                 }
                 asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(r4[0]),
                              "r"(r4[1]), "r"(r4[2]), "r"(r4[3]));
