@@ -183,7 +183,8 @@ MLA_API size_t mla_decode_workspace_size(int batch, int num_queries, int num_hea
  * is expanded to e4m3 codes in shared memory as its pages arrive, which is
  * exact, and then takes the same arithmetic. For a bf16 cache both contractions
  * use bf16 operands (kind::f16). With every cache a NaN among a head's visible
- * scores (from a cached NaN or from its query) makes that row NaN, out and lse.
+ * scores (from a cached NaN, or from a NaN or an infinity in its query) makes
+ * that row NaN, out and lse.
  *
  * q           device, bf16 [batch][num_queries][num_heads][576]
  * kv_pages    device, the cache; num_pages pages of page_size (= 64) tokens

@@ -1238,6 +1238,12 @@ __global__ void __launch_bounds__(kSplitThreads)
     frexpf(amax, &e);
     shift = 8 - e;  // scaled max in [2^7, 2^8)
   }
+  // (e4m3 has no infinity, and the conversion saturates: a head that holds one becomes NaN,
+  // which is the difference of infinities that its softmax comes to)
+  if (isinf(amax)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = NAN;
+  }
   // (2^shift is no float32 number for a head below 2^-119: then in two factors, both exact)
   const float pre = shift > 64 ? 0x1p64f : 1.0f, sc = ldexpf(1.0f, shift > 64 ? shift - 64 : shift);
 #pragma unroll

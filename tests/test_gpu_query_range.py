@@ -40,3 +40,27 @@ def test_tiny_heads(cuda_device, cache, scale):
     out, lse, ws = gpu_decode(w, pages, cuda_device, f16_operands=cache == "f16 operands")
     assert binding.read_device_status(ws) == 0
     assert_close(out, lse, *ref, what=f"{cache}, {scale} scale")
+
+
+@pytest.mark.parametrize("cache", ["e2m1", "e4m3", "bf16", "f16 operands"])
+@pytest.mark.parametrize("bits", [0x7F80, 0xFF80])
+def test_infinity_in_a_head(cuda_device, cache, bits):
+    """Its scores are infinities of both signs, whose differences are NaN: its row alone is NaN."""
+    w = wl.make_lengths_workload("infinite head", 522, [2000, 150], num_heads=16)
+    kw = {"f16_operands": cache == "f16 operands"}
+    if cache == "e2m1":
+        pages, ref_pages = fill(w, cuda_device)
+        ref_out, ref_lse = reference(w, ref_pages)
+    else:
+        dtype = "bf16" if cache == "bf16" else "e4m3"
+        pages = gpu_fill_cache(w, cuda_device, dtype)
+        ref_out, ref_lse = oracle_decode(w, oracle_fill_cache(w, dtype), dtype)
+        if dtype == "bf16":
+            kw["kv_scale"] = 1.0
+    q = w.q_bits.copy()
+    q[0, 0, 5, 33] = bits
+    out, lse, _ = gpu_decode(w, pages, cuda_device, q_bits=q, **kw)
+    assert np.isnan(lse[0, 0, 5]) and np.isnan(out[0, 0, 5]).all()
+    rest = [h for h in range(16) if h != 5]
+    assert_close(out[0, 0, rest], lse[0, 0, rest], ref_out[0, 0, rest], ref_lse[0, 0, rest], what="the other heads")
+    assert_close(out[1], lse[1], ref_out[1], ref_lse[1], what="the other request")
