@@ -991,10 +991,14 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
         for (int i = 0; i < 16; ++i) tm = fmaxf(tm, s[i]);
         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
         if (lane < 16) pmax_s[(j & 1) * 128 + g * 64 + h] = tm;
-        if (!p_free && !flags[F_ABORT] && !tc::mbar_wait(bar(BAR_PV_DONE + slot3), par3, kWaitNs)) {
-          flags[F_ABORT] = 1;
-          stop = true;
-          atomicOr(p.ws.status, MLA_DEVICE_ERR_TIMEOUT);
+        if (!p_free) {  // (nobody goes on to write the P buffer without this wait)
+          if (flags[F_ABORT]) {
+            stop = true;
+          } else if (!tc::mbar_wait(bar(BAR_PV_DONE + slot3), par3, kWaitNs)) {
+            flags[F_ABORT] = 1;
+            stop = true;
+            atomicOr(p.ws.status, MLA_DEVICE_ERR_TIMEOUT);
+          }
         }
         // lazy running max: O is rescaled only when a head's page max rises more than
         // kRescaleThresh above it or falls more than kLowThresh below it; a half
