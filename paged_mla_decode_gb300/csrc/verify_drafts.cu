@@ -89,6 +89,16 @@ __device__ __forceinline__ uint64_t joined(const Slices& w) {
          (uint64_t)(int64_t)w.s[2];
 }
 __device__ __forceinline__ float unit(float u) { return u > 0.f ? fminf(u, 1.f - 0x1p-24f) : 0.f; }
+// floor(u * total) of a uniform u = m * 2^-s (m below 2^24, s from 24 on): the 88-bit product
+// m * total, shifted.
+__device__ __forceinline__ uint64_t share(float u, uint64_t total) {
+  const uint32_t bits = __float_as_uint(u), e = bits >> 23;
+  const uint64_t m = (bits & 0x7fffffu) | (e > 0 ? 0x800000u : 0u);
+  const int s = 150 - (int)max(e, 1u);
+  const uint64_t hi = __umul64hi(m, total), lo = m * total;
+  if (s >= 64) return s < 128 ? hi >> (s - 64) : 0;
+  return (hi << (64 - s)) | (lo >> s);
+}
 
 // The distribution that the next token is drawn from: p, or what a rejection leaves of it.
 template <class T>
@@ -279,7 +289,7 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kBlocksPerSm)
     }
   }
   // the border: the first token whose running sum exceeds u * total, in integers
-  const uint64_t at = __umul64hi(__float2ull_rz(unit(u_sample) * 0x1p64f), total);
+  const uint64_t at = share(unit(u_sample), total);
   int w = 0;
   while (w < kVerifyWarps && before + s_warp[w] <= at) before += s_warp[w++];
   if (total == 0 || at < before || w == kVerifyWarps) {  // in another block's run
