@@ -345,7 +345,7 @@ MLA_API mla_status mla_kv_gather(const void* kv_pages, int64_t num_pages, int pa
  * block_table     device, int32 [batch][max_pages], updated in place
  * page_tags       device, uint32 [num_pages], updated in place; or NULL
  * expected_tags   device, uint32 [batch][max_pages], updated in place; NULL
- *                 exactly if page_tags is
+ *                 exactly if page_tags is (without requests or pages either may be)
  * seq_lens_out, pages_held_out  device, int32 [batch]
  * free_count_out  device, int32
  *                 Each output of these three may be the same buffer as its

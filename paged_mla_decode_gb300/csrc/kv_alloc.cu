@@ -330,7 +330,9 @@ extern "C" mla_status mla_kv_alloc(const int32_t* seq_lens, const int32_t* new_t
     return MLA_ERR_INVALID_ARG;
   if ((free_capacity > 0 && !free_pages) || (num_slots > 0 && !slot_mapping))
     return MLA_ERR_INVALID_ARG;
-  if ((page_tags == nullptr) != (expected_tags == nullptr)) return MLA_ERR_INVALID_ARG;
+  // (an array without an entry may have no address)
+  if (batch > 0 && num_pages > 0 && (page_tags == nullptr) != (expected_tags == nullptr))
+    return MLA_ERR_INVALID_ARG;
   const void* ptrs[14] = {seq_lens,      new_tokens,   pages_held,     free_pages,     free_count,
                           block_table,   page_tags,    expected_tags,  seq_lens_out,   pages_held_out,
                           free_count_out, cu_tokens,   slot_mapping,   request_status};
