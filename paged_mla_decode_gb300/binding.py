@@ -262,11 +262,12 @@ def mla_decode_grouped(q: torch.Tensor, kv_pages: torch.Tensor, block_table: tor
     assert block_table.dtype == torch.int32 and block_table.dim() == 2
     assert block_table.is_contiguous() and block_table.shape[0] == batch
     assert seq_lens.dtype == torch.int32 and seq_lens.numel() == batch
-    assert prefix_pages.dtype == torch.int32 and prefix_pages.is_contiguous()
+    assert prefix_pages.dtype == torch.int32
+    assert forks < 1 or prefix_pages.numel() * forks >= batch  # (the library refuses such forks)
     assert out.dtype == torch.bfloat16 and tuple(out.shape) == (batch, nq, heads, 512)
     assert lse.dtype == torch.float32 and tuple(lse.shape) == (batch, nq, heads)
     dtype = kv_dtype_code(kv_pages)
-    _same_device(_device_of(kv_pages), q, block_table, seq_lens, out, lse, workspace)
+    _same_device(_device_of(kv_pages), q, block_table, seq_lens, prefix_pages, out, lse, workspace)
     st = load_library().mla_decode_grouped(
         _ptr(q), _ptr(kv_pages), int(kv_pages.shape[0]), _page_size(kv_pages),
         dtype, _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
@@ -281,10 +282,10 @@ def mla_decode_combine(part_out: torch.Tensor, part_lse: torch.Tensor, out: torc
     """Merge ``part_out [S, R, 512]`` / ``part_lse [S, R]`` into ``out [R, 512]`` / ``lse [R]``."""
     assert part_out.dtype == torch.float32 and part_lse.dtype == torch.float32
     num_parts, rows = int(part_lse.shape[0]), int(part_lse.shape[1])
-    assert tuple(part_out.shape) == (num_parts, rows, 512) and part_out.is_contiguous()
-    assert part_lse.is_contiguous()
-    assert out.dtype == torch.bfloat16 and out.numel() == rows * 512 and out.is_contiguous()
+    assert tuple(part_out.shape) == (num_parts, rows, 512)
+    assert out.dtype == torch.bfloat16 and out.numel() == rows * 512
     assert lse.dtype == torch.float32 and lse.numel() == rows
+    _same_device(_device_of(out), part_out, part_lse, out, lse)
     st = load_library().mla_decode_combine(_ptr(part_out), _ptr(part_lse), num_parts, rows,
                                            _ptr(out), _ptr(lse), _stream(stream))
     _check(st, "mla_decode_combine")
@@ -303,15 +304,15 @@ def mla_kv_check(page_tags: torch.Tensor, block_table: torch.Tensor,
     -1 for every request that failed), to be passed to mla_decode as seq_lens.
     """
     tag_types = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
-    assert page_tags.dtype in tag_types and page_tags.dim() == 1 and page_tags.is_contiguous()
+    assert page_tags.dtype in tag_types and page_tags.dim() == 1
     assert block_table.dtype == torch.int32 and block_table.dim() == 2
-    assert block_table.is_contiguous()
     batch, max_pages = int(block_table.shape[0]), int(block_table.shape[1])
-    assert expected_tags.dtype in tag_types and expected_tags.is_contiguous()
-    assert tuple(expected_tags.shape) == (batch, max_pages)
+    assert expected_tags.dtype in tag_types and tuple(expected_tags.shape) == (batch, max_pages)
     assert seq_lens.dtype == torch.int32 and seq_lens.numel() == batch
     assert request_status.dtype in tag_types and request_status.numel() == batch
     assert checked_seq_lens.dtype == torch.int32 and checked_seq_lens.numel() == batch
+    _same_device(_device_of(block_table), page_tags, block_table, expected_tags, seq_lens,
+                 request_status, checked_seq_lens)
     st = load_library().mla_kv_check(_ptr(page_tags), int(page_tags.numel()), _ptr(block_table),
                                      _ptr(expected_tags), max_pages, _ptr(seq_lens), batch, 64,
                                      _ptr(request_status), _ptr(checked_seq_lens),
@@ -472,9 +473,11 @@ def mla_decode_static_scratch(q: torch.Tensor, kv_pages: torch.Tensor,
     assert out.dtype == torch.bfloat16 and tuple(out.shape) == (batch, nq, heads, 512)
     assert lse.dtype == torch.float32 and tuple(lse.shape) == (batch, nq, heads)
     dtype = kv_dtype_code(kv_pages)
-    _same_device(_device_of(kv_pages), q, block_table, seq_lens, out, lse)
+    device = _device_of(kv_pages)
+    _same_device(device, q, block_table, seq_lens, out, lse)
     if device_status is not None:
         assert device_status.dtype == torch.int32 and device_status.numel() >= 1
+        _same_device(device, device_status)
     st = load_library().mla_decode_static_scratch(
         _ptr(q), _ptr(kv_pages), int(kv_pages.shape[0]), _page_size(kv_pages),
         dtype, _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
