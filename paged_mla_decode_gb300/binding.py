@@ -150,17 +150,26 @@ def _check(status: int, where: str):
         raise MlaError(status, where)
 
 
+def _refuse(what: str):
+    """An argument that the library cannot check. (Not an assert statement: python -O drops those,
+    and the pointer would go to a kernel.)"""
+    raise AssertionError(what)
+
+
 def kv_dtype_code(kv_pages: torch.Tensor) -> int:
     """The cache's element type, from its tensor (and a check of its shape).
 
     uint8 ``[num_pages, 64, 576]`` holds e4m3 codes, bfloat16 of that shape bf16
     values, uint8 ``[num_pages, 19008]`` e2m1 pages.
     """
-    assert kv_pages.is_contiguous()
+    if not kv_pages.is_contiguous():
+        _refuse("kv_pages is not contiguous")
     if kv_pages.dtype == torch.uint8 and kv_pages.dim() == 2:
-        assert kv_pages.shape[1] == MLA_E2M1_PAGE_BYTES
+        if kv_pages.shape[1] != MLA_E2M1_PAGE_BYTES:
+            _refuse("kv_pages of an e2m1 cache are [num_pages, 19008]")
         return MLA_KV_E2M1
-    assert kv_pages.dim() == 3 and kv_pages.shape[2] == 576
+    if kv_pages.dim() != 3 or kv_pages.shape[2] != 576:
+        _refuse("kv_pages are [num_pages, 64, 576]")
     if kv_pages.dtype == torch.uint8:
         return MLA_KV_E4M3
     if kv_pages.dtype == torch.bfloat16:
@@ -179,30 +188,57 @@ _I32, _U32 = torch.int32, torch.uint32
 def _int32(device: int, *tensors) -> None:
     """Each tensor is a contiguous int32 (for tags and status words also uint32) one on `device`."""
     for t in tensors:
-        assert t.dtype is _I32 or t.dtype is _U32
-        assert t.is_contiguous() and t.get_device() == device
+        if t.dtype is not _I32 and t.dtype is not _U32:
+            _refuse("an index tensor is not int32")
+        if not t.is_contiguous() or t.get_device() != device:
+            _refuse("an index tensor is not contiguous, or on another device")
 
 
 def _device_of(t: torch.Tensor) -> int:
     """The tensor's CUDA device, which must be the current one (the library launches there)."""
     device = t.get_device()
-    assert t.is_cuda and device == torch.cuda.current_device()
+    if not t.is_cuda or device != torch.cuda.current_device():
+        _refuse("a tensor is not on the current CUDA device")
     return device
 
 
 def _same_device(device: int, *tensors) -> None:
     """Each tensor is contiguous and on `device`: its pointer is all the library gets."""
     for t in tensors:
-        assert t.is_contiguous() and t.get_device() == device
+        if not t.is_contiguous() or t.get_device() != device:
+            _refuse("a tensor is not contiguous, or on another device")
+
+
+def _entries(latent: torch.Tensor, rope: torch.Tensor, rows: int) -> None:
+    if latent.dtype != torch.bfloat16 or latent.shape != (rows, 512):
+        _refuse("latent is bfloat16 [tokens, 512]")
+    if rope.dtype != torch.bfloat16 or rope.shape != (rows, 64):
+        _refuse("rope is bfloat16 [tokens, 64]")
+
+
+def _decode_shape(q, block_table, seq_lens, out, lse):
+    """Batch, queries and heads of a decode, whose types and shapes fit."""
+    if q.dtype != torch.bfloat16 or q.dim() != 4 or q.shape[3] != 576:
+        _refuse("q is bfloat16 [batch, queries, heads, 576]")
+    batch, nq, heads, _ = q.shape
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch:
+        _refuse("block_table is int32 [batch, max_pages]")
+    if seq_lens.dtype != torch.int32 or seq_lens.numel() != batch:
+        _refuse("seq_lens is int32 [batch]")
+    if out.dtype != torch.bfloat16 or out.shape != (batch, nq, heads, 512):
+        _refuse("out is bfloat16 [batch, queries, heads, 512]")
+    if lse.dtype != torch.float32 or lse.shape != (batch, nq, heads):
+        _refuse("lse is float32 [batch, queries, heads]")
+    return batch, nq, heads
 
 
 def mla_kv_append(latent: torch.Tensor, rope: torch.Tensor, slot_mapping: torch.Tensor,
                   kv_pages: torch.Tensor, kv_scale: float, stream=None) -> None:
     """Write tokens' 512 latent + 64 rope elements into their cache slots."""
     num_tokens = int(slot_mapping.numel())
-    assert latent.dtype == torch.bfloat16 and rope.dtype == torch.bfloat16
-    assert slot_mapping.dtype == torch.int32
-    assert latent.shape == (num_tokens, 512) and rope.shape == (num_tokens, 64)
+    if slot_mapping.dtype != torch.int32:
+        _refuse("slot_mapping is int32")
+    _entries(latent, rope, num_tokens)
     dtype = kv_dtype_code(kv_pages)
     _same_device(_device_of(kv_pages), latent, rope, slot_mapping)
     st = load_library().mla_kv_append(_ptr(latent), _ptr(rope), _ptr(slot_mapping), num_tokens,
@@ -226,13 +262,7 @@ def mla_decode(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tenso
     ``kv_pages`` as in :func:`kv_dtype_code` (e4m3, bf16 or e2m1 pages).
     ``f16_operands`` calls mla_decode_f16_operands (the e4m3 cache widened to f16
     operands) instead of mla_decode."""
-    assert q.dtype == torch.bfloat16 and q.dim() == 4 and q.shape[3] == 576 and q.is_contiguous()
-    batch, nq, heads, _ = q.shape
-    assert block_table.dtype == torch.int32 and block_table.dim() == 2
-    assert block_table.is_contiguous() and block_table.shape[0] == batch
-    assert seq_lens.dtype == torch.int32 and seq_lens.numel() == batch
-    assert out.dtype == torch.bfloat16 and tuple(out.shape) == (batch, nq, heads, 512)
-    assert lse.dtype == torch.float32 and tuple(lse.shape) == (batch, nq, heads)
+    batch, nq, heads = _decode_shape(q, block_table, seq_lens, out, lse)
     dtype = kv_dtype_code(kv_pages)
     _same_device(_device_of(kv_pages), q, block_table, seq_lens, out, lse, workspace)
     lib = load_library()
@@ -257,15 +287,9 @@ def mla_decode_grouped(q: torch.Tensor, kv_pages: torch.Tensor, block_table: tor
                        sm_scale: float, kv_scale: float, out: torch.Tensor, lse: torch.Tensor,
                        workspace: torch.Tensor, num_ctas: int = 0, stream=None) -> None:
     """mla_decode for groups of ``forks`` requests sharing ``prefix_pages[g]`` pages."""
-    assert q.dtype == torch.bfloat16 and q.dim() == 4 and q.shape[3] == 576 and q.is_contiguous()
-    batch, nq, heads, _ = q.shape
-    assert block_table.dtype == torch.int32 and block_table.dim() == 2
-    assert block_table.is_contiguous() and block_table.shape[0] == batch
-    assert seq_lens.dtype == torch.int32 and seq_lens.numel() == batch
-    assert prefix_pages.dtype == torch.int32
-    assert forks < 1 or prefix_pages.numel() * forks >= batch  # (the library refuses such forks)
-    assert out.dtype == torch.bfloat16 and tuple(out.shape) == (batch, nq, heads, 512)
-    assert lse.dtype == torch.float32 and tuple(lse.shape) == (batch, nq, heads)
+    batch, nq, heads = _decode_shape(q, block_table, seq_lens, out, lse)
+    if prefix_pages.dtype != torch.int32 or prefix_pages.numel() * max(forks, 1) < batch:
+        _refuse("prefix_pages is int32 [batch / forks]")
     dtype = kv_dtype_code(kv_pages)
     _same_device(_device_of(kv_pages), q, block_table, seq_lens, prefix_pages, out, lse, workspace)
     st = load_library().mla_decode_grouped(
@@ -280,11 +304,15 @@ def mla_decode_grouped(q: torch.Tensor, kv_pages: torch.Tensor, block_table: tor
 def mla_decode_combine(part_out: torch.Tensor, part_lse: torch.Tensor, out: torch.Tensor,
                        lse: torch.Tensor, stream=None) -> None:
     """Merge ``part_out [S, R, 512]`` / ``part_lse [S, R]`` into ``out [R, 512]`` / ``lse [R]``."""
-    assert part_out.dtype == torch.float32 and part_lse.dtype == torch.float32
+    if part_out.dtype != torch.float32 or part_lse.dtype != torch.float32 or part_lse.dim() != 2:
+        _refuse("part_out and part_lse are float32 [parts, rows, 512] and [parts, rows]")
     num_parts, rows = int(part_lse.shape[0]), int(part_lse.shape[1])
-    assert tuple(part_out.shape) == (num_parts, rows, 512)
-    assert out.dtype == torch.bfloat16 and out.numel() == rows * 512
-    assert lse.dtype == torch.float32 and lse.numel() == rows
+    if part_out.shape != (num_parts, rows, 512):
+        _refuse("part_out is [parts, rows, 512]")
+    if out.dtype != torch.bfloat16 or out.numel() != rows * 512:
+        _refuse("out is bfloat16 [rows, 512]")
+    if lse.dtype != torch.float32 or lse.numel() != rows:
+        _refuse("lse is float32 [rows]")
     _same_device(_device_of(out), part_out, part_lse, out, lse)
     st = load_library().mla_decode_combine(_ptr(part_out), _ptr(part_lse), num_parts, rows,
                                            _ptr(out), _ptr(lse), _stream(stream))
@@ -303,14 +331,20 @@ def mla_kv_check(page_tags: torch.Tensor, block_table: torch.Tensor,
     (MLA_KV_CHECK_* bits, int32) and ``checked_seq_lens [batch]`` (the lengths,
     -1 for every request that failed), to be passed to mla_decode as seq_lens.
     """
-    tag_types = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
-    assert page_tags.dtype in tag_types and page_tags.dim() == 1
-    assert block_table.dtype == torch.int32 and block_table.dim() == 2
+    tag_types = (_I32, _U32)
+    if page_tags.dtype not in tag_types or page_tags.dim() != 1:
+        _refuse("page_tags is int32 or uint32 [num_pages]")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        _refuse("block_table is int32 [batch, max_pages]")
     batch, max_pages = int(block_table.shape[0]), int(block_table.shape[1])
-    assert expected_tags.dtype in tag_types and tuple(expected_tags.shape) == (batch, max_pages)
-    assert seq_lens.dtype == torch.int32 and seq_lens.numel() == batch
-    assert request_status.dtype in tag_types and request_status.numel() == batch
-    assert checked_seq_lens.dtype == torch.int32 and checked_seq_lens.numel() == batch
+    if expected_tags.dtype not in tag_types or expected_tags.shape != (batch, max_pages):
+        _refuse("expected_tags is int32 or uint32 [batch, max_pages]")
+    if seq_lens.dtype != torch.int32 or seq_lens.numel() != batch:
+        _refuse("seq_lens is int32 [batch]")
+    if request_status.dtype not in tag_types or request_status.numel() != batch:
+        _refuse("request_status is int32 or uint32 [batch]")
+    if checked_seq_lens.dtype != torch.int32 or checked_seq_lens.numel() != batch:
+        _refuse("checked_seq_lens is int32 [batch]")
     _same_device(_device_of(block_table), page_tags, block_table, expected_tags, seq_lens,
                  request_status, checked_seq_lens)
     st = load_library().mla_kv_check(_ptr(page_tags), int(page_tags.numel()), _ptr(block_table),
@@ -332,18 +366,19 @@ def mla_kv_gather(kv_pages: torch.Tensor, kv_scale: float, block_table: torch.Te
     :func:`kv_dtype_code`.
     """
     dtype, device = kv_dtype_code(kv_pages), _device_of(kv_pages)
-    assert block_table.dim() == 2
+    if block_table.dim() != 2:
+        _refuse("block_table is [batch, max_pages]")
     batch, max_pages = block_table.shape
     rows = latent.shape[0]
     _int32(device, block_table, cu_tokens)
-    assert cu_tokens.dim() == 1 and cu_tokens.shape[0] == batch + 1
+    if cu_tokens.dim() != 1 or cu_tokens.shape[0] != batch + 1:
+        _refuse("cu_tokens is [batch + 1]")
     if starts is not None:
         _int32(device, starts)
-        assert starts.numel() == batch
-    assert latent.dtype == torch.bfloat16 and rope.dtype == torch.bfloat16
-    assert latent.shape == (rows, 512) and rope.shape == (rows, 64)
-    assert latent.is_contiguous() and rope.is_contiguous()
-    assert latent.get_device() == device and rope.get_device() == device
+        if starts.numel() != batch:
+            _refuse("starts is [batch]")
+    _entries(latent, rope, rows)
+    _same_device(device, latent, rope)
     st = load_library().mla_kv_gather(kv_pages.data_ptr(), kv_pages.shape[0],
                                       _page_size(kv_pages), dtype, kv_scale,
                                       block_table.data_ptr(), max_pages, _ptr(starts),
@@ -371,19 +406,23 @@ def mla_kv_alloc(seq_lens: torch.Tensor, new_tokens: torch.Tensor, pages_held: t
     length -1 and slots -1).
     """
     device = _device_of(block_table)
-    assert block_table.dim() == 2
+    if block_table.dim() != 2:
+        _refuse("block_table is [batch, max_pages]")
     batch, max_pages = block_table.shape
     _int32(device, seq_lens, new_tokens, pages_held, free_pages, free_count, block_table,
            seq_lens_out, pages_held_out, free_count_out, cu_tokens, slot_mapping, request_status)
-    assert seq_lens.numel() == batch and new_tokens.numel() == batch
-    assert pages_held.numel() == batch and pages_held_out.numel() == batch
-    assert seq_lens_out.numel() == batch and request_status.numel() == batch
-    assert free_count.numel() == 1 and free_count_out.numel() == 1
-    assert cu_tokens.numel() == batch + 1
-    assert (page_tags is None) == (expected_tags is None)
+    if (seq_lens.numel() != batch or new_tokens.numel() != batch or pages_held.numel() != batch
+            or pages_held_out.numel() != batch or seq_lens_out.numel() != batch
+            or request_status.numel() != batch):
+        _refuse("lengths, pages held and status words are [batch]")
+    if free_count.numel() != 1 or free_count_out.numel() != 1 or cu_tokens.numel() != batch + 1:
+        _refuse("free_count and free_count_out have one element, cu_tokens batch + 1")
+    if (page_tags is None) != (expected_tags is None):
+        _refuse("page_tags and expected_tags are given together")
     if page_tags is not None:
         _int32(device, page_tags, expected_tags)
-        assert page_tags.numel() == num_pages and expected_tags.shape == block_table.shape
+        if page_tags.numel() != num_pages or expected_tags.shape != block_table.shape:
+            _refuse("page_tags is [num_pages], expected_tags [batch, max_pages]")
     st = load_library().mla_kv_alloc(
         seq_lens.data_ptr(), new_tokens.data_ptr(), batch, 64, pages_held.data_ptr(),
         free_pages.data_ptr(), free_count.data_ptr(), free_pages.numel(), num_pages,
@@ -397,9 +436,11 @@ def mla_kv_alloc(seq_lens: torch.Tensor, new_tokens: torch.Tensor, pages_held: t
 def _row_stride(probs: torch.Tensor) -> int:
     """Elements between the rows of ``[batch, rows, vocab]`` probabilities, evenly apart."""
     batch, rows, vocab = probs.shape
-    assert vocab == 1 or probs.stride(2) == 1
+    if vocab != 1 and probs.stride(2) != 1:
+        _refuse("a row of probabilities is not contiguous")
     stride = probs.stride(1) if rows > 1 else probs.stride(0) if batch > 1 else vocab
-    assert stride >= vocab and (batch == 1 or probs.stride(0) == rows * stride)
+    if stride < vocab or (batch != 1 and probs.stride(0) != rows * stride):
+        _refuse("the rows of probabilities are not evenly apart")
     return stride
 
 
@@ -420,30 +461,38 @@ def mla_verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | No
     ``num_accepted [batch]`` and, given ``seq_lens``, ``seq_lens_out``: the
     lengths without the rejected drafts (may be ``seq_lens`` itself).
     """
-    assert target_probs.dim() == 3
+    if target_probs.dim() != 3:
+        _refuse("target_probs is [batch, drafts + 1, vocab]")
     device = _device_of(target_probs)
     batch, rows, vocab = target_probs.shape
     drafts = rows - 1
-    assert target_probs.dtype in (torch.float32, torch.bfloat16)
+    if target_probs.dtype not in (torch.float32, torch.bfloat16):
+        _refuse("target_probs is float32 or bfloat16")
     dtype = MLA_PROB_F32 if target_probs.dtype == torch.float32 else MLA_PROB_BF16
     target_stride = _row_stride(target_probs) if batch > 0 else vocab
     draft_stride = vocab
     if draft_probs is not None:
-        assert draft_probs.dtype == target_probs.dtype
-        assert draft_probs.get_device() == device
-        assert draft_probs.shape == (batch, drafts, vocab)
+        if draft_probs.dtype != target_probs.dtype or draft_probs.shape != (batch, drafts, vocab):
+            _refuse("draft_probs is [batch, drafts, vocab], of target_probs' type")
+        if draft_probs.get_device() != device:
+            _refuse("draft_probs is on another device")
         if batch > 0 and drafts > 0:
             draft_stride = _row_stride(draft_probs)
-    assert draft_tokens.shape == (batch, drafts) and out_tokens.shape == (batch, rows)
-    assert uniforms.dtype == torch.float32 and uniforms.shape == (batch, rows)
-    assert uniforms.is_contiguous() and uniforms.get_device() == device
-    assert num_accepted.numel() == batch
+    if draft_tokens.shape != (batch, drafts) or out_tokens.shape != (batch, rows):
+        _refuse("draft_tokens is [batch, drafts], out_tokens [batch, drafts + 1]")
+    if uniforms.dtype != torch.float32 or uniforms.shape != (batch, rows):
+        _refuse("uniforms is float32 [batch, drafts + 1]")
+    _same_device(device, uniforms)
+    if num_accepted.numel() != batch:
+        _refuse("num_accepted is [batch]")
     _int32(device, draft_tokens, out_tokens, num_accepted)
-    assert seq_lens_out is None or seq_lens is not None
+    if seq_lens_out is not None and seq_lens is None:
+        _refuse("seq_lens_out needs seq_lens")
     for t in (num_drafts, seq_lens, seq_lens_out):
         if t is not None:
             _int32(device, t)
-            assert t.numel() == batch
+            if t.numel() != batch:
+                _refuse("num_drafts, seq_lens and seq_lens_out are [batch]")
     st = load_library().mla_verify_drafts(
         target_probs.data_ptr(), target_stride, _ptr(draft_probs), draft_stride, dtype,
         draft_tokens.data_ptr(), uniforms.data_ptr(), _ptr(num_drafts), _ptr(seq_lens), batch,
@@ -465,18 +514,13 @@ def mla_decode_static_scratch(q: torch.Tensor, kv_pages: torch.Tensor,
     capture. ``device_status`` (int32, one element, optional) receives the call's
     MLA_DEVICE_ERR_* bits.
     """
-    assert q.dtype == torch.bfloat16 and q.dim() == 4 and q.shape[3] == 576 and q.is_contiguous()
-    batch, nq, heads, _ = q.shape
-    assert block_table.dtype == torch.int32 and block_table.dim() == 2
-    assert block_table.is_contiguous() and block_table.shape[0] == batch
-    assert seq_lens.dtype == torch.int32 and seq_lens.numel() == batch
-    assert out.dtype == torch.bfloat16 and tuple(out.shape) == (batch, nq, heads, 512)
-    assert lse.dtype == torch.float32 and tuple(lse.shape) == (batch, nq, heads)
+    batch, nq, heads = _decode_shape(q, block_table, seq_lens, out, lse)
     dtype = kv_dtype_code(kv_pages)
     device = _device_of(kv_pages)
     _same_device(device, q, block_table, seq_lens, out, lse)
     if device_status is not None:
-        assert device_status.dtype == torch.int32 and device_status.numel() >= 1
+        if device_status.dtype != torch.int32 or device_status.numel() < 1:
+            _refuse("device_status is int32, one element")
         _same_device(device, device_status)
     st = load_library().mla_decode_static_scratch(
         _ptr(q), _ptr(kv_pages), int(kv_pages.shape[0]), _page_size(kv_pages),

@@ -1,11 +1,17 @@
 """The binding refuses, for every entry point, tensors whose pointer the library cannot use: host
 tensors, strided ones, arrays that are too short."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 from paged_mla_decode_gb300 import binding
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _check_args(dev):
@@ -71,3 +77,44 @@ def test_device_status_of_the_static_scratch(cuda_device):
     for bad in (status.cpu(), status[:0], status.long()):
         with pytest.raises(AssertionError):
             binding.mla_decode_static_scratch(**a, device_status=bad)
+
+
+def test_refusals_stand_without_assert_statements():
+    """python -O drops assert statements; the checks stay. (Host tensors, so that no call could
+    reach a kernel.)"""
+    code = """
+import torch
+from paged_mla_decode_gb300 import binding as b
+bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+f32 = lambda *s: torch.zeros(s)
+pages = torch.zeros(2, 64, 576, dtype=torch.uint8)
+dec = (bf(1, 1, 16, 576), pages, i32(1, 2), i32(1))
+out = (bf(1, 1, 16, 512), f32(1, 1, 16))
+ws = torch.zeros(9, dtype=torch.uint8)
+calls = {
+    "append": lambda: b.mla_kv_append(bf(3, 512), bf(3, 64), i32(3), pages, 1.0),
+    "decode": lambda: b.mla_decode(*dec, 0.1, 1.0, *out, ws),
+    "grouped": lambda: b.mla_decode_grouped(*dec, 1, i32(1), 0.1, 1.0, *out, ws),
+    "static": lambda: b.mla_decode_static_scratch(*dec, 0.1, 1.0, *out),
+    "combine": lambda: b.mla_decode_combine(f32(2, 3, 512), f32(2, 3), bf(3, 512), f32(3)),
+    "check": lambda: b.mla_kv_check(i32(2), i32(1, 2), i32(1, 2), i32(1), i32(1), i32(1)),
+    "gather": lambda: b.mla_kv_gather(pages, 1.0, i32(1, 2), i32(2), bf(3, 512), bf(3, 64)),
+    "alloc": lambda: b.mla_kv_alloc(i32(1), i32(1), i32(1), i32(4), i32(1), 4, i32(1, 2), i32(1), i32(1), i32(1),
+                                    i32(2), i32(3), i32(1)),
+    "verify": lambda: b.mla_verify_drafts(f32(1, 2, 5), None, i32(1, 1), f32(1, 2), i32(1, 2), i32(1)),
+    "pages": lambda: b.kv_dtype_code(pages[:, :, :575]),
+    "stride": lambda: b._row_stride(f32(2, 3, 10)[..., ::2]),
+}
+b.load_library = lambda *a: print("reached the library")
+for name, call in calls.items():
+    try:
+        call()
+    except AssertionError as e:
+        print(name, "refused")
+"""
+    for flags in ([], ["-O"]):
+        run = subprocess.run([sys.executable, *flags, "-c", code], capture_output=True, text=True, cwd=ROOT)
+        got = run.stdout.split("\n")[:-1]
+        assert run.returncode == 0 and len(got) == 11, run.stdout + run.stderr
+        assert all(line.endswith(" refused") for line in got), got
