@@ -89,15 +89,12 @@ __device__ __forceinline__ uint64_t joined(const Slices& w) {
          (uint64_t)(int64_t)w.s[2];
 }
 __device__ __forceinline__ float unit(float u) { return u > 0.f ? fminf(u, 1.f - 0x1p-24f) : 0.f; }
-// floor(u * total) of a uniform u = m * 2^-s (m below 2^24, s from 24 on): the 88-bit product
-// m * total, shifted.
+// floor(u * total) for a uniform u, which from 2^-41 on is a multiple of 2^-64; a smaller one is
+// first raised by a power of two (as exact as the rest, and no time where there is none).
 __device__ __forceinline__ uint64_t share(float u, uint64_t total) {
-  const uint32_t bits = __float_as_uint(u), e = bits >> 23;
-  const uint64_t m = (bits & 0x7fffffu) | (e > 0 ? 0x800000u : 0u);
-  const int s = 150 - (int)max(e, 1u);
-  const uint64_t hi = __umul64hi(m, total), lo = m * total;
-  if (s >= 64) return s < 128 ? hi >> (s - 64) : 0;
-  return (hi << (64 - s)) | (lo >> s);
+  int shift = 0;
+  while (__builtin_expect(u > 0.f && u < 0x1p-41f, 0)) u *= 0x1p20f, shift += 20;
+  return __umul64hi(__float2ull_rz(u * 0x1p64f), total) >> min(shift, 63);
 }
 
 // The distribution that the next token is drawn from: p, or what a rejection leaves of it.
