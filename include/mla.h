@@ -385,7 +385,13 @@ MLA_API mla_status mla_kv_alloc(const int32_t* seq_lens, const int32_t* new_toke
  *   w_0 + .. + w_i > uniforms[b][max_drafts] * (w_0 + .. + w_{vocab-1});
  *   out_tokens[b] = x_0 .. x_{a-1}, the next token, then -1;
  *   seq_lens_out[b] = seq_lens[b] - (k - a), the cached tokens that stay
- *   (seq_lens[b] counts the k + 1 queries of the step, as for mla_decode).
+ *   (seq_lens[b] counts the k + 1 queries of the step).
+ * A call of mla_decode has max_drafts + 1 queries for every request, the last of
+ * them the last cached token. So a request with k < max_drafts drafts is cached
+ * and decoded with max_drafts + 1 new tokens, anything behind its drafts, which
+ * gives row j of target_probs the output of query j; here it passes the length
+ * without that padding, mla_decode's less max_drafts - k. The padding's slots
+ * are the next step's.
  * With draft_probs NULL, q_j puts all its weight on x_j: u_j < p_j(x_j), and the
  * rest is p_a without x_a. A draft outside [0, vocab) is rejected. If all
  * weights are zero the next token is -1. A request with k outside
