@@ -7,8 +7,7 @@ kernel does it; the benchmark divides them by measured time.
   for trillion-parameter coding agents", section "Tensor parallel was the best
   parallelism strategy for maximum interactivity"), one byte each in FP8 e4m3
   or two in BF16 ("Smaller, faster, safer: running Kimi and GLM at scale",
-  section "Quantizing the KV cache"), 297 bytes in the 4-bit e2m1 cache (32
-  elements share an exponent nibble). A decode step reads every unique page
+  section "Quantizing the KV cache"). A decode step reads every unique page
   once, plus 4 bytes of block table per page, plus queries, and writes outputs.
 * Flops: per cached token and query row, 2*576 for the score and 2*512 for the
   weighted value sum.
@@ -22,12 +21,11 @@ D_ENTRY = 576
 D_LATENT = 512
 
 KV_ELEMENT_BYTES = {"e4m3": 1, "bf16": 2}
-E2M1_TOKEN_BYTES = D_ENTRY // 2 + D_ENTRY // 32 // 2  # codes, and a nibble per 32 elements: 297
 
 
 def kv_bytes_per_token(kv_dtype: str) -> int:
     """Bytes of one cached token's latent entry for one layer."""
-    return E2M1_TOKEN_BYTES if kv_dtype == "e2m1" else D_ENTRY * KV_ELEMENT_BYTES[kv_dtype]
+    return D_ENTRY * KV_ELEMENT_BYTES[kv_dtype]
 
 
 def flops_per_token_row() -> int:
