@@ -349,12 +349,16 @@ MLA_API mla_status mla_kv_gather(const void* kv_pages, int64_t num_pages, int pa
  * seq_lens_out, pages_held_out  device, int32 [batch]
  * free_count_out  device, int32
  *                 Each output of these three may be the same buffer as its
- *                 input, so that a captured step can be replayed.
+ *                 input, so that a captured step can be replayed. (The length of a
+ *                 refused request is then gone: keep seq_lens apart, or a copy,
+ *                 where refused requests are to be tried again.)
  * cu_tokens       device, int32 [batch + 1] (saturates at 2^31 - 1)
  * slot_mapping    device, int32 [num_slots]
  * request_status  device, uint32 [batch]
  * Pointers need 4-byte alignment here. A page named twice by the free list, or
- * free and held, is the caller's error.
+ * free and held, is the caller's error. Pages come back to the list by the
+ * caller's own writes: a finished request's block-table entries, behind the
+ * first *free_count.
  */
 #define MLA_KV_ALLOC_BAD_LENGTH 0x1u
 #define MLA_KV_ALLOC_TABLE_FULL 0x2u

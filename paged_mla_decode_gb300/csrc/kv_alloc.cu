@@ -28,8 +28,9 @@ constexpr int kAllocThreads = 1024;    // at most; a step's few rows take fewer
 constexpr int kAllocWarps = kAllocThreads / 32;
 constexpr int64_t kBlockRows = 4096;   // rows that are worth a block of their own
 // Rows that a warp fills at a time, with one search for their request: 32 in a step of few
-// rows, 128 in larger calls, and 512 where requests are long (4,096 rows each on average):
-// there most runs have one or two requests, and the warp looks their pages up at once. 32
+// rows, 128 in larger calls, and 512 where the slot map has 4,096 entries a request (its size
+// is what the host knows; a map that is much larger than its rows is taken for one of long
+// requests): there most runs have one or two requests, and the warp looks their pages up at once. 32
 // requests of 60k-140k new tokens take 10.3 us so (16.5 with 128 rows a time, each row its
 // own lookup), 512 of 100-5,000 13.9 (12.3), 256 of four 15 (8.2); between 1,000 and 4,000
 // rows a request the two are even.

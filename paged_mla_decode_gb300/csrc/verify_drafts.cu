@@ -18,8 +18,8 @@
 // by latency for few (10 us: the drafts' probabilities, the run, the cluster's exchange,
 // the final scan, one after the other). So a request is worked by a cluster of up to eight blocks, each
 // summing a run of the vocabulary; the blocks exchange their sums through distributed
-// shared memory, and the one whose run holds the border scans the 1/16 of it (a warp's
-// run) that does, with all its threads at once.
+// shared memory, and the one whose run holds the border scans the warp's run that does (1/16
+// or 1/8 of its own, by the shape of block), with all its threads at once.
 #include <algorithm>
 
 #include <cooperative_groups.h>
