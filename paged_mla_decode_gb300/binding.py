@@ -304,7 +304,7 @@ def mla_decode_grouped(q: torch.Tensor, kv_pages: torch.Tensor, block_table: tor
 def mla_decode_combine(part_out: torch.Tensor, part_lse: torch.Tensor, out: torch.Tensor,
                        lse: torch.Tensor, stream=None) -> None:
     """Merge ``part_out [S, R, 512]`` / ``part_lse [S, R]`` into ``out [R, 512]`` / ``lse [R]``."""
-    if part_out.dtype != torch.float32 or part_lse.dtype != torch.float32 or part_lse.dim() != 2:
+    if part_out.dtype != torch.float32 or part_lse.dtype != torch.float32:
         _refuse("part_out and part_lse are float32 [parts, rows, 512] and [parts, rows]")
     num_parts, rows = int(part_lse.shape[0]), int(part_lse.shape[1])
     if part_out.shape != (num_parts, rows, 512):
