@@ -246,6 +246,50 @@ MLA_API mla_status mla_decode_grouped(const void* q, const void* kv_pages, int64
                                       mla_stream_t stream);
 
 /*
+ * mla_decode_tree -- attention of a tree of drafted tokens.
+ *
+ * A drafter may propose several continuations of a request: a tree whose nodes are
+ * verified in parallel without changing the target model's distribution ("How to
+ * serve trillions of tokens for trillion-parameter coding agents", section "Use
+ * custom speculative decoding ..."). The n = num_nodes[b] nodes of request b are its
+ * last n cached tokens, in node order (node 0 the last sampled token, the others
+ * drafts behind it); L = seq_lens[b] counts them. Node j sees the L - n tokens of the
+ * context and each node i < n whose bit i is set in tree_mask[b][j], for a tree its
+ * ancestors and itself; any other set is as good, and a row that sees no token gets
+ * out = 0, lse = -inf. K, s, out and lse as in mla_decode, over the tokens that the
+ * node sees. A chain of drafts is the mask 2^(j + 1) - 1.
+ *
+ * The max_nodes * num_heads query rows of a request are cut into tiles of 64, whatever
+ * nodes they belong to, which share each page that is read. Arithmetic as mla_decode's;
+ * so a NaN in an entry makes the rows that see it NaN, and no others. (A cached bf16
+ * infinity makes the rows that see it NaN, or drops out where its score is -inf.)
+ *
+ * tree_mask   device, uint64 [batch][max_nodes]
+ * num_nodes   device, int32 [batch]; NULL: max_nodes each. Rows j >= num_nodes[b] get
+ *             out = 0, lse = -inf. A request with num_nodes[b] outside
+ *             [0, max_nodes] or a length outside [num_nodes[b], max_pages * 64] is
+ *             a bad length (MLA_DEVICE_ERR_BAD_LENGTH, out = 0, lse = -inf).
+ * max_nodes   1 .. MLA_MAX_TREE_NODES
+ * q           device, bf16 [batch][max_nodes][num_heads][576]
+ * out         device, bf16 [batch][max_nodes][num_heads][512]
+ * lse         device, fp32 [batch][max_nodes][num_heads]
+ * workspace   at least mla_decode_tree_workspace_size(batch, max_nodes, num_heads,
+ *             num_ctas) bytes, zero-filled before its first use.
+ * Other arguments as mla_decode, num_heads and the cache types too.
+ */
+#define MLA_MAX_TREE_NODES 64
+MLA_API size_t mla_decode_tree_workspace_size(int batch, int max_nodes, int num_heads,
+                                              int num_ctas);
+MLA_API mla_status mla_decode_tree(const void* q, const void* kv_pages, int64_t num_pages,
+                                   int page_size, int kv_dtype, const int32_t* block_table,
+                                   int max_pages, const int32_t* seq_lens,
+                                   const uint64_t* tree_mask, const int32_t* num_nodes,
+                                   int batch, int max_nodes, int num_heads, float sm_scale,
+                                   float kv_scale, int num_ctas, void* workspace,
+                                   size_t workspace_bytes, void* out, float* lse,
+                                   mla_stream_t stream);
+
+/*
  * mla_decode_f16_operands -- mla_decode with 16-bit tensor-core operands.
  *
  * Same arguments, contract and results (within the same tolerance) as

@@ -39,9 +39,11 @@ Modules:
 * :mod:`oracle.paging` -- the page allocator's side of a step, request by request.
 * :mod:`oracle.verify` -- verification of drafted tokens in rational arithmetic
   ([K2.6] section "Use custom speculative decoding ...").
+* :mod:`oracle.tree` -- a tree of drafts: attention by node masks, logits to probabilities,
+  verification down the tree, the kept nodes' entries moved together.
 
 Every function is pinned by ``tests/test_oracle_*.py`` against closed forms,
 library routines, brute force and invariants (see each test's docstring).
 """
 
-from . import attention, e2m1, e4m3, integrity, paging, verify  # noqa: F401
+from . import attention, e2m1, e4m3, integrity, paging, tree, verify  # noqa: F401

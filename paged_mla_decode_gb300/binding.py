@@ -43,12 +43,14 @@ MLA_KV_ALLOC_NO_PAGES = 0x8
 MLA_PROB_F32 = 0
 MLA_PROB_BF16 = 1
 MLA_MAX_DRAFTS = 31
+MLA_MAX_TREE_NODES = 64
 
 EXPORTED = ("mla_abi_version", "mla_status_string", "mla_kv_append",
             "mla_decode_workspace_size", "mla_decode", "mla_decode_f16_operands",
             "mla_decode_grouped_workspace_size", "mla_decode_grouped",
             "mla_decode_combine", "mla_kv_check", "mla_decode_static_scratch",
-            "mla_kv_gather", "mla_kv_alloc", "mla_verify_drafts")
+            "mla_kv_gather", "mla_kv_alloc", "mla_verify_drafts",
+            "mla_decode_tree_workspace_size", "mla_decode_tree")
 
 _lib = None
 
@@ -98,6 +100,13 @@ def open_library(path: str) -> ctypes.CDLL:
                                        c.c_int, c.c_int, c.c_void_p, c.c_float, c.c_float,
                                        c.c_int, c.c_void_p, c.c_size_t, c.c_void_p, c.c_void_p,
                                        c.c_void_p]
+    lib.mla_decode_tree_workspace_size.restype = c.c_size_t
+    lib.mla_decode_tree_workspace_size.argtypes = [c.c_int, c.c_int, c.c_int, c.c_int]
+    lib.mla_decode_tree.restype = c.c_int
+    lib.mla_decode_tree.argtypes = [c.c_void_p, c.c_void_p, c.c_int64, c.c_int, c.c_int, c.c_void_p,
+                                    c.c_int, c.c_void_p, c.c_void_p, c.c_void_p, c.c_int, c.c_int,
+                                    c.c_int, c.c_float, c.c_float, c.c_int, c.c_void_p, c.c_size_t,
+                                    c.c_void_p, c.c_void_p, c.c_void_p]
     lib.mla_decode_combine.restype = c.c_int
     lib.mla_decode_combine.argtypes = [c.c_void_p, c.c_void_p, c.c_int, c.c_int64, c.c_void_p,
                                        c.c_void_p, c.c_void_p]
@@ -299,6 +308,49 @@ def mla_decode_grouped(q: torch.Tensor, kv_pages: torch.Tensor, block_table: tor
         int(num_ctas), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
         _ptr(out), _ptr(lse), _stream(stream))
     _check(st, "mla_decode_grouped")
+
+
+def mla_decode_tree_workspace_size(batch: int, max_nodes: int, num_heads: int,
+                                   num_ctas: int = 0) -> int:
+    return int(load_library().mla_decode_tree_workspace_size(batch, max_nodes, num_heads, num_ctas))
+
+
+def _tree_masks(device: int, tree_mask: torch.Tensor, batch: int, nodes: int) -> None:
+    """Node masks are contiguous 64-bit words ``[batch, nodes]`` on `device`."""
+    if tree_mask.dtype not in (torch.int64, torch.uint64) or tree_mask.shape != (batch, nodes):
+        _refuse("tree_mask is int64 or uint64 [batch, nodes]")
+    _same_device(device, tree_mask)
+
+
+def mla_decode_tree(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor,
+                    seq_lens: torch.Tensor, tree_mask: torch.Tensor, sm_scale: float,
+                    kv_scale: float, out: torch.Tensor, lse: torch.Tensor,
+                    workspace: torch.Tensor, num_nodes: torch.Tensor | None = None,
+                    num_ctas: int = 0, stream=None) -> None:
+    """Attention of a tree of drafted tokens, the last ``num_nodes[b]`` cached tokens of request b.
+
+    ``q`` is ``[batch, max_nodes, heads, 576]``, ``tree_mask`` 64-bit words ``[batch,
+    max_nodes]`` (int64 or uint64; bit i of word j: node j sees node i, for a tree its
+    ancestors and itself); without ``num_nodes`` every request has ``max_nodes``. Rows of
+    nodes that a request does not have get out = 0, lse = -inf. ``kv_pages`` as in
+    :func:`kv_dtype_code`; the workspace's size is :func:`mla_decode_tree_workspace_size`.
+    """
+    batch, nodes, heads = _decode_shape(q, block_table, seq_lens, out, lse)
+    dtype = kv_dtype_code(kv_pages)
+    device = _device_of(kv_pages)
+    _tree_masks(device, tree_mask, batch, nodes)
+    _same_device(device, q, block_table, seq_lens, out, lse, workspace)
+    if num_nodes is not None:
+        _int32(device, num_nodes)
+        if num_nodes.numel() != batch:
+            _refuse("num_nodes is [batch]")
+    st = load_library().mla_decode_tree(
+        _ptr(q), _ptr(kv_pages), int(kv_pages.shape[0]), _page_size(kv_pages), dtype,
+        _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), _ptr(tree_mask),
+        _ptr(num_nodes), batch, nodes, heads, float(sm_scale), float(kv_scale), int(num_ctas),
+        _ptr(workspace), int(workspace.numel() * workspace.element_size()), _ptr(out), _ptr(lse),
+        _stream(stream))
+    _check(st, "mla_decode_tree")
 
 
 def mla_decode_combine(part_out: torch.Tensor, part_lse: torch.Tensor, out: torch.Tensor,

@@ -113,6 +113,7 @@ struct MergeParams {
   float* lse;
   unsigned* status;
   int stage_pieces;
+  OutputRows to_rows;
 };
 
 // Row number k (from 0) among those of more than kFewPieces pieces; -1 if there are fewer.
@@ -163,7 +164,8 @@ __device__ __forceinline__ void merge_unit_by_warp(const MergeParams& p, int64_t
   const int64_t rh = unit / kMergeQuarters;
   const int r = (int)(rh / p.heads), h = (int)(rh - (int64_t)r * p.heads);
   const int np = __ldcg(p.row_np + r), base = __ldcg(p.row_base + r);
-  if (np > kFewPieces) return;  // another block's
+  const int64_t to = p.to_rows.of(r, h, p.heads);
+  if (np > kFewPieces || to < 0) return;  // another block's, or nobody's
   float l_own = -INFINITY;
   int bad = 0;
   if (lane < np) {
@@ -202,8 +204,8 @@ __device__ __forceinline__ void merge_unit_by_warp(const MergeParams& p, int64_t
   uint2 packed;
   packed.x = *reinterpret_cast<const uint32_t*>(&lo);
   packed.y = *reinterpret_cast<const uint32_t*>(&hi);
-  *reinterpret_cast<uint2*>(p.out + rh * kDLatent + 128 * quarter + 4 * lane) = packed;
-  if (quarter == 0 && lane == 0) p.lse[rh] = empty ? -INFINITY : m + logf(total);
+  *reinterpret_cast<uint2*>(p.out + to * kDLatent + 128 * quarter + 4 * lane) = packed;
+  if (quarter == 0 && lane == 0) p.lse[to] = empty ? -INFINITY : m + logf(total);
 }
 
 // Unit `unit` by the whole block.
@@ -219,7 +221,7 @@ __device__ __forceinline__ void merge_unit_by_block(const MergeParams& p, int64_
   uint32_t phase = 0;
   const bool ok = merge_unit(
       unit, p.heads, p.row_base, p.row_np, p.piece_err, p.part_lse, p.part_out, p.out, p.lse,
-      p.stage_pieces, stage, sm, mb, phase, (int)threadIdx.x, [] { __syncthreads(); },
+      p.to_rows, p.stage_pieces, stage, sm, mb, phase, (int)threadIdx.x, [] { __syncthreads(); },
       [](bool pred) { return __syncthreads_or(pred ? 1 : 0) != 0; });
   if (!ok && threadIdx.x == 0) atomicOr(p.status, MLA_DEVICE_ERR_TIMEOUT);
 }
@@ -261,7 +263,7 @@ combine_dense_kernel(const float* __restrict__ part_out, const float* __restrict
 
 cudaError_t launch_combine_pieces(const DecodeWorkspace& ws, int rows, int heads, int passes,
                                   int max_pieces_per_row, __nv_bfloat16* out, float* lse,
-                                  cudaStream_t stream) {
+                                  cudaStream_t stream, int tiles, int query_rows) {
   static std::atomic<int> configured[64];
   int dev = 0;
   cudaGetDevice(&dev);
@@ -292,6 +294,7 @@ cudaError_t launch_combine_pieces(const DecodeWorkspace& ws, int rows, int heads
   p.out = out;
   p.lse = lse;
   p.status = ws.status;
+  p.to_rows = OutputRows{tiles, query_rows < tiles * heads ? query_rows : 0};
   p.stage_pieces = merge_stage_pieces(max_pieces_per_row, rows);
   const int64_t blocks =
       few_rows ? p.units : p.many_blocks + (p.units + kMergeWarps - 1) / kMergeWarps;

@@ -199,7 +199,9 @@ enum Flag { F_ABORT = 0, F_PIECE_BAD = 1 };
 // softmax warps after they have waited for it.
 struct PageDesc {
   int32_t page;    // block-table entry
-  int16_t valid;   // tokens of the row in this page (1..64)
+  int8_t valid;    // tokens of the row in this page (1..64)
+  int8_t context;  // tree decode: how many of them come before the nodes (below 0: the
+                   // page starts at node -context); 64 where all do
   int16_t flags;   // kDescPieceStart | kDescPieceEnd | kDescPageOk
   int32_t row;     // request row r = b * Q + j
   int32_t slot;    // partial slot of this piece
@@ -224,7 +226,21 @@ struct Fp8Params {
   int forks;                    // requests per group
   int workers;                  // CTAs / forks: workers of the shared-prefix plan
   const int32_t* prefix_pages;  // [batch / forks] shared pages of each group
+  // tree decode (kTree) only: nq is the tiles of a request, heads the rows of a tile
+  const uint64_t* tree_mask;
+  const int32_t* num_nodes;
+  int max_nodes, node_heads;
+  int query_rows;               // of a request
 };
+
+template <class P>
+__device__ __forceinline__ P row_plan(const Fp8Params& p) {
+  if constexpr (std::is_same_v<P, TreePlan>)
+    return TreePlan{p.seq_lens, p.num_nodes, p.batch, p.max_nodes, p.node_heads, p.nq, p.heads,
+                    p.max_pages, kPageSize, p.G, 0};
+  else
+    return Plan{p.seq_lens, p.batch, p.nq, p.max_pages, kPageSize, p.G, 0};
+}
 
 __device__ inline GroupPlan group_plan(const Fp8Params& p, int kind) {
   return GroupPlan{p.seq_lens, p.batch, p.nq, p.max_pages, kPageSize,
@@ -463,10 +479,25 @@ __device__ __forceinline__ void expand_page(const Expander& x, uint32_t raw, uin
   }
 }
 
+// Bit i: token i of the 16 from token `first` of a page on is one that a query row with
+// node mask m sees, where the page's first `context` tokens come before the nodes.
+__device__ __forceinline__ uint32_t tree_visible(uint64_t m, int context, int first) {
+  const int s = context - first;  // of the 16, before the nodes
+  if (s >= 16) return 0xffffu;
+  const uint64_t nodes = s >= 0 ? m << s : m >> -s;
+  return ((uint32_t)nodes | (s > 0 ? (1u << s) - 1u : 0u)) & 0xffffu;
+}
+// Whether one of four e4m3 codes is a NaN (0x7f, 0xff).
+__device__ __forceinline__ bool e4m3x4_has_nan(uint32_t w) {
+  return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+}
+
 // kGrouped: the grouped decode (GroupPlan): this CTA's shared-prefix range, then
 // its suffix range; otherwise mla_decode's single plan (Plan).
 // kE2m1: a 4-bit cache, expanded to e4m3 pages by seven more warps; otherwise e4m3.
-template <bool kGrouped, bool kE2m1>
+// kTree: the tree decode (TreePlan): a row is a tile of a request's query rows, each of
+// which sees the context and, of the nodes' tokens, those in its mask.
+template <bool kGrouped, bool kE2m1, bool kTree>
 __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
     decode_fp8_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap lat_map,
                       const __grid_constant__ CUtensorMap rope_map) {
@@ -500,7 +531,8 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
   // wait for all earlier work in the stream (see launch_decode_fp8), so the
   // lengths, block table and pages may be read at once; only the split query
   // itself needs the split kernel to have completed (griddep_wait before q_op).
-  Plan plan{p.seq_lens, p.batch, p.nq, p.max_pages, kPageSize, p.G, 0};
+  using RowPlan = std::conditional_t<kTree, TreePlan, Plan>;
+  RowPlan plan = row_plan<RowPlan>(p);
   const int c = blockIdx.x;
   int64_t* s_plan_x = reinterpret_cast<int64_t*>(smem + M::kOffPlanX);  // kGrouped only
   if (warp == 0) {
@@ -527,7 +559,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
       }
     } else {
       // the whole plan in one warp pass: total tiles, then this CTA's first row
-      Plan pl = plan;
+      RowPlan pl = plan;
       pl.set_total(plan_total_tiles_warp(pl));
       const int64_t xb = c < pl.G ? pl.cta_start(c) : 0;
       RowCursor f = plan_find_row_warp(pl, xb, c == 0, p.ws.row_base, p.ws.row_np, p.ws.status);
@@ -586,7 +618,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
   const PageDesc* desc = reinterpret_cast<const PageDesc*>(smem + kOffDesc);
   // This CTA's walk over its pages (the TMA lane describes each page from it; the
   // MMA issuers follow their own copy for the piece boundaries, in registers).
-  using Walker = std::conditional_t<kGrouped, SegWalker, PageWalker<Plan>>;
+  using Walker = std::conditional_t<kGrouped, SegWalker, PageWalker<RowPlan>>;
   auto start_walker = [&](Walker& pw) {
     if constexpr (kGrouped) {
       GroupPlan A = group_plan(p, 1), B = group_plan(p, 2);
@@ -619,14 +651,19 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
         auto describe_next = [&]() {
           PageDesc& d = ring[jn % kDescRing];
           const bool ps = pw.piece_start();
-          d.valid = (int16_t)pw.valid_tokens();
+          d.valid = (int8_t)pw.valid_tokens();
+          if constexpr (kTree) {
+            // (the nodes' tokens are the row's last ones)
+            const int before = pw.cur.n - plan.nodes(pw.cur.r / plan.tiles);
+            d.context = (int8_t)min(before - pw.page_in_row() * kPageSize, kPageSize);
+          }
           d.flags = (int16_t)((ps ? kDescPieceStart : 0) | (pw.piece_end() ? kDescPieceEnd : 0) |
                               (pw.shared() ? kDescShared : 0));
           d.row = pw.qrow;
           d.slot = pw.slot;
           cp_async_4(smem_u32(&d.page), p.block_table + pw.bt_row + pw.page_in_row());
           cp_async_commit();
-          if (ps && jn > 0)  // the softmax warps read this row's q when they reach it
+          if (!kTree && ps && jn > 0)  // the softmax warps read this row's q when they reach it
             tc::prefetch_l2_bulk(p.q + (int64_t)pw.qrow * H * kDEntry,
                                  (uint32_t)(H * kDEntry * sizeof(__nv_bfloat16)));
           pw.next();
@@ -854,6 +891,8 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
       const uint32_t lane_hi = (uint32_t)(32 * q4) << 16;
       const uint32_t lane_lo = (uint32_t)(32 * q4 + 16) << 16;
       float m = -INFINITY, lpart = 0.f, qmul = 0.f;
+      uint64_t nodes_seen = 0;  // tree decode: of this thread's row
+      bool row_live = true;
       int piece = 0;
       bool ok = true;
       {
@@ -900,6 +939,10 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
           // (half g: 32 + 2g, 33 + 2g), 64-byte swizzled.
           griddep_wait();  // the split kernel has completed and its writes are visible
           const bool live = h < H;
+          if constexpr (kTree) {
+            nodes_seen = tree_row_mask(plan, p.tree_mask, row, h);
+            row_live = tree_row_live(plan, row, h);
+          }
           qmul = live ? __ldcg(p.ws.q_mul + (int64_t)row * 64 + h) : 0.f;
           const int r = 32 * q4 + lane;
           const uint4* src =
@@ -981,7 +1024,15 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
           s[i] = v.x;
           s[i + 1] = v.y;
         }
-        if (nvis < kPageSize) {  // (only a row's last page, or a bad page id, hides tokens)
+        const bool has_nodes = kTree && d.context < kPageSize;
+        if (has_nodes && page_ok) {
+          // (the nodes are a request's last tokens: a page with any of them, or with fewer
+          // than 64 tokens, has this test; a node behind the request's last is in no mask)
+          const uint32_t seen = tree_visible(nodes_seen, d.context, 16 * c16);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (!((seen >> i) & 1u)) s[i] = -INFINITY;
+        } else if (nvis < kPageSize) {  // (only a row's last page, or a bad page id, hides tokens)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             if (16 * c16 + i >= nvis) s[i] = -INFINITY;
@@ -1097,6 +1148,23 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
                          "r"(0u));
           }
         }
+        if (has_nodes && page_ok) {
+          // A NaN in a node's entry is one for the rows that see it, which their scores
+          // make NaN already. For the others it would be 0 * NaN in PV, so chunks with a
+          // NaN code become zeros.
+          const uint32_t page_base = sbase + kOffPages + slot * kPageBytes;
+          const int first = max((int)d.context, 0);
+          for (int i = t; i < (nvis - first) * 32; i += kSmThreads) {
+            const int rrow = first + (i >> 5), u = i & 31;
+            const uint32_t a = page_base + (u >> 3) * kLatBlock + rrow * 128 + (u & 7) * 16;
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+            if (e4m3x4_has_nan(w[0]) || e4m3x4_has_nan(w[1]) || e4m3x4_has_nan(w[2]) ||
+                e4m3x4_has_nan(w[3]))
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(a), "r"(0u));
+          }
+        }
         tc::fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
@@ -1123,7 +1191,8 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
           }
           named_bar_softmax();
           if (g == 0 && lane < 16) {
-            const float l = lsum_s[h] + lsum_s[64 + h];
+            // (a row without a node has whatever its q gives: it counts as empty)
+            const float l = row_live ? lsum_s[h] + lsum_s[64 + h] : 0.f;
             linv_s[h] = l > 0.f ? p.kv_scale / l : 0.f;
             if (h < H)
               // (a NaN among the scores: lse = +inf, with which the merge makes the row NaN)
@@ -1196,8 +1265,9 @@ constexpr int kSplitHeads = 8;
 constexpr int kSplitThreads = kSplitHeads * kQOpChunks;  // 288
 
 __global__ void __launch_bounds__(kSplitThreads)
-    q_split_kernel(const __nv_bfloat16* __restrict__ q, int heads, float score_mul,
-                   uint8_t* __restrict__ q_op, float* __restrict__ q_mul) {
+    q_split_kernel(const __nv_bfloat16* __restrict__ q, int heads, int rows_a_request,
+                   int query_rows, float score_mul, uint8_t* __restrict__ q_op,
+                   float* __restrict__ q_mul) {
   // All earlier work in the stream has completed once this returns; the decode
   // kernel that follows may start only after every block has passed it.
   griddep_wait();
@@ -1209,11 +1279,15 @@ __global__ void __launch_bounds__(kSplitThreads)
   const int groups = (heads + kSplitHeads - 1) / kSplitHeads;
   const int64_t row = blockIdx.x / groups;
   const int h = (int)(blockIdx.x - row * groups) * kSplitHeads + hl;
-  const bool live = h < heads;
+  // where its query lies: the request's rows follow each other (a tree's may end inside the
+  // last of its tiles)
+  const int64_t request = row / rows_a_request;
+  const int at = (int)(row - request * rows_a_request) * heads + h;
+  const bool live = h < heads && at < query_rows;
   if (tid < kSplitHeads) s_amax[tid] = 0u;
   uint4 a[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
   if (live) {
-    const uint4* src = reinterpret_cast<const uint4*>(q + (row * heads + h) * kDEntry) + 2 * u;
+    const uint4* src = reinterpret_cast<const uint4*>(q + (request * query_rows + at) * kDEntry) + 2 * u;
     a[0] = __ldg(src);
     a[1] = __ldg(src + 1);
   }
@@ -1234,7 +1308,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   __syncthreads();
   atomicMax(&s_amax[hl], __float_as_uint(amax));  // non-negative: integer order = float order
   __syncthreads();
-  if (!live) return;
+  if (h >= heads) return;
   amax = __uint_as_float(s_amax[hl]);
   int shift = 0;
   if (amax > 0.f && isfinite(amax)) {
@@ -1334,7 +1408,7 @@ __global__ void __launch_bounds__(32) group_plan_kernel(const Fp8Params p) {
 }  // namespace
 
 // One variant of the decode kernel: its shared-memory limit once per device, then the launch.
-template <bool kGrouped, bool kE2m1>
+template <bool kGrouped, bool kE2m1, bool kTree = false>
 static cudaError_t launch_variant(const Fp8Params& p, const CUtensorMap& lat_map,
                                   const CUtensorMap& rope_map, cudaStream_t stream) {
   using M = Map<kE2m1>;
@@ -1343,7 +1417,7 @@ static cudaError_t launch_variant(const Fp8Params& p, const CUtensorMap& lat_map
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !configured[dev].load()) {
-    cudaError_t e = cudaFuncSetAttribute(decode_fp8_kernel<kGrouped, kE2m1>,
+    cudaError_t e = cudaFuncSetAttribute(decode_fp8_kernel<kGrouped, kE2m1, kTree>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev].store(1);
@@ -1356,7 +1430,7 @@ static cudaError_t launch_variant(const Fp8Params& p, const CUtensorMap& lat_map
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_fp8_kernel<kGrouped, kE2m1>, p, lat_map, rope_map);
+  return cudaLaunchKernelEx(&cfg, decode_fp8_kernel<kGrouped, kE2m1, kTree>, p, lat_map, rope_map);
 }
 
 // Tensor maps of an e4m3 pool viewed as [num_pages * 64 rows][576 bytes] (a page is 64
@@ -1414,6 +1488,11 @@ cudaError_t launch_decode_fp8(const DecodeLaunch& d, cudaStream_t stream) {
   p.forks = grouped ? d.forks : 1;
   p.workers = grouped ? d.G / d.forks : 0;
   p.prefix_pages = d.prefix_pages;
+  p.tree_mask = d.tree_mask;
+  p.num_nodes = d.num_nodes;
+  p.max_nodes = d.max_nodes;
+  p.node_heads = d.node_heads;
+  p.query_rows = d.query_rows();
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   if (grouped) {
     cudaLaunchConfig_t gc = {};
@@ -1433,10 +1512,13 @@ cudaError_t launch_decode_fp8(const DecodeLaunch& d, cudaStream_t stream) {
     sc.stream = stream;
     sc.attrs = attr;
     sc.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&sc, q_split_kernel, d.q, d.heads, d.score_mul,
+    cudaError_t e = cudaLaunchKernelEx(&sc, q_split_kernel, d.q, d.heads, d.nq, p.query_rows, d.score_mul,
                                        d.ws.q_op, d.ws.q_mul);
     if (e != cudaSuccess) return e;
   }
+  if (d.tree_mask != nullptr)
+    return d.e2m1 ? launch_variant<false, true, true>(p, lat_map, rope_map, stream)
+                  : launch_variant<false, false, true>(p, lat_map, rope_map, stream);
   if (d.e2m1)
     return grouped ? launch_variant<true, true>(p, lat_map, rope_map, stream)
                    : launch_variant<false, true>(p, lat_map, rope_map, stream);

@@ -23,6 +23,17 @@ constexpr int kMergeStagePieces = 160;
 constexpr uint32_t kMergeSliceBytes = 128 * 4;
 constexpr uint64_t kMergeWaitNs = 2000000000ull;
 
+// Output row of row r, head h: r * heads + h, or the request's where its rows end inside
+// the last of its tiles (launch_combine_pieces); -1: none.
+struct OutputRows {
+  int tiles, query_rows;  // query_rows = 0: as many as tiles * heads
+  __device__ __forceinline__ int64_t of(int r, int h, int heads) const {
+    if (query_rows == 0) return (int64_t)r * heads + h;
+    const int b = r / tiles, at = (r - b * tiles) * heads + h;
+    return at < query_rows ? (int64_t)b * query_rows + at : -1;
+  }
+};
+
 // Shared memory of a merge group besides the staging area.
 struct MergeShared {
   float w[kMergeStagePieces];
@@ -47,12 +58,14 @@ __device__ inline bool merge_unit(int64_t unit, int heads, const int32_t* __rest
                                   const float* __restrict__ part_lse,
                                   const float* __restrict__ part_out,
                                   __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
-                                  int stage_pieces, float4* stage, MergeShared& sm, uint32_t mb,
+                                  const OutputRows& to_rows, int stage_pieces, float4* stage, MergeShared& sm, uint32_t mb,
                                   uint32_t& phase, int tid, Sync sync, SyncOr sync_or) {
   const int quarter = (int)(unit % kMergeQuarters);
   const int64_t rh = unit / kMergeQuarters;
   const int r = (int)(rh / heads);
   const int h = (int)(rh - (int64_t)r * heads);
+  const int64_t to = to_rows.of(r, h, heads);
+  if (to < 0) return true;
   const int warp = tid >> 5, lane = tid & 31;
   const int np = __ldcg(row_np + r);
   const int base = __ldcg(row_base + r);
@@ -139,8 +152,8 @@ __device__ inline bool merge_unit(int64_t unit, int heads, const int32_t* __rest
     uint2 packed;
     packed.x = *reinterpret_cast<uint32_t*>(&lo);
     packed.y = *reinterpret_cast<uint32_t*>(&hi);
-    *reinterpret_cast<uint2*>(out + rh * kDLatent + 128 * quarter + 4 * lane) = packed;
-    if (quarter == 0 && lane == 0) lse[rh] = empty ? -INFINITY : m + logf(total);
+    *reinterpret_cast<uint2*>(out + to * kDLatent + 128 * quarter + 4 * lane) = packed;
+    if (quarter == 0 && lane == 0) lse[to] = empty ? -INFINITY : m + logf(total);
   }
   sync();  // sm and the stage are free for the next unit
   return !timed_out;

@@ -203,6 +203,62 @@ struct GroupPlan {
   }
 };
 
+// ---------------------------------------------------------------------------
+// Tree decode (mla_decode_tree).
+//
+// The max_nodes * heads query rows of a request lie behind each other in q, node by
+// node, and every one of them walks the same pages: they are cut into tiles of
+// `tile_rows` rows, whatever nodes those belong to, and a plan row is one tile,
+// r = b * tiles + i, over all L tokens of its request (which of the last n, the
+// nodes', a query row sees is its node's mask). Tiles with no node of the request
+// have no tokens. A request is bad if n is outside [0, max_nodes] or L outside
+// [n, max_pages * 64].
+// ---------------------------------------------------------------------------
+struct TreePlan {
+  static constexpr bool kGrouped = false;
+  const int32_t* seq_lens;
+  const int32_t* num_nodes;  // may be null: max_nodes each
+  int batch, max_nodes, heads, tiles, tile_rows, max_pages, tile;
+  int G;
+  int64_t T;
+
+  __device__ void set_total(int64_t total) {
+    T = total;
+    if (T < G) G = (int)T;
+  }
+  __device__ int rows() const { return batch * tiles; }
+  __device__ int nodes(int b) const { return num_nodes ? __ldg(num_nodes + b) : max_nodes; }
+  __device__ int row_tokens(int r) const {
+    const int b = r / tiles, i = r - b * tiles;
+    const int L = __ldg(seq_lens + b), n = nodes(b);
+    if (n < 0 || n > max_nodes || L < n || (int64_t)L > (int64_t)max_pages * kPageSize) return -1;
+    return i * tile_rows < n * heads ? L : 0;
+  }
+  __device__ int row_tiles(int r) const {
+    const int n = row_tokens(r);
+    return n <= 0 ? 0 : (n + tile - 1) / tile;
+  }
+  __device__ int64_t cta_start(int c) const { return (int64_t)c * T / G; }
+  __device__ int cta_of(int64_t x) const { return (int)(((x + 1) * G - 1) / T); }
+  __device__ int row_pieces(int64_t rt, int t) const {
+    return t == 0 ? 0 : cta_of(rt + t - 1) - cta_of(rt) + 1;
+  }
+  __device__ int q_row(int r, int /*fork*/) const { return r; }
+  __device__ int64_t bt_base(int r) const { return (int64_t)(r / tiles) * max_pages; }
+  // node of query row h of plan row r (max_nodes or more: none)
+  __device__ int node_of(int r, int h) const { return ((r - (r / tiles) * tiles) * tile_rows + h) / heads; }
+};
+// The nodes that query row h of plan row r sees, as bits; 0 if the row has no node.
+__device__ inline uint64_t tree_row_mask(const TreePlan& p, const uint64_t* tree_mask, int r, int h) {
+  const int b = r / p.tiles, node = p.node_of(r, h), n = min(max(p.nodes(b), 0), p.max_nodes);
+  if (node >= n) return 0;
+  return __ldg(tree_mask + (int64_t)b * p.max_nodes + node) & (~0ull >> (64 - n));
+}
+// Whether query row h of plan row r has a node.
+__device__ inline bool tree_row_live(const TreePlan& p, int r, int h) {
+  return p.node_of(r, h) < p.nodes(r / p.tiles);
+}
+
 template <class P>
 __device__ inline void cursor_next_row(const P& p, RowCursor& cur) {
   do {

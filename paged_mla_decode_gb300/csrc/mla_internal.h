@@ -43,6 +43,12 @@ struct DecodeLaunch {
   // [g * forks, (g + 1) * forks) share their first prefix_pages[g] pages
   int forks = 1;
   const int32_t* prefix_pages = nullptr;
+  // tree decode only (else tree_mask == nullptr): nq is the tiles of a request, heads the
+  // rows of a tile (see TreePlan), of which a request has max_nodes * node_heads in all
+  const uint64_t* tree_mask = nullptr;
+  const int32_t* num_nodes = nullptr;  // may be null
+  int max_nodes = 0, node_heads = 0;
+  int query_rows() const { return tree_mask ? max_nodes * node_heads : nq * heads; }  // of a request
 };
 
 // Split-KV decode on the tcgen05 tensor cores (decode_tc.cu); heads <= 64.
@@ -56,10 +62,12 @@ cudaError_t launch_decode_fp8(const DecodeLaunch& d, cudaStream_t stream);
 
 // Merge the pieces written by a decode kernel into out (bf16) and lse (fp32);
 // max_pieces_per_row is the number of decode CTAs (it sizes the staging), passes
-// the number of plans that cut the rows (2 for the grouped decode).
+// the number of plans that cut the rows (2 for the grouped decode). Row r, head h goes to
+// output row r * heads + h; where `tiles` rows make a request of query_rows < tiles * heads
+// output rows, to row (r / tiles) * query_rows + (r % tiles) * heads + h if there is one.
 cudaError_t launch_combine_pieces(const DecodeWorkspace& ws, int rows, int heads, int passes,
                                   int max_pieces_per_row, __nv_bfloat16* out, float* lse,
-                                  cudaStream_t stream);
+                                  cudaStream_t stream, int tiles = 1, int query_rows = 0);
 
 // Launch attribute that lets a kernel start while the previous kernel in the
 // stream is finishing (programmatic dependent launch); kernels launched with it
