@@ -477,6 +477,140 @@ MLA_API mla_status mla_verify_drafts(const void* target_probs, int64_t target_st
                                      int32_t* seq_lens_out, mla_stream_t stream);
 
 /*
+ * mla_logits_to_probs -- logits to the probabilities that a request samples from.
+ *
+ * What stands between the target model's logits and the verification of drafts, which
+ * must not change the model's distribution ("How to serve trillions of tokens for
+ * trillion-parameter coding agents", section "Use custom speculative decoding ..."): each
+ * request's own settings, for mla_verify_drafts (rows = drafts + 1) and mla_verify_tree
+ * (rows = nodes), and for a drafter's logits alike. For row j of request b, token v, with
+ * n(v) = max(token_counts[b][v], 0) + the number of drafts i >= 1 with bit i of
+ * tree_mask[b][j] and node_tokens[b][i] = v (node 0's token is among the counted):
+ *   if n(v) > 0 or v is in the prompt: x = x > 0 ? x / repetition : x * repetition;
+ *   if n(v) > 0: x = x - frequency * n(v) - presence;
+ *   x = x + biases[b][i] for every i with bias_tokens[b][i] = v;
+ *   x = -inf where bit v of allowed[b][j] is 0, and where x is NaN;
+ *   p(v) = exp((x(v) - max x) / temperature) / sum.
+ * A temperature that is not above 0 puts all weight on the maximum, the lowest token of
+ * equal ones; tokens at +inf share the weight; a row without a token above -inf is 0
+ * throughout (the verifications then give the token -1). Arithmetic in fp32, rounded once.
+ *
+ * logits        device, [batch][rows] rows of `vocab`, logit_stride >= vocab elements apart
+ * probs         device, likewise, prob_stride apart; may be `logits` (same type and stride)
+ * logit_dtype, prob_dtype  MLA_PROB_F32 or MLA_PROB_BF16
+ * vocab         1 .. MLA_MAX_PROBS_VOCAB (UNSUPPORTED beyond: a row is kept on chip)
+ * temperature   device, fp32 [batch]; NULL: 1
+ * num_rows      device, int32 [batch]; rows j >= num_rows[b] are left as they were; NULL: none
+ * node_tokens   device, int32 [batch][rows]; NULL exactly if tree_mask is (then no drafts
+ *               count). Tokens outside the vocabulary count for nothing.
+ * tree_mask     device, uint64 [batch][rows], rows <= MLA_MAX_TREE_NODES; 8-byte aligned. A
+ *               chain of drafts is 2^(j + 1) - 1.
+ * token_counts  device, int32 [batch][vocab]; NULL: 0
+ * prompt_mask   device, uint32 [batch][ceil(vocab / 32)], bit v % 32 of word v / 32; NULL: 0
+ * repetition, frequency, presence  device, fp32 [batch]; NULL: 1, 0, 0
+ * bias_tokens   device, int32 [batch][num_biases]; entries outside the vocabulary (-1:
+ *               padding) are skipped; the same token may come twice
+ * biases        device, fp32 [batch][num_biases]
+ * num_biases    0 .. MLA_MAX_BIASES (UNSUPPORTED beyond)
+ * allowed       device, uint32 [batch][rows][ceil(vocab / 32)]; NULL: everything
+ * Other pointers need the alignment of their elements here.
+ */
+#define MLA_MAX_PROBS_VOCAB 393216
+#define MLA_MAX_BIASES 1024
+MLA_API mla_status mla_logits_to_probs(
+    const void* logits, int64_t logit_stride, int logit_dtype, void* probs, int64_t prob_stride,
+    int prob_dtype, int batch, int rows, int vocab, const float* temperature,
+    const int32_t* num_rows, const int32_t* node_tokens, const uint64_t* tree_mask,
+    const int32_t* token_counts, const uint32_t* prompt_mask, const float* repetition,
+    const float* frequency, const float* presence, const int32_t* bias_tokens, const float* biases,
+    int num_biases, const uint32_t* allowed, mla_stream_t stream);
+
+/*
+ * mla_verify_tree -- walk down a tree of drafts, sample the token behind it.
+ *
+ * mla_verify_drafts for a tree. The parent of node i > 0 is the last node before i that
+ * bits of tree_mask[b][i] name (its last ancestor); a node without one is never reached.
+ * With p_v = target_probs[b][v], q_v = draft_probs[b][v] (which v's children were drawn
+ * from, independently of each other), x_i = node_tokens[b][i], u = uniforms[b], from node
+ * v = 0 on, R = p_v and W = 1:
+ *   the children i of v are tried in order: i is kept if u_i * q_v(x_i) * W < R(x_i);
+ *   then v = i, R = p_i, W = 1. Else R = max(R - W * q_v, 0) and W = the sum of R.
+ *   When no child is left: the next token is drawn from R (from p_v if R is 0 everywhere):
+ *   the smallest token whose running sum exceeds u_0 times the sum.
+ * With draft_probs NULL a child's token was certain: it is kept if u_i * W < R(x_i), else
+ * W = max(W - R(x_i), 0) and R(x_i) = 0. A draft outside [0, vocab) is rejected. For a chain
+ * this is mla_verify_drafts' rule.
+ *   out_tokens[b] = the kept drafts' tokens, the next token (-1 if all weights are
+ *   zero), then -1; path[b] = 0, the kept nodes, then -1;
+ *   num_accepted[b] = a, the number of kept drafts;
+ *   seq_lens_out[b] = seq_lens[b] - n + a + 1, the length after mla_kv_compact;
+ *   token_counts[b][t] += 1 for every token t of out_tokens[b] that is not -1.
+ * A request with n = num_nodes[b] outside [1, max_nodes] or seq_lens[b] < n is left out:
+ * out_tokens[b] = path[b] = -1 throughout, num_accepted[b] = -1, seq_lens_out[b] =
+ * seq_lens[b], token_counts[b] as it was.
+ *
+ * Arithmetic as in mla_verify_drafts: weights are summed as integers in units of 2^-60.
+ * After a node's second rejection R = max(p_v - c * q_v, 0) for the sum c of its Ws, c
+ * rounded to fp32 and R too. A row's probabilities must sum to less than 16 (beyond it the
+ * sums wrap: some child or none is kept, some token or -1 follows).
+ *
+ * target_probs, draft_probs  device, [batch][max_nodes] rows of `vocab` probabilities,
+ *               target_stride, draft_stride elements apart; rows >= num_nodes[b] and a
+ *               leaf's row of draft_probs are never read
+ * node_tokens   device, int32 [batch][max_nodes]; node 0's is not looked at
+ * tree_mask     device, uint64 [batch][max_nodes], 8-byte aligned
+ * uniforms      device, fp32 [batch][max_nodes]: u_0 for the sample, u_i for node i
+ * num_nodes     device, int32 [batch]; NULL: max_nodes each
+ * seq_lens      device, int32 [batch], lengths with all nodes; may be NULL (then
+ *               seq_lens_out is too)
+ * max_nodes     1 .. MLA_MAX_TREE_NODES
+ * out_tokens, path  device, int32 [batch][max_nodes]
+ * num_accepted  device, int32 [batch]
+ * seq_lens_out  device, int32 [batch]; may be seq_lens, or NULL
+ * token_counts  device, int32 [batch][vocab], as mla_logits_to_probs takes them; or NULL
+ * Other pointers need the alignment of their elements here.
+ */
+MLA_API mla_status mla_verify_tree(const void* target_probs, int64_t target_stride,
+                                   const void* draft_probs, int64_t draft_stride, int prob_dtype,
+                                   const int32_t* node_tokens, const uint64_t* tree_mask,
+                                   const float* uniforms, const int32_t* num_nodes,
+                                   const int32_t* seq_lens, int batch, int max_nodes, int vocab,
+                                   int32_t* out_tokens, int32_t* path, int32_t* num_accepted,
+                                   int32_t* seq_lens_out, int32_t* token_counts,
+                                   mla_stream_t stream);
+
+/*
+ * mla_kv_compact -- move the kept nodes' entries behind the context.
+ *
+ * After mla_verify_tree the kept nodes' entries stand among those of rejected ones
+ * (drafts are verified in parallel: section "Use custom speculative decoding ..." of the
+ * page above). For request b with a = num_accepted[b] >= 1, and
+ * base = seq_lens[b] - a - 1 the tokens of its context:
+ *   the entry of token base + path[b][i] goes to token base + i, i = 1 .. a,
+ * in each of num_layers caches with the same block table, as stored (bit for bit). All
+ * entries are read before one is written. A source outside [base, base + max_nodes) or
+ * beyond the block-table row, or a source or destination in no page of the cache, is
+ * skipped. Requests with a < 1, a >= max_nodes, or a length outside
+ * [a + 1, max_pages * 64] are left as they are. The block table must still name the pages
+ * of the rejected nodes.
+ *
+ * kv_pages      device, the first layer's pages (layout by kv_dtype); written in place
+ * layer_stride  bytes from one layer's pages to the next's, a multiple of 16 and at least
+ *               a layer's pages (not looked at with one layer)
+ * num_layers    0 .. 65535
+ * seq_lens      device, int32 [batch], lengths after verification (its seq_lens_out)
+ * path          device, int32 [batch][max_nodes]
+ * num_accepted  device, int32 [batch]
+ * Other arguments as mla_decode_tree; index arrays need 4-byte alignment.
+ */
+MLA_API mla_status mla_kv_compact(void* kv_pages, int num_layers, int64_t layer_stride,
+                                  int64_t num_pages, int page_size, int kv_dtype,
+                                  const int32_t* block_table, int max_pages,
+                                  const int32_t* seq_lens, const int32_t* path,
+                                  const int32_t* num_accepted, int batch, int max_nodes,
+                                  mla_stream_t stream);
+
+/*
  * mla_kv_check -- integrity check of requests' page mappings before decode.
  *
  * The check of "Smaller, faster, safer: running Kimi and GLM at scale",

@@ -71,7 +71,8 @@ def probabilities(logits, temperature=1.0, counts=None, prompt=None, repetition=
     if top == np.inf:
         p[x == np.inf] = 1.0
     else:
-        p = np.exp((x - top) / temperature)
+        some = x > -np.inf
+        p[some] = np.exp((x[some] - top) / temperature)
     return p / p.sum()
 
 

@@ -44,13 +44,16 @@ MLA_PROB_F32 = 0
 MLA_PROB_BF16 = 1
 MLA_MAX_DRAFTS = 31
 MLA_MAX_TREE_NODES = 64
+MLA_MAX_PROBS_VOCAB = 393216
+MLA_MAX_BIASES = 1024
 
 EXPORTED = ("mla_abi_version", "mla_status_string", "mla_kv_append",
             "mla_decode_workspace_size", "mla_decode", "mla_decode_f16_operands",
             "mla_decode_grouped_workspace_size", "mla_decode_grouped",
             "mla_decode_combine", "mla_kv_check", "mla_decode_static_scratch",
             "mla_kv_gather", "mla_kv_alloc", "mla_verify_drafts",
-            "mla_decode_tree_workspace_size", "mla_decode_tree")
+            "mla_decode_tree_workspace_size", "mla_decode_tree", "mla_logits_to_probs",
+            "mla_verify_tree", "mla_kv_compact")
 
 _lib = None
 
@@ -133,6 +136,20 @@ def open_library(path: str) -> ctypes.CDLL:
                                       c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p, c.c_int,
                                       c.c_int, c.c_int, c.c_void_p, c.c_void_p, c.c_void_p,
                                       c.c_void_p]
+    lib.mla_logits_to_probs.restype = c.c_int
+    lib.mla_logits_to_probs.argtypes = [
+        c.c_void_p, c.c_int64, c.c_int, c.c_void_p, c.c_int64, c.c_int, c.c_int, c.c_int, c.c_int,
+        c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p,
+        c.c_void_p, c.c_void_p, c.c_void_p, c.c_int, c.c_void_p, c.c_void_p]
+    lib.mla_verify_tree.restype = c.c_int
+    lib.mla_verify_tree.argtypes = [
+        c.c_void_p, c.c_int64, c.c_void_p, c.c_int64, c.c_int, c.c_void_p, c.c_void_p, c.c_void_p,
+        c.c_void_p, c.c_void_p, c.c_int, c.c_int, c.c_int, c.c_void_p, c.c_void_p, c.c_void_p,
+        c.c_void_p, c.c_void_p, c.c_void_p]
+    lib.mla_kv_compact.restype = c.c_int
+    lib.mla_kv_compact.argtypes = [
+        c.c_void_p, c.c_int, c.c_int64, c.c_int64, c.c_int, c.c_int, c.c_void_p, c.c_int, c.c_void_p,
+        c.c_void_p, c.c_void_p, c.c_int, c.c_int, c.c_void_p]
     return lib
 
 
@@ -551,6 +568,184 @@ def mla_verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | No
         drafts, vocab, out_tokens.data_ptr(), num_accepted.data_ptr(), _ptr(seq_lens_out),
         _stream(stream))
     _check(st, "mla_verify_drafts")
+
+
+def _float32(device: int, count: int, *tensors) -> None:
+    """Each tensor that is given holds `count` contiguous float32 on `device`."""
+    for t in tensors:
+        if t is not None:
+            if t.dtype is not torch.float32 or t.numel() != count:
+                _refuse("a setting or uniform is float32, one for each request (or node)")
+            _same_device(device, t)
+
+
+def _prob_dtype(t: torch.Tensor) -> int:
+    if t.dtype is torch.float32:
+        return MLA_PROB_F32
+    if t.dtype is torch.bfloat16:
+        return MLA_PROB_BF16
+    _refuse("logits and probabilities are float32 or bfloat16")
+
+
+def mla_logits_to_probs(logits: torch.Tensor, probs: torch.Tensor,
+                        temperature: torch.Tensor | None = None,
+                        num_rows: torch.Tensor | None = None,
+                        node_tokens: torch.Tensor | None = None,
+                        tree_mask: torch.Tensor | None = None,
+                        token_counts: torch.Tensor | None = None,
+                        prompt_mask: torch.Tensor | None = None,
+                        repetition: torch.Tensor | None = None,
+                        frequency: torch.Tensor | None = None,
+                        presence: torch.Tensor | None = None,
+                        bias_tokens: torch.Tensor | None = None,
+                        biases: torch.Tensor | None = None,
+                        allowed: torch.Tensor | None = None, stream=None) -> None:
+    """The probabilities that each request's settings make of its rows of logits.
+
+    ``logits`` and ``probs`` are ``[batch, rows, vocab]``, float32 or bfloat16 each, rows evenly
+    apart (``probs`` may be ``logits``). ``temperature``, ``repetition``, ``frequency`` and
+    ``presence`` are float32 ``[batch]``; ``token_counts`` int32 ``[batch, vocab]`` and
+    ``prompt_mask`` 32-bit words ``[batch, ceil(vocab / 32)]`` say which tokens came before;
+    ``node_tokens`` int32 and ``tree_mask`` 64-bit words, both ``[batch, rows]``, which drafts come
+    before each row as well (bit 0 never counts). ``bias_tokens`` (-1: none) and ``biases`` are
+    ``[batch, n]``, ``allowed`` 32-bit words ``[batch, rows, ceil(vocab / 32)]``. Rows from
+    ``num_rows[b]`` on are left as they were. The result is what :func:`mla_verify_drafts` and
+    :func:`mla_verify_tree` take.
+    """
+    if logits.dim() != 3 or probs.shape != logits.shape:
+        _refuse("logits and probs are [batch, rows, vocab]")
+    device = _device_of(logits)
+    if probs.get_device() != device:
+        _refuse("probs is on another device")
+    batch, rows, vocab = logits.shape
+    in_type, out_type = _prob_dtype(logits), _prob_dtype(probs)
+    in_stride = out_stride = vocab
+    if batch > 0 and rows > 0 and vocab > 0:
+        in_stride, out_stride = _row_stride(logits), _row_stride(probs)
+    _float32(device, batch, temperature, repetition, frequency, presence)
+    if num_rows is not None:
+        _int32(device, num_rows)
+        if num_rows.numel() != batch:
+            _refuse("num_rows is [batch]")
+    if (node_tokens is None) != (tree_mask is None):
+        _refuse("node_tokens and tree_mask are given together")
+    if tree_mask is not None:
+        _tree_masks(device, tree_mask, batch, rows)
+        _int32(device, node_tokens)
+        if node_tokens.shape != (batch, rows):
+            _refuse("node_tokens is [batch, rows]")
+    words = (vocab + 31) // 32
+    for t, shape in ((token_counts, (batch, vocab)), (prompt_mask, (batch, words)), (allowed, (batch, rows, words))):
+        if t is not None:
+            _int32(device, t)
+            if t.shape != shape:
+                _refuse("token_counts is [batch, vocab], prompt_mask [batch, words], allowed [batch, rows, words]")
+    if (bias_tokens is None) != (biases is None):
+        _refuse("bias_tokens and biases are given together")
+    num_biases = 0
+    if biases is not None:
+        _int32(device, bias_tokens)
+        if bias_tokens.dim() != 2 or bias_tokens.shape[0] != batch:
+            _refuse("bias_tokens is [batch, n]")
+        num_biases = bias_tokens.shape[1]
+        _float32(device, batch * num_biases, biases)
+    st = load_library().mla_logits_to_probs(
+        logits.data_ptr(), in_stride, in_type, probs.data_ptr(), out_stride, out_type, batch, rows,
+        vocab, _ptr(temperature), _ptr(num_rows), _ptr(node_tokens), _ptr(tree_mask),
+        _ptr(token_counts), _ptr(prompt_mask), _ptr(repetition), _ptr(frequency), _ptr(presence),
+        _ptr(bias_tokens), _ptr(biases), num_biases, _ptr(allowed), _stream(stream))
+    _check(st, "mla_logits_to_probs")
+
+
+def mla_verify_tree(target_probs: torch.Tensor, draft_probs: torch.Tensor | None,
+                    node_tokens: torch.Tensor, tree_mask: torch.Tensor, uniforms: torch.Tensor,
+                    out_tokens: torch.Tensor, path: torch.Tensor, num_accepted: torch.Tensor,
+                    num_nodes: torch.Tensor | None = None, seq_lens: torch.Tensor | None = None,
+                    seq_lens_out: torch.Tensor | None = None,
+                    token_counts: torch.Tensor | None = None, stream=None) -> None:
+    """Walk down each request's tree of drafts and sample the token behind the last kept node.
+
+    ``target_probs`` and ``draft_probs`` (which a node's children were drawn from; None: they were
+    certain) are ``[batch, N, vocab]``, float32 or bfloat16, rows evenly apart; ``node_tokens`` int32,
+    ``tree_mask`` 64-bit words and ``uniforms`` float32 in [0, 1) are ``[batch, N]`` (``uniforms[:, 0]``
+    is the sample's). ``num_nodes [batch]`` limits a request to fewer nodes. Writes ``out_tokens
+    [batch, N]`` (kept drafts, next token, then -1), ``path [batch, N]`` (0, kept nodes, then -1),
+    ``num_accepted [batch]``, given ``seq_lens`` also ``seq_lens_out``, the lengths after
+    :func:`mla_kv_compact` (may be ``seq_lens`` itself), and adds the tokens to ``token_counts
+    [batch, vocab]``.
+    """
+    if target_probs.dim() != 3:
+        _refuse("target_probs is [batch, nodes, vocab]")
+    device = _device_of(target_probs)
+    batch, nodes, vocab = target_probs.shape
+    dtype = _prob_dtype(target_probs)
+    target_stride = draft_stride = vocab
+    if batch > 0 and nodes > 0 and vocab > 0:
+        target_stride = _row_stride(target_probs)
+    if draft_probs is not None:
+        if draft_probs.dtype != target_probs.dtype or draft_probs.shape != target_probs.shape:
+            _refuse("draft_probs has target_probs' type and shape")
+        if draft_probs.get_device() != device:
+            _refuse("draft_probs is on another device")
+        if batch > 0 and nodes > 0 and vocab > 0:
+            draft_stride = _row_stride(draft_probs)
+    _tree_masks(device, tree_mask, batch, nodes)
+    if node_tokens.shape != (batch, nodes) or out_tokens.shape != (batch, nodes) or path.shape != (batch, nodes):
+        _refuse("node_tokens, out_tokens and path are [batch, nodes]")
+    if uniforms.shape != (batch, nodes):
+        _refuse("uniforms is float32 [batch, nodes]")
+    _float32(device, batch * nodes, uniforms)
+    if num_accepted.numel() != batch:
+        _refuse("num_accepted is [batch]")
+    _int32(device, node_tokens, out_tokens, path, num_accepted)
+    if seq_lens_out is not None and seq_lens is None:
+        _refuse("seq_lens_out needs seq_lens")
+    for t in (num_nodes, seq_lens, seq_lens_out):
+        if t is not None:
+            _int32(device, t)
+            if t.numel() != batch:
+                _refuse("num_nodes, seq_lens and seq_lens_out are [batch]")
+    if token_counts is not None:
+        _int32(device, token_counts)
+        if token_counts.shape != (batch, vocab):
+            _refuse("token_counts is [batch, vocab]")
+    st = load_library().mla_verify_tree(
+        target_probs.data_ptr(), target_stride, _ptr(draft_probs), draft_stride, dtype,
+        node_tokens.data_ptr(), tree_mask.data_ptr(), uniforms.data_ptr(), _ptr(num_nodes),
+        _ptr(seq_lens), batch, nodes, vocab, out_tokens.data_ptr(), path.data_ptr(),
+        num_accepted.data_ptr(), _ptr(seq_lens_out), _ptr(token_counts), _stream(stream))
+    _check(st, "mla_verify_tree")
+
+
+def mla_kv_compact(kv_pages: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                   path: torch.Tensor, num_accepted: torch.Tensor, stream=None) -> None:
+    """Move the kept nodes' cache entries behind each request's context, in every layer's cache.
+
+    ``kv_pages`` as in :func:`kv_dtype_code`, or several layers of it: one more dimension in front,
+    each layer contiguous. ``seq_lens`` are the lengths after verification, ``path [batch, N]`` and
+    ``num_accepted [batch]`` as :func:`mla_verify_tree` writes them.
+    """
+    several = kv_pages.dim() == (4 if kv_pages.shape[-1] == 576 else 3)
+    layers = int(kv_pages.shape[0]) if several else 1
+    if several and layers == 0:
+        _refuse("kv_pages has no layer")
+    first = kv_pages[0] if several else kv_pages
+    dtype = kv_dtype_code(first)
+    device = _device_of(kv_pages)
+    if block_table.dim() != 2:
+        _refuse("block_table is [batch, max_pages]")
+    batch, max_pages = block_table.shape
+    if path.dim() != 2 or path.shape[0] != batch:
+        _refuse("path is [batch, nodes]")
+    if seq_lens.numel() != batch or num_accepted.numel() != batch:
+        _refuse("seq_lens and num_accepted are [batch]")
+    _int32(device, block_table, seq_lens, path, num_accepted)
+    st = load_library().mla_kv_compact(
+        kv_pages.data_ptr(), layers, kv_pages.stride(0) * kv_pages.element_size() if several else 0,
+        int(first.shape[0]), _page_size(first), dtype, block_table.data_ptr(), max_pages,
+        seq_lens.data_ptr(), path.data_ptr(), num_accepted.data_ptr(), batch, int(path.shape[1]),
+        _stream(stream))
+    _check(st, "mla_kv_compact")
 
 
 def mla_decode_static_scratch(q: torch.Tensor, kv_pages: torch.Tensor,
