@@ -443,7 +443,7 @@ def _run_verify(s):
 
 
 def _run_compact(s):
-    case, pool, table, path = s["case"], s["pool"], s["table"], s["path"].long()
+    case, pool, table = s["case"], s["pool"], s["table"]
     four_bit = case["cache"] == "e2m1"
     if own:
         from paged_mla_decode_gb300 import binding
@@ -453,6 +453,7 @@ def _run_compact(s):
             binding.mla_kv_gather(pool, KV_SCALE, table, s["cu"], s["latent"], s["rope"], starts=s["starts"])
             return {"latent": s["latent"], "rope": s["rope"]}
         return {"pool": pool.view(torch.float8_e4m3fn) if case["cache"] == "e4m3" else pool}
+    path = s["path"].long()
     b, i = torch.nonzero(path >= 0, as_tuple=True)
     base = (s["lens"] - s["accepted"] - 1).long()[b]
     src, dst = base + path[b, i], base + i
