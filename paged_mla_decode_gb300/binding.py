@@ -725,12 +725,20 @@ def mla_kv_compact(kv_pages: torch.Tensor, block_table: torch.Tensor, seq_lens: 
     each layer contiguous. ``seq_lens`` are the lengths after verification, ``path [batch, N]`` and
     ``num_accepted [batch]`` as :func:`mla_verify_tree` writes them.
     """
-    several = kv_pages.dim() == (4 if kv_pages.shape[-1] == 576 else 3)
-    layers = int(kv_pages.shape[0]) if several else 1
-    if several and layers == 0:
-        _refuse("kv_pages has no layer")
-    first = kv_pages[0] if several else kv_pages
-    dtype = kv_dtype_code(first)
+    # (the whole tensor's shape and type are looked at: taking a layer out of it costs more
+    # host time than the launch)
+    shape = kv_pages.shape
+    inner = 2 if shape[-1] == MLA_E2M1_PAGE_BYTES else 3
+    several = len(shape) == inner + 1
+    if not several or not kv_pages.is_contiguous() or shape[0] == 0:
+        if several and shape[0] == 0:
+            _refuse("kv_pages has no layer")
+        dtype = kv_dtype_code(kv_pages[0] if several else kv_pages)
+    elif inner == 2 and kv_pages.dtype is torch.uint8:
+        dtype = MLA_KV_E2M1
+    else:
+        dtype = kv_dtype_code(kv_pages.view(-1, *shape[-2:]))
+    layers = shape[0] if several else 1
     device = _device_of(kv_pages)
     if block_table.dim() != 2:
         _refuse("block_table is [batch, max_pages]")
@@ -742,7 +750,7 @@ def mla_kv_compact(kv_pages: torch.Tensor, block_table: torch.Tensor, seq_lens: 
     _int32(device, block_table, seq_lens, path, num_accepted)
     st = load_library().mla_kv_compact(
         kv_pages.data_ptr(), layers, kv_pages.stride(0) * kv_pages.element_size() if several else 0,
-        int(first.shape[0]), _page_size(first), dtype, block_table.data_ptr(), max_pages,
+        shape[-inner], 64 if inner == 2 else shape[-2], dtype, block_table.data_ptr(), max_pages,
         seq_lens.data_ptr(), path.data_ptr(), num_accepted.data_ptr(), batch, int(path.shape[1]),
         _stream(stream))
     _check(st, "mla_kv_compact")

@@ -12,11 +12,12 @@
 // A drafted token's row also counts the drafts on its own path (the node mask's bits).
 //
 // A row is read once and written once, so DRAM bounds many rows. A cluster of up to eight
-// blocks keeps it in shared memory in between (163,840 floats are 80 KB a block): each block
-// makes exp(x - its own maximum) and their sum, the blocks exchange both once, and one factor
-// exp(own max - max) / sum finishes its part. Tokens that a list names (biases, drafts) are
-// worked out after the others, from their logits, by a thread an entry that adds up all of its
-// token's entries in order: two entries of a token write the same value.
+// blocks works a row in two passes over its logits: the first keeps a running maximum and
+// sum in every thread, which the blocks exchange through distributed shared memory; the second, which
+// finds the logits in L2, writes exp(x - max) / sum. Nothing is staged, so many blocks share an SM
+// and one's loads cover another's barriers. Tokens that a list names (biases, drafts) are left
+// out of the first pass, by a bit each, and worked out by a thread an entry, which adds up all of
+// its token's entries in order: two entries of a token come to the same value.
 #include <algorithm>
 #include <atomic>
 
@@ -31,9 +32,15 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kMaxCluster = 8;
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kMaxRun = 48 * 1024;  // tokens of a block: 192 KB of shared memory
-static_assert((int64_t)kMaxCluster * kMaxRun >= MLA_MAX_PROBS_VOCAB, "a row fits a cluster");
+// Two shapes of block. With few rows a block has an SM to itself and most of its loads should
+// be in flight at once; with many, several smaller blocks an SM cover each other's waits.
+struct Few {
+  static constexpr int kThreads = 1024, kBlocksPerSm = 1, kUnroll = 2;
+};
+struct Many {
+  static constexpr int kThreads = 256, kBlocksPerSm = 5, kUnroll = 1;
+};
+
 
 struct ProbsParams {
   const void* logits;
@@ -59,15 +66,18 @@ struct ProbsParams {
 
 // What changes a row's logits, the same for all of its tokens.
 struct RowSettings {
-  float repetition, frequency, presence;
+  float repetition, inverse, frequency, presence;
   const int32_t* counts;     // of the request; may be null
   const uint32_t* prompt;    // may be null
   const uint32_t* allowed;   // of the row; may be null
 };
 
+// (x / repetition is x times its rounded inverse: one more rounding of 2^-24, no division
+// for each token)
 __device__ __forceinline__ float penalised(float x, int count, bool in_prompt, const RowSettings& s) {
-  if (count > 0 || in_prompt) x = x > 0.f ? x / s.repetition : x * s.repetition;
-  if (count > 0) x = x - s.frequency * (float)count - s.presence;
+  const float f = x > 0.f ? s.inverse : s.repetition;
+  if (count > 0 || in_prompt) x *= f;
+  if (count > 0) x = x - fmaf(s.frequency, (float)count, s.presence);
   return x;
 }
 __device__ __forceinline__ bool bit_of(const uint32_t* words, int v) {
@@ -118,27 +128,98 @@ __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-struct BlockStats {
+// Running maximum and sum of exp((x - max) / t); greedy: the lowest token with the maximum.
+struct Stats {
   float max, sum;
-  int first;  // greedy: the lowest token with the maximum
+  int first;
 };
 
-// exp((x - m) / t) with k = 2 log2(e) / t >= 0 (of half the difference, which does not
-// overflow); 1 at the maximum whatever k, 0 at -inf and
-// beside an infinite maximum
+// exp((x - m) / t) for x <= m < inf, m > -inf, with k = 2 log2(e) / t (of half the
+// difference, which does not overflow)
 __device__ __forceinline__ float weight_of(float x, float m, float k) {
-  const float w = fast_exp2(fmaf(0.5f, x, -0.5f * m) * k);
-  return x == m ? 1.f : x == -INFINITY || m == INFINITY ? 0.f : w;
+  return fast_exp2(fmaf(0.5f, x, -0.5f * m) * k);
+}
+// the same for any m: beside an infinite maximum only its equals have a weight
+__device__ __forceinline__ float weight_of_any(float x, float m, float k) {
+  if (x == m) return m > -INFINITY ? 1.f : 0.f;
+  return m == INFINITY || x == -INFINITY ? 0.f : weight_of(x, m, k);
 }
 
+template <int kCount>
+__device__ __forceinline__ void add_tokens(Stats& s, const float (&x)[kCount], int token, bool greedy, float k) {
+  float top = x[0];
+#pragma unroll
+  for (int e = 1; e < kCount; ++e) top = fmaxf(top, x[e]);
+  if (top > s.max) {
+    s.sum = s.max > -INFINITY ? s.sum * weight_of_any(s.max, top, k) : 0.f;
+    s.max = top;
+    if (greedy) {
+#pragma unroll
+      for (int e = kCount - 1; e >= 0; --e)
+        if (x[e] == top) s.first = token + e;
+    }
+  }
+  if (greedy || s.max == -INFINITY) return;
+  if (s.max == INFINITY) {
+#pragma unroll
+    for (int e = 0; e < kCount; ++e) s.sum += x[e] == INFINITY ? 1.f : 0.f;
+    return;
+  }
+  float part = 0.f;
+#pragma unroll
+  for (int e = 0; e < kCount; ++e) part += weight_of(x[e], s.max, k);
+  s.sum += part;
+}
+// All lanes' together, the same in every lane.
+__device__ __forceinline__ Stats join(Stats s, float k) {
+  Stats r = s;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) r.max = fmaxf(r.max, __shfl_xor_sync(0xffffffffu, r.max, o));
+  r.sum = s.sum * weight_of_any(s.max, r.max, k);
+  r.first = s.max == r.max ? s.first : 0x7fffffff;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    r.sum += __shfl_xor_sync(0xffffffffu, r.sum, o);
+    r.first = min(r.first, __shfl_xor_sync(0xffffffffu, r.first, o));
+  }
+  return r;
+}
+
+// Eight tokens' settings as loaded: the counts and a byte each of prompt and grammar.
+struct EightSettings {
+  int4 a, b;
+  uint32_t prompt, allowed;
+  __device__ __forceinline__ void load(const RowSettings& st, int i) {
+    a = b = make_int4(0, 0, 0, 0);
+    if (st.counts) {
+      a = __ldg(reinterpret_cast<const int4*>(st.counts + i));
+      b = __ldg(reinterpret_cast<const int4*>(st.counts + i) + 1);
+    }
+    prompt = st.prompt ? __ldg(st.prompt + (i >> 5)) >> (i & 31) : 0u;
+    allowed = st.allowed ? __ldg(st.allowed + (i >> 5)) >> (i & 31) : 0xffu;
+  }
+  __device__ __forceinline__ void apply(float (&x)[8], const RowSettings& st, bool penalties) const {
+    if (penalties) {
+      const int c[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = penalised(x[e], c[e], (prompt >> e) & 1u, st);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = fmaxf(x[e], -INFINITY);  // (NaN: -inf)
+      if (!((allowed >> e) & 1u)) x[e] = -INFINITY;
+    }
+  }
+};
+
 // kVec: rows of logits, probabilities and counts allow 16-byte accesses.
-template <class In, class Out, bool kVec>
-__global__ void __launch_bounds__(kThreads) logits_probs_kernel(const ProbsParams p) {
-  extern __shared__ __align__(16) float s_x[];  // [run], then the lists
-  __shared__ BlockStats s_stats;  // read by the cluster
-  __shared__ float s_red[kWarps];
-  __shared__ int s_redi[kWarps];
-  __shared__ int s_paths;
+template <class In, class Out, bool kVec, class Shape>
+__global__ void __launch_bounds__(Shape::kThreads, Shape::kBlocksPerSm)
+    logits_probs_kernel(const ProbsParams p) {
+  constexpr int kThreads = Shape::kThreads, kWarps = kThreads / 32, kUnroll = Shape::kUnroll;
+  extern __shared__ uint32_t s_lists[];
+  __shared__ Stats s_stats;  // read by the cluster
+  __shared__ Stats s_warp[kWarps];
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -149,209 +230,179 @@ __global__ void __launch_bounds__(kThreads) logits_probs_kernel(const ProbsParam
   Out* probs = static_cast<Out*>(p.probs) + row * p.prob_stride;
   RowSettings st;
   st.repetition = p.repetition ? p.repetition[b] : 1.f;
+  st.inverse = 1.f / st.repetition;
   st.frequency = p.frequency ? p.frequency[b] : 0.f;
   st.presence = p.presence ? p.presence[b] : 0.f;
   st.counts = p.counts ? p.counts + (int64_t)b * V : nullptr;
   st.prompt = p.prompt ? p.prompt + (int64_t)b * p.words : nullptr;
   st.allowed = p.allowed ? p.allowed + row * p.words : nullptr;
   const float temperature = p.temperature ? p.temperature[b] : 1.f;
-  const bool greedy = !(temperature > 0.f);
-  const float k = 2.f * kLog2e / temperature;
+  const bool greedy = !(temperature > 0.f), penalties = p.penalties != 0;
+  // (within the positive floats: 0 or infinity times a difference could be NaN)
+  const float k = fminf(fmaxf(2.f * kLog2e / temperature, 0x1p-149f), 0x1.fffffep127f);
   const int lo = (int)min((int64_t)rank * p.run, (int64_t)V);
   const int hi = (int)min((int64_t)lo + p.run, (int64_t)V);
+  const int all8 = kVec ? lo + ((hi - lo) & ~7) : lo;  // tokens from here on go one by one
+  Stats mine{-INFINITY, 0.f, 0x7fffffff};
 
-  // ---- lists: the biases, and the drafts on this row's path ----
-  int32_t* s_bias_token = reinterpret_cast<int32_t*>(s_x + p.run);
-  float* s_bias = reinterpret_cast<float*>(s_bias_token + p.num_biases);
-  int32_t* s_path = reinterpret_cast<int32_t*>(s_bias + p.num_biases);  // [64]
-  for (int i = tid; i < p.num_biases; i += kThreads) {
-    s_bias_token[i] = p.bias_tokens[(int64_t)b * p.num_biases + i];
-    s_bias[i] = p.biases[(int64_t)b * p.num_biases + i];
-  }
+  // ---- the lists: biases, and the drafts on this row's path ----
   const uint64_t on_path =
-      p.tree_mask && p.penalties ? p.tree_mask[row] & ~1ull & (~0ull >> (64 - p.rows)) : 0;
-  if (tid < 64 && ((on_path >> tid) & 1u))
-    s_path[__popcll(on_path & ((1ull << tid) - 1))] = p.node_tokens[(int64_t)b * p.rows + tid];
-  if (tid == 0) s_paths = __popcll(on_path);
-
-  // ---- every token, without the lists ----
-  const bool plain = !p.penalties;
-  float top = -INFINITY;
-  if constexpr (kVec) {
-    constexpr int kUnroll = 2;
-    for (int i0 = lo; i0 < hi; i0 += kUnroll * 8 * kThreads) {
-      Eight<In> in[kUnroll];
-      int4 c[kUnroll][2];
-      uint32_t seen[kUnroll], ok[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + (u * kThreads + tid) * 8;
-        if (i + 8 <= hi) {
-          in[u].load(logits + i);
-          ok[u] = st.allowed ? __ldg(st.allowed + (i >> 5)) >> (i & 31) : 0xffu;
-          seen[u] = st.prompt ? __ldg(st.prompt + (i >> 5)) >> (i & 31) : 0u;
-          c[u][0] = c[u][1] = make_int4(0, 0, 0, 0);
-          if (st.counts) {
-            c[u][0] = __ldg(reinterpret_cast<const int4*>(st.counts + i));
-            c[u][1] = __ldg(reinterpret_cast<const int4*>(st.counts + i) + 1);
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + (u * kThreads + tid) * 8;
-        if (i + 8 <= hi) {
-          float x[8];
-          in[u].get(x);
-          if (!plain) {
-            const int cc[8] = {c[u][0].x, c[u][0].y, c[u][0].z, c[u][0].w,
-                               c[u][1].x, c[u][1].y, c[u][1].z, c[u][1].w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (cc[e] > 0 || ((seen[u] >> e) & 1u)) x[e] = penalised(x[e], cc[e], true, st);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (!((ok[u] >> e) & 1u) || isnan(x[e])) x[e] = -INFINITY;
-            top = fmaxf(top, x[e]);
-          }
-          float4* to = reinterpret_cast<float4*>(s_x + (i - lo));
-          to[0] = make_float4(x[0], x[1], x[2], x[3]);
-          to[1] = make_float4(x[4], x[5], x[6], x[7]);
-        }
-      }
-    }
-  }
-  // (all of them, one by one, or the last seven)
-  for (int i = (kVec ? lo + ((hi - lo) & ~7) : lo) + tid; i < hi; i += kThreads) {
-    float x = as_float(logits[i]);
-    if (!plain)
-      x = penalised(x, st.counts ? st.counts[i] : 0, st.prompt && bit_of(st.prompt, i), st);
-    if (isnan(x) || (st.allowed && !bit_of(st.allowed, i))) x = -INFINITY;
-    s_x[i - lo] = x;
-    top = fmaxf(top, x);
-  }
-  __syncthreads();
-
-  // ---- the tokens of the lists ----
-  const int paths = s_paths, entries = p.num_biases + paths;
+      p.tree_mask && penalties ? p.tree_mask[row] & ~1ull & (~0ull >> (64 - p.rows)) : 0;
+  const int paths = __popcll(on_path), entries = p.num_biases + paths;
+  int32_t* s_token = reinterpret_cast<int32_t*>(s_lists);       // [entries]
+  float* s_bias = reinterpret_cast<float*>(s_token + p.num_biases + 64);  // [num_biases]
+  float* s_x = s_bias + p.num_biases;                            // [entries]
+  uint32_t* s_listed = reinterpret_cast<uint32_t*>(s_x + p.num_biases + 64);  // [run / 32]
   if (entries > 0) {
+    for (int i = tid; i < p.num_biases; i += kThreads) {
+      s_token[i] = p.bias_tokens[(int64_t)b * p.num_biases + i];
+      s_bias[i] = p.biases[(int64_t)b * p.num_biases + i];
+    }
+    if (tid < 64 && ((on_path >> tid) & 1u))
+      s_token[p.num_biases + __popcll(on_path & ((1ull << tid) - 1))] =
+          p.node_tokens[(int64_t)b * p.rows + tid];
+    for (int i = tid; i < p.run / 32; i += kThreads) s_listed[i] = 0u;
+    __syncthreads();
     for (int e = tid; e < entries; e += kThreads) {
-      const int v = e < p.num_biases ? s_bias_token[e] : s_path[e - p.num_biases];
+      const int v = s_token[e];
       if (v < lo || v >= hi) continue;
       int count = st.counts ? max(st.counts[v], 0) : 0;
-      for (int i = 0; i < paths; ++i) count += s_path[i] == v;
       float x = as_float(logits[v]);
-      if (!plain) x = penalised(x, count, st.prompt && bit_of(st.prompt, v), st);
+      for (int i = 0; i < paths; ++i) count += s_token[p.num_biases + i] == v;
+      if (penalties) x = penalised(x, count, st.prompt && bit_of(st.prompt, v), st);
       for (int i = 0; i < p.num_biases; ++i)
-        if (s_bias_token[i] == v) x += s_bias[i];
-      if (isnan(x) || (st.allowed && !bit_of(st.allowed, v))) x = -INFINITY;
-      s_x[v - lo] = x;
+        if (s_token[i] == v) x += s_bias[i];
+      x = fmaxf(x, -INFINITY);
+      if (st.allowed && !bit_of(st.allowed, v)) x = -INFINITY;
+      s_x[e] = x;
+      const uint32_t bit = 1u << ((v - lo) & 31);
+      if (atomicOr(&s_listed[(v - lo) >> 5], bit) & bit) continue;  // its token is in the sum
+      const float one[1] = {x};
+      // (greedy: a thread's entries come in no order of tokens)
+      if (greedy && x == mine.max && x > -INFINITY) mine.first = min(mine.first, v);
+      else add_tokens(mine, one, v, greedy, k);
     }
     __syncthreads();
-    top = -INFINITY;  // (a bias may lower the maximum)
-    for (int i = tid; i < hi - lo; i += kThreads) top = fmaxf(top, s_x[i]);
   }
 
-  // ---- this block's maximum, then its exponentials and their sum ----
+  // ---- first pass: the row's maximum and sum ----
+  Stats dense{-INFINITY, 0.f, 0x7fffffff};
+  if constexpr (kVec) {
+    for (int i0 = lo + 8 * tid; i0 < all8; i0 += kUnroll * 8 * kThreads) {
+      Eight<In> in[kUnroll];
+      EightSettings set[kUnroll];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) s_red[warp] = top;
-  __syncthreads();
-  top = s_red[0];
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * 8 * kThreads;
+        if (i < all8) {
+          in[u].load(logits + i);
+          set[u].load(st, i);
+        }
+      }
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_red[w]);
-  float sum = 0.f;
-  int first = 0x7fffffff;
-  const int n4 = (hi - lo) >> 2;
-  if (greedy) {
-    for (int i = tid; i < hi - lo; i += kThreads)
-      if (s_x[i] == top) first = min(first, lo + i);
-  } else {
-    for (int i = tid; i < n4; i += kThreads) {
-      float4 x = reinterpret_cast<float4*>(s_x)[i];
-      x.x = weight_of(x.x, top, k);
-      x.y = weight_of(x.y, top, k);
-      x.z = weight_of(x.z, top, k);
-      x.w = weight_of(x.w, top, k);
-      sum += (x.x + x.y) + (x.z + x.w);
-      reinterpret_cast<float4*>(s_x)[i] = x;
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * 8 * kThreads;
+        if (i < all8) {
+          float x[8];
+          in[u].get(x);
+          if (entries > 0) set[u].allowed &= ~(s_listed[(i - lo) >> 5] >> ((i - lo) & 31));
+          set[u].apply(x, st, penalties);
+          add_tokens(dense, x, i, greedy, k);
+        }
+      }
     }
-    for (int i = 4 * n4 + tid; i < hi - lo; i += kThreads) sum += s_x[i] = weight_of(s_x[i], top, k);
   }
-  __syncthreads();  // (s_red has been read)
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+  auto one_token = [&](int i) -> float {
+    float x = as_float(logits[i]);
+    if (penalties)
+      x = penalised(x, st.counts ? st.counts[i] : 0, st.prompt && bit_of(st.prompt, i), st);
+    x = fmaxf(x, -INFINITY);
+    return st.allowed && !bit_of(st.allowed, i) ? -INFINITY : x;
+  };
+  for (int i = all8 + tid; i < hi; i += kThreads) {
+    if (entries > 0 && ((s_listed[(i - lo) >> 5] >> ((i - lo) & 31)) & 1u)) continue;
+    const float one[1] = {one_token(i)};
+    add_tokens(dense, one, i, greedy, k);
   }
-  if (lane == 0) {
-    s_red[warp] = sum;
-    s_redi[warp] = first;
+  // the entries' and the others'
+  {
+    const float top = fmaxf(mine.max, dense.max);
+    mine.first = min(mine.max == top ? mine.first : 0x7fffffff, dense.max == top ? dense.first : 0x7fffffff);
+    mine.sum = mine.sum * weight_of_any(mine.max, top, k) + dense.sum * weight_of_any(dense.max, top, k);
+    mine.max = top;
   }
+  mine = join(mine, k);
+  if (lane == 0) s_warp[warp] = mine;
   __syncthreads();
-  if (tid == 0) {
-    sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      sum += s_red[w];
-      first = min(first, s_redi[w]);
-    }
-    s_stats = BlockStats{top, sum, first};
+  if (warp == 0) {
+    mine = lane < kWarps ? s_warp[lane] : Stats{-INFINITY, 0.f, 0x7fffffff};
+    mine = join(mine, k);
+    if (lane == 0) s_stats = mine;
   }
   cluster.sync();
 
   // ---- all blocks': lane r looks at block r's ----
-  BlockStats mine{-INFINITY, 0.f, 0x7fffffff};
-  if (lane < ranks) mine = *cluster.map_shared_rank(&s_stats, lane);
-  float all = mine.max;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+  Stats all{-INFINITY, 0.f, 0x7fffffff};
+  if (lane < ranks) all = *cluster.map_shared_rank(&s_stats, lane);
   cluster.barrier_arrive();  // (nobody leaves before the others have read its numbers)
-  if (greedy) {
-    int at = mine.max == all && all > -INFINITY ? mine.first : 0x7fffffff;
+  all = join(all, k);
+  // ---- second pass: exp((x - max) / t) / sum ----
+  // (a row with nothing allowed has no maximum above -inf: all of it is 0)
+  const bool none = !(all.max > -INFINITY), infinite = all.max == INFINITY;
+  const float factor = none ? 0.f : 1.f / all.sum;
+  auto value = [&](float x, int i) -> float {
+    if (greedy) return i == all.first && !none ? 1.f : 0.f;
+    if (none) return 0.f;
+    return (infinite ? (x == INFINITY ? 1.f : 0.f) : weight_of(x, all.max, k)) * factor;
+  };
+  if constexpr (kVec) {
+    for (int i0 = lo + 8 * tid; i0 < all8; i0 += kUnroll * 8 * kThreads) {
+      Eight<In> in[kUnroll];
+      EightSettings set[kUnroll];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) at = min(at, __shfl_xor_sync(0xffffffffu, at, o));
-    for (int i = lo + tid; i < hi; i += kThreads) put(probs + i, i == at ? 1.f : 0.f);
-  } else {
-    float total = mine.sum * weight_of(mine.max, all, k);
-    if (all == -INFINITY) total = 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    // (a row with nothing allowed has no maximum above -inf: all of it is 0)
-    const float factor = all > -INFINITY && top > -INFINITY ? weight_of(top, all, k) / total : 0.f;
-    int from = lo;
-    if constexpr (kVec) {
-      for (int i = 8 * tid; i + 8 <= hi - lo; i += 8 * kThreads) {
-        const float4 a = reinterpret_cast<const float4*>(s_x + i)[0];
-        const float4 c = reinterpret_cast<const float4*>(s_x + i)[1];
-        const float x[8] = {a.x * factor, a.y * factor, a.z * factor, a.w * factor,
-                            c.x * factor, c.y * factor, c.z * factor, c.w * factor};
-        Eight<Out>::store(probs + lo + i, x);
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * 8 * kThreads;
+        if (i < all8) {
+          in[u].load(logits + i);
+          set[u].load(st, i);
+        }
       }
-      from = lo + ((hi - lo) & ~7);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * 8 * kThreads;
+        if (i < all8) {
+          float x[8];
+          in[u].get(x);
+          set[u].apply(x, st, penalties);
+          if (greedy || none || infinite) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = value(x[e], i + e);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = weight_of(x[e], all.max, k) * factor;
+          }
+          Eight<Out>::store(probs + i, x);
+        }
+      }
     }
-    for (int i = from + tid; i < hi; i += kThreads) put(probs + i, s_x[i - lo] * factor);
+  }
+  for (int i = all8 + tid; i < hi; i += kThreads) put(probs + i, value(one_token(i), i));
+  if (entries > 0) {
+    __syncthreads();  // (what was written for the listed tokens is written again)
+    for (int e = tid; e < entries; e += kThreads) {
+      const int v = s_token[e];
+      if (v < lo || v >= hi) continue;
+      put(probs + v, value(s_x[e], v));
+    }
   }
   cluster.barrier_wait();
 }
 
-template <class In, class Out, bool kVec>
-cudaError_t launch_probs(ProbsParams p, cudaStream_t stream) {
-  // blocks of a row: as many as keep 2,048 tokens each; runs of whole words of the masks
-  int ranks = 1;
-  while (ranks < kMaxCluster && p.vocab >= 2 * ranks * 2048) ranks *= 2;
-  p.run = ((p.vocab + ranks - 1) / ranks + 31) / 32 * 32;
-  const int bytes = 4 * p.run + 8 * p.num_biases + 4 * 64;
-  static std::atomic<int> configured[64];
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !configured[dev].load()) {
-    const cudaError_t e = cudaFuncSetAttribute(logits_probs_kernel<In, Out, kVec>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               4 * kMaxRun + 8 * MLA_MAX_BIASES + 4 * 64);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) configured[dev].store(1);
-  }
+template <class In, class Out, bool kVec, class Shape>
+cudaError_t launch_probs(const ProbsParams& p, int ranks, cudaStream_t stream) {
+  const size_t bytes = p.num_biases > 0 || p.tree_mask
+                           ? 4 * (size_t)(3 * p.num_biases + 2 * 64) + (size_t)p.run / 8
+                           : 0;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ranks;
@@ -359,21 +410,30 @@ cudaError_t launch_probs(ProbsParams p, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)p.batch * p.rows * ranks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)bytes;
+  cfg.blockDim = dim3(Shape::kThreads);
+  cfg.dynamicSmemBytes = bytes;  // at most 18 KB
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logits_probs_kernel<In, Out, kVec>, p);
+  return cudaLaunchKernelEx(&cfg, logits_probs_kernel<In, Out, kVec, Shape>, p);
 }
 
 template <class In, class Out>
-cudaError_t launch_probs(const ProbsParams& p, cudaStream_t stream) {
+cudaError_t launch_probs(ProbsParams p, cudaStream_t stream) {
+  // blocks of a row: as many as keep 2,048 tokens each; runs of whole words of the masks
+  int ranks = 1;
+  while (ranks < kMaxCluster && p.vocab >= 2 * ranks * 2048) ranks *= 2;
+  p.run = ((p.vocab + ranks - 1) / ranks + 31) / 32 * 32;
+  const bool few = (int64_t)p.batch * p.rows * ranks <= device_sm_count();
   const uintptr_t at = reinterpret_cast<uintptr_t>(p.logits) | reinterpret_cast<uintptr_t>(p.probs) |
                        (uintptr_t)(p.logit_stride * (int64_t)sizeof(In)) |
                        (uintptr_t)(p.prob_stride * (int64_t)sizeof(Out)) |
                        (p.counts ? reinterpret_cast<uintptr_t>(p.counts) | (uintptr_t)((int64_t)p.vocab * 4) : 0);
-  return (at & 15u) == 0 ? launch_probs<In, Out, true>(p, stream) : launch_probs<In, Out, false>(p, stream);
+  if ((at & 15u) == 0)
+    return few ? launch_probs<In, Out, true, Few>(p, ranks, stream)
+               : launch_probs<In, Out, true, Many>(p, ranks, stream);
+  return few ? launch_probs<In, Out, false, Few>(p, ranks, stream)
+             : launch_probs<In, Out, false, Many>(p, ranks, stream);
 }
 
 }  // namespace
