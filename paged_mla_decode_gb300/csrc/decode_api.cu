@@ -241,10 +241,10 @@ extern "C" mla_status mla_decode_tree(const void* q, const void* kv_pages, int64
   p.num_nodes = num_nodes;
   p.max_nodes = max_nodes;
   p.node_heads = num_heads;
-  if (!p.bf16 && num_pages > (int64_t)(0x7fffffff / kPageSize)) return MLA_ERR_UNSUPPORTED;
+  if (num_pages > (int64_t)(0x7fffffff / kPageSize)) return MLA_ERR_UNSUPPORTED;
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = p.bf16 ? launch_decode_tensor_core(p, s) : launch_decode_fp8(p, s);
+  cudaError_t e = p.bf16 ? launch_decode_bf16_tree(p, s) : launch_decode_fp8(p, s);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   e = launch_combine_pieces(p.ws, (int)rows, t.tile_rows, 1, G,
                             static_cast<__nv_bfloat16*>(out), lse, s, t.tiles, p.query_rows());

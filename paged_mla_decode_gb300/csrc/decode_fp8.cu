@@ -67,6 +67,7 @@
 #include "kv_e2m1.cuh"
 #include "mla_common.cuh"
 #include "mla_internal.h"
+#include "page_walk.cuh"
 #include "tc_ptx.cuh"
 
 // Clock-stamp points of the pipeline: nothing unless a tracing build defines
@@ -194,21 +195,6 @@ struct Map {
 
 enum Flag { F_ABORT = 0, F_PIECE_BAD = 1 };
 
-// What every role needs to know about the CTA's j-th page, written by the TMA
-// warp (the only planner walker) before it signals the page, read by the MMA and
-// softmax warps after they have waited for it.
-struct PageDesc {
-  int32_t page;    // block-table entry
-  int8_t valid;    // tokens of the row in this page (1..64)
-  int8_t context;  // tree decode: how many of them come before the nodes (below 0: the
-                   // page starts at node -context); 64 where all do
-  int16_t flags;   // kDescPieceStart | kDescPieceEnd | kDescPageOk
-  int32_t row;     // request row r = b * Q + j
-  int32_t slot;    // partial slot of this piece
-};
-constexpr int16_t kDescPieceStart = 1, kDescPieceEnd = 2, kDescPageOk = 4;
-constexpr int16_t kDescShared = 8;  // grouped decode: a shared-prefix page (informational)
-
 struct Fp8Params {
   const __nv_bfloat16* q;
   const uint8_t* kv;  // 4-bit cache only (an e4m3 cache is read through the tensor maps)
@@ -246,56 +232,6 @@ __device__ inline GroupPlan group_plan(const Fp8Params& p, int kind) {
   return GroupPlan{p.seq_lens, p.batch, p.nq, p.max_pages, kPageSize,
                    kind == 1 ? p.workers : p.G, 0, kind, p.forks, p.prefix_pages};
 }
-
-// Cursor over a CTA's pages (one page per step). The row's partial slot and
-// block-table offset are computed once per row: a step costs no division.
-// `cta` is the worker index in the plan; for the grouped decode's plans the
-// slot comes from the row table and `fork` picks the query row.
-template <class P>
-struct PageWalker {
-  P plan;
-  RowCursor cur;
-  int64_t x, x_end, x_begin;
-  int cta;         // this CTA's worker index in the plan
-  int fork;        // grouped decode: the fork this CTA works for
-  int slot;        // partial slot of the current row's piece in this CTA
-  int qrow;        // query / output row of the current row
-  int64_t bt_row;  // block-table offset of the current row's first page
-  const int32_t* row_base;  // grouped decode: the row table
-  const int32_t* row_np1;
-
-  __device__ void init(const P& p, const RowCursor& c, int cta_index, int64_t xb, int64_t xe,
-                       int fork_index = 0, const int32_t* rb = nullptr,
-                       const int32_t* np1 = nullptr) {
-    plan = p; cur = c; cta = cta_index; x = xb; x_begin = xb; x_end = xe;
-    fork = fork_index; row_base = rb; row_np1 = np1;
-    row_changed();
-    settle();
-  }
-  __device__ void row_changed() {
-    if constexpr (P::kGrouped) {
-      qrow = plan.q_row(cur.r, fork);
-      slot = __ldcg(row_base + qrow) + (plan.kind == 2 ? __ldcg(row_np1 + qrow) : 0) +
-             (cta - plan.cta_of(cur.rt));
-    } else {
-      qrow = cur.r;
-      slot = cur.base + (cta - plan.cta_of(cur.rt));
-    }
-    bt_row = plan.bt_base(cur.r);
-  }
-  __device__ void settle() {
-    if (x < x_end && x == cur.rt + cur.t) {
-      cursor_next_row(plan, cur);
-      row_changed();
-    }
-  }
-  __device__ int page_in_row() const { return (int)(x - cur.rt); }
-  __device__ bool piece_start() const { return x == x_begin || x == cur.rt; }
-  __device__ bool piece_end() const { return x + 1 == x_end || x + 1 == cur.rt + cur.t; }
-  __device__ int valid_tokens() const { return min(kPageSize, cur.n - page_in_row() * kPageSize); }
-  __device__ void next() { ++x; settle(); }
-  __device__ bool shared() const { return false; }
-};
 
 // The grouped decode's walker: this CTA's range of the shared-prefix plan (as
 // fork `fork` of its worker), then its range of the suffix plan.
@@ -363,30 +299,9 @@ __device__ __forceinline__ float4 e4m3x4_value(uint32_t codes) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// Two float operations in one instruction, each rounded as by itself. The softmax warps
+// Float additions and products go two at a time (add2 and its like): the softmax warps
 // share their schedulers with the other roles: 31 requests of 60k-140k tokens 382 us with
-// a 4-bit cache, 390 without these; e4m3 327 and 331.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n .reg .b64 a, b, r;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
-      " add.rn.f32x2 r, a, b;\n mov.b64 {%0, %1}, r;\n}\n"
-      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n .reg .b64 a, b, r;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
-      " mul.rn.f32x2 r, a, b;\n mov.b64 {%0, %1}, r;\n}\n"
-      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n .reg .b64 a, b, c, r;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
-      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 r, a, b, c;\n mov.b64 {%0, %1}, r;\n}\n"
-      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
+// a 4-bit cache, 390 one by one; e4m3 327 and 331.
 
 // Rows of the expansion table by exponent nibble (e2m1_as_e4m3), copied to shared memory.
 __device__ const uint64_t kE2m1Lut[16] = {
@@ -479,14 +394,6 @@ __device__ __forceinline__ void expand_page(const Expander& x, uint32_t raw, uin
   }
 }
 
-// Bit i: token i of the 16 from token `first` of a page on is one that a query row with
-// node mask m sees, where the page's first `context` tokens come before the nodes.
-__device__ __forceinline__ uint32_t tree_visible(uint64_t m, int context, int first) {
-  const int s = context - first;  // of the 16, before the nodes
-  if (s >= 16) return 0xffffu;
-  const uint64_t nodes = s >= 0 ? m << s : m >> -s;
-  return ((uint32_t)nodes | (s > 0 ? (1u << s) - 1u : 0u)) & 0xffffu;
-}
 // Whether one of four e4m3 codes is a NaN (0x7f, 0xff).
 __device__ __forceinline__ bool e4m3x4_has_nan(uint32_t w) {
   return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;

@@ -26,7 +26,6 @@
 // Every mbarrier wait is bounded (2 s); on timeout the CTA records
 // MLA_DEVICE_ERR_TIMEOUT, stops, drains its MMAs (bounded) and frees TMEM.
 #include <atomic>
-#include <type_traits>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -98,22 +97,16 @@ struct TcParams {
   float kv_scale;
   int G;
   DecodeWorkspace ws;
-  // tree decode (kTree) only: nq is the tiles of a request, heads the rows of a tile
-  const uint64_t* tree_mask;
-  const int32_t* num_nodes;
-  int max_nodes, node_heads;
-  int query_rows;  // of a request
 };
 
 // One tile: up to two consecutive pages of one row inside this CTA's range.
-template <class P>
-struct TileWalkerOf {
-  P plan;
+struct TileWalker {
+  Plan plan;
   RowCursor cur;
   int64_t x, x_end, x_begin;
   int npages;       // pages in the current tile (1 or 2)
 
-  __device__ void init(const P& p, const RowCursor& c, int64_t xb, int64_t xe) {
+  __device__ void init(const Plan& p, const RowCursor& c, int64_t xb, int64_t xe) {
     plan = p; cur = c; x = xb; x_begin = xb; x_end = xe;
     settle();
   }
@@ -200,7 +193,7 @@ __device__ __forceinline__ void transpose_reduce64(float (&v)[64], int lane, flo
   head0 = base;
 }
 
-template <bool kBf16, bool kTree>
+template <bool kBf16>
 __global__ void __maxnreg__(168)
     decode_tc_kernel(const TcParams p, const __grid_constant__ CUtensorMap q_map) {
   extern __shared__ uint8_t smem_raw[];
@@ -221,15 +214,7 @@ __global__ void __maxnreg__(168)
 
   // ---- planning (shared by all roles) ----
   __shared__ int64_t s_plan[6];
-  using RowPlan = std::conditional_t<kTree, TreePlan, Plan>;
-  using TileWalker = TileWalkerOf<RowPlan>;
-  RowPlan plan;
-  if constexpr (kTree)
-    plan = TreePlan{p.seq_lens, p.num_nodes, p.batch, p.max_nodes, p.node_heads, p.nq, p.heads,
-                    p.max_pages, kPageSize, p.G, 0};
-  else
-    plan = Plan{p.seq_lens, p.batch, p.nq, p.max_pages, kPageSize, p.G, 0};
-  __shared__ uint64_t s_nodes_seen[kTree ? kN : 1];  // of each row of the tile
+  Plan plan{p.seq_lens, p.batch, p.nq, p.max_pages, kPageSize, p.G, 0};
   if (warp == 0) {
     const int64_t T = plan_total_tiles_warp(plan);
     if (lane == 0) s_plan[0] = T;
@@ -287,9 +272,8 @@ __global__ void __maxnreg__(168)
       auto issue_q = [&](int r) {
         tc::mbar_arrive_expect_tx(bar(BAR_Q_TMA), (uint32_t)(kChunks * H * 128));
         for (int ch = 0; ch < kChunks; ++ch)
-          // (a tree's last tile may reach into the next request, or past the end: zeros)
-          tc::tma_load_2d(sbase + kOffQ + ch * kQChunkBytes, &q_map, 64 * ch,
-                          r / p.nq * p.query_rows + r % p.nq * H, bar(BAR_Q_TMA));
+          tc::tma_load_2d(sbase + kOffQ + ch * kQChunkBytes, &q_map, 64 * ch, r * H,
+                          bar(BAR_Q_TMA));
       };
       // rows H..63 of the Q tile stay zero (padded heads); TMA writes only rows < H
       if (H < kN) {
@@ -631,9 +615,6 @@ __global__ void __maxnreg__(168)
             }
           }
           if (hf == 0) qm_w[h] = h < H ? p.score_mul * ldexpf(1.0f, -shift) : 0.f;
-          if constexpr (kTree) {
-            if (hf == 0) s_nodes_seen[h] = h < H ? tree_row_mask(plan, p.tree_mask, tw.cur.r, h) : 0;
-          }
           tc::fence_proxy_async_smem();
           named_bar_softmax();  // q tile and qmul ready
         }
@@ -705,31 +686,6 @@ __global__ void __maxnreg__(168)
           s[4 * h4 + 1] = vis ? s[4 * h4 + 1] * c4.y : -INFINITY;
           s[4 * h4 + 2] = vis ? s[4 * h4 + 2] * c4.z : -INFINITY;
           s[4 * h4 + 3] = vis ? s[4 * h4 + 3] * c4.w : -INFINITY;
-        }
-        if constexpr (kTree) {
-          // this token's number among the nodes: of those, a row sees the ones in its mask
-          const int node = tw.page_in_row() * kPageSize + t -
-                           (tw.cur.n - plan.nodes(tw.cur.r / plan.tiles));
-          if (vis && node >= 0) {
-#pragma unroll
-            for (int h = 0; h < kN; ++h)
-              if (!((s_nodes_seen[h] >> node) & 1u)) s[h] = -INFINITY;
-            // A NaN or an infinity in a node's entry is the scores' of the rows that see it;
-            // for the others it would be 0 * NaN in PV, so chunks with one become zeros.
-            // (All of them have been read by QK.)
-#pragma unroll 1
-            for (int u = 0; u < kDLatent / 8; ++u) {
-              const uint32_t a = sbase + kv_tile_off(t, u & 7, u >> 3);
-              uint32_t w[4];
-              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
-              bool bad = false;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                bad |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
-              if (bad) asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(a), "r"(0u));
-            }
-          }
         }
         // Lazy running max: the per-head maximum over the tile is needed only when
         // some score exceeds its head's current max by more than the threshold (or
@@ -870,10 +826,7 @@ __global__ void __maxnreg__(168)
           float* out = p.ws.part_out + (int64_t)slot * H * kDLatent + t;
           if (t < 64) {
             const float* rs = red_sum + (k & 1) * 256;
-            float l = l_sum[t] + rs[t] + rs[64 + t] + rs[128 + t] + rs[192 + t];
-            if constexpr (kTree) {  // (a row without a node has whatever its q gives)
-              if (!tree_row_live(plan, tw.cur.r, t)) l = 0.f;
-            }
+            const float l = l_sum[t] + rs[t] + rs[64 + t] + rs[128 + t] + rs[192 + t];
             l_sum[t] = l;
             alpha[t] = l > 0.f ? p.kv_scale / l : 0.f;  // 1/l per head
           }
@@ -932,13 +885,13 @@ __global__ void __maxnreg__(168)
   if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-template <bool kBf16, bool kTree = false>
+template <bool kBf16>
 cudaError_t launch_decode_tc(const TcParams& p, cudaStream_t stream) {
   static std::atomic<int> configured[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !configured[dev].load()) {
-    cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<kBf16, kTree>,
+    cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<kBf16>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     configured[dev].store(1);
@@ -955,7 +908,7 @@ cudaError_t launch_decode_tc(const TcParams& p, cudaStream_t stream) {
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
   CUtensorMap q_map;
-  const cuuint64_t dims[2] = {(cuuint64_t)kDEntry, (cuuint64_t)p.batch * p.query_rows};
+  const cuuint64_t dims[2] = {(cuuint64_t)kDEntry, (cuuint64_t)p.batch * p.nq * p.heads};
   const cuuint64_t strides[1] = {(cuuint64_t)kDEntry * 2};
   const cuuint32_t box[2] = {64, (cuuint32_t)p.heads};
   const cuuint32_t estr[2] = {1, 1};
@@ -964,7 +917,7 @@ cudaError_t launch_decode_tc(const TcParams& p, cudaStream_t stream) {
                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-  decode_tc_kernel<kBf16, kTree><<<p.G, kThreads, kSmemBytes, stream>>>(p, q_map);
+  decode_tc_kernel<kBf16><<<p.G, kThreads, kSmemBytes, stream>>>(p, q_map);
   return cudaGetLastError();
 }
 
@@ -985,12 +938,6 @@ cudaError_t launch_decode_tensor_core(const DecodeLaunch& d, cudaStream_t stream
   p.kv_scale = d.kv_scale;
   p.G = d.G;
   p.ws = d.ws;
-  p.tree_mask = d.tree_mask;
-  p.num_nodes = d.num_nodes;
-  p.max_nodes = d.max_nodes;
-  p.node_heads = d.node_heads;
-  p.query_rows = d.query_rows();
-  if (d.tree_mask != nullptr) return launch_decode_tc<true, true>(p, stream);  // bf16 cache
   return d.bf16 ? launch_decode_tc<true>(p, stream) : launch_decode_tc<false>(p, stream);
 }
 

@@ -60,6 +60,9 @@ cudaError_t launch_decode_tensor_core(const DecodeLaunch& d, cudaStream_t stream
 // decode kernel, which reads it.
 cudaError_t launch_decode_fp8(const DecodeLaunch& d, cudaStream_t stream);
 
+// Split-KV tree decode over a bf16 cache (decode_bf16_tree.cu); num_pages * 64 < 2^31.
+cudaError_t launch_decode_bf16_tree(const DecodeLaunch& d, cudaStream_t stream);
+
 // Merge the pieces written by a decode kernel into out (bf16) and lse (fp32);
 // max_pieces_per_row is the number of decode CTAs (it sizes the staging), passes
 // the number of plans that cut the rows (2 for the grouped decode). Row r, head h goes to
