@@ -47,13 +47,20 @@ extern "C" size_t mla_decode_grouped_workspace_size(int batch, int num_queries, 
 }
 
 namespace {
-// The query rows of a tree decode's requests, as TreePlan cuts them.
+// The query rows of a tree decode's requests, as TreePlan cuts them, and its workers: CTAs with
+// a tile of up to 64 rows each, or pairs of CTAs with 128.
 struct TreeShape {
-  int tiles, tile_rows;
+  int tiles, tile_rows, workers;
 };
-TreeShape tree_shape(int max_nodes, int num_heads) {
+TreeShape tree_shape(int max_nodes, int num_heads, int num_ctas, bool may_pair) {
   const int rows = max_nodes * num_heads;
-  return rows <= 64 ? TreeShape{1, rows} : TreeShape{(rows + 63) / 64, 64};
+  if (rows <= 64) return TreeShape{1, rows, num_ctas};
+  const int tiles = (rows + 63) / 64;
+  // a pair takes 0.8 of the time that its CTAs would take one by one, and an odd number of
+  // tiles costs it a half that has no rows
+  if (may_pair && num_ctas >= 2 && (tiles % 2 == 0 || tiles >= 5))
+    return TreeShape{(tiles + 1) / 2, 128, num_ctas / 2};
+  return TreeShape{tiles, 64, num_ctas};
 }
 bool tree_shape_ok(int batch, int max_nodes, int num_heads) {
   return batch >= 0 && max_nodes >= 1 && max_nodes <= MLA_MAX_TREE_NODES &&
@@ -183,8 +190,13 @@ extern "C" size_t mla_decode_tree_workspace_size(int batch, int max_nodes, int n
   if (!tree_shape_ok(batch, max_nodes, num_heads) || num_ctas < 0) return 0;
   if (num_ctas == 0) num_ctas = mla::device_sm_count();
   if (num_ctas <= 0) return 0;
-  const TreeShape t = tree_shape(max_nodes, num_heads);
-  return mla::workspace_layout((int64_t)batch * t.tiles, t.tile_rows, num_ctas).total;
+  size_t most = 0;  // (the cache's type is not known here)
+  for (const bool may_pair : {false, true}) {
+    const TreeShape t = tree_shape(max_nodes, num_heads, num_ctas, may_pair);
+    const size_t n = mla::workspace_layout((int64_t)batch * t.tiles, t.tile_rows, t.workers).total;
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 extern "C" mla_status mla_decode_tree(const void* q, const void* kv_pages, int64_t num_pages,
@@ -215,10 +227,11 @@ extern "C" mla_status mla_decode_tree(const void* q, const void* kv_pages, int64
   if ((int64_t)batch * max_pages > 0x7fffffffLL) return MLA_ERR_UNSUPPORTED;
   const int G = num_ctas ? num_ctas : device_sm_count();
   if (G <= 0) return MLA_ERR_CUDA;
-  const TreeShape t = tree_shape(max_nodes, num_heads);
+  // (a 4-bit cache's pages are expanded by each CTA for itself)
+  const TreeShape t = tree_shape(max_nodes, num_heads, G, kv_dtype != MLA_KV_E2M1);
   const int64_t rows = (int64_t)batch * t.tiles;
   if (rows * t.tile_rows > 0x7fffffffLL) return MLA_ERR_UNSUPPORTED;
-  const WorkspaceLayout L = workspace_layout(rows, t.tile_rows, G);
+  const WorkspaceLayout L = workspace_layout(rows, t.tile_rows, t.workers);
   if (workspace_bytes < L.total) return MLA_ERR_WORKSPACE;
 
   DecodeLaunch p;
@@ -235,7 +248,7 @@ extern "C" mla_status mla_decode_tree(const void* q, const void* kv_pages, int64
   p.e2m1 = kv_dtype == MLA_KV_E2M1;
   p.score_mul = sm_scale * kLog2e * kv_scale;
   p.kv_scale = kv_scale;
-  p.G = G;
+  p.G = t.workers;
   carve_workspace(p.ws, workspace, L);
   p.tree_mask = tree_mask;
   p.num_nodes = num_nodes;
@@ -246,7 +259,7 @@ extern "C" mla_status mla_decode_tree(const void* q, const void* kv_pages, int64
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = p.bf16 ? launch_decode_bf16_tree(p, s) : launch_decode_fp8(p, s);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
-  e = launch_combine_pieces(p.ws, (int)rows, t.tile_rows, 1, G,
+  e = launch_combine_pieces(p.ws, (int)rows, t.tile_rows, 1, t.workers,
                             static_cast<__nv_bfloat16*>(out), lse, s, t.tiles, p.query_rows());
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

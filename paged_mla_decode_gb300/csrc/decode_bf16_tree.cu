@@ -76,7 +76,8 @@ enum Bar {
   BAR_Q_FULL = BAR_O_EMPTY + 1,       // the query tile's bytes landed
   BAR_Q_EMPTY = BAR_Q_FULL + 1,       // QK of the piece's last page is done
   BAR_DRAIN = BAR_Q_EMPTY + 1,        // [2] one per issuer warp
-  kNumBars = BAR_DRAIN + 2
+  BAR_FREE = BAR_DRAIN + 2,           // [2] pairs: both CTAs' PVs have read the page in the slot
+  kNumBars = BAR_FREE + 2
 };
 constexpr int kOffTmem = kOffBar + 8 * kNumBars;
 constexpr int kSmemBytes = kOffTmem + 16 + 1024;  // slack for the 1024 alignment
@@ -122,6 +123,9 @@ __device__ __forceinline__ bool bf16x2_not_finite(uint32_t w) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
+// kPair: two CTAs of a cluster walk the same pages for the two halves of a 128-row tile, each
+// bringing half of every page into both CTAs' shared memory (as in decode_fp8.cu).
+template <bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_bf16_tree_kernel(const Bf16TreeParams p, const __grid_constant__ CUtensorMap kv_map,
                             const __grid_constant__ CUtensorMap q_map) {
@@ -139,7 +143,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * (uint32_t)i; };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int c = blockIdx.x;
+  const int c = kPair ? blockIdx.x >> 1 : blockIdx.x;
+  const int half = kPair ? (int)tc::cluster_rank() : 0;  // of the tile's rows
+  constexpr uint16_t kBoth = 3;
   griddep_wait();  // all earlier work in the stream is complete
   TreePlan plan{p.seq_lens, p.num_nodes, p.batch, p.max_nodes, p.node_heads, p.tiles, p.tile_rows,
                 p.max_pages, kPageSize, p.G, 0};
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     TreePlan pl = plan;
     pl.set_total(plan_total_tiles_warp(pl));
     const int64_t xb = c < pl.G ? pl.cta_start(c) : 0;
-    const RowCursor f = plan_find_row_warp(pl, xb, c == 0, p.ws.row_base, p.ws.row_np, p.ws.status);
+    const RowCursor f = plan_find_row_warp(pl, xb, c == 0 && half == 0, p.ws.row_base, p.ws.row_np, p.ws.status);
     if (lane == 0) {
       s_plan[0] = pl.T;
       s_plan[1] = f.r;
@@ -162,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::prefetch_tensormap(&q_map);
     for (int i = 0; i < kNumBars; ++i) {
       const bool by_softmax = (i >= BAR_S_EMPTY && i < BAR_P_FULL + 2) || i == BAR_O_EMPTY;
-      tc::mbar_init(bar(i), by_softmax ? kSmWarps : 1);
+      tc::mbar_init(bar(i), by_softmax ? kSmWarps : i >= BAR_FREE ? 2 : 1);
     }
     tc::fence_mbar_init();
     flags[F_ABORT] = 0;
@@ -173,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_relinquish();
   }
   // rows that TMA does not write (a request of fewer than 64) are zeros
-  if (p.tile_rows < kTileRows) {
+  if (!kPair && p.tile_rows < kTileRows) {
     const int units = (kTileRows - p.tile_rows) * 8;  // 16-byte pieces of a chunk
     for (int i = tid; i < kChunks * units; i += kThreads) {
       const int ch = i / units, u = i - ch * units;
@@ -185,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
+  if constexpr (kPair) tc::cluster_sync();  // both CTAs' barriers are there
   tc::fence_after_sync();
   griddep_launch_dependents();  // the merge may be scheduled (it waits for this grid)
   plan.set_total(s_plan[0]);
@@ -192,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t x_begin = works ? plan.cta_start(c) : 0, x_end = works ? plan.cta_start(c + 1) : 0;
   const uint32_t tmem = *tmem_slot;
   const RowCursor cur0{(int)s_plan[1], s_plan[2], (int)s_plan[3], (int)s_plan[4], (int)s_plan[5]};
-  const int H = p.tile_rows;
+  const int H = kPair ? kTileRows : p.tile_rows;  // rows of this CTA
+  const int row_step = kPair ? 2 * H : H, row0 = H * half;  // in a piece's partials
   auto abort_cta = [&]() {
     flags[F_ABORT] = 1;
     atomicOr(p.ws.status, MLA_DEVICE_ERR_TIMEOUT);
@@ -241,20 +249,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++piece;
             const int b = d->row / p.tiles;
-            const int y = b * p.query_rows + (d->row - b * p.tiles) * H;
+            const int y = b * p.query_rows + (d->row - b * p.tiles) * row_step + row0;
             tc::mbar_arrive_expect_tx(bar(BAR_Q_FULL), (uint32_t)(kChunks * H * 128));
             for (int ch = 0; ch < kChunks; ++ch)
               tc::tma_load_2d(sbase + kOffQ + ch * kChunkBytes, &q_map, 64 * ch, y, bar(BAR_Q_FULL));
           }
           const int slot = (int)(j % kSlots);
           if (j >= kSlots &&
-              (!tc::mbar_wait(bar(BAR_PV_DONE + slot), (uint32_t)(j / kSlots - 1) & 1, kWaitNs) ||
+              (!tc::mbar_wait(bar((kPair ? BAR_FREE : BAR_PV_DONE) + slot), (uint32_t)(j / kSlots - 1) & 1, kWaitNs) ||
                flags[F_ABORT])) {
             ok = false;
             break;
           }
           if (page_ok) {
             tc::mbar_arrive_expect_tx(bar(BAR_PAGE_FULL + slot), (uint32_t)kPageBytes);
+            if constexpr (kPair) {  // (the other half's bytes count here too)
+              for (int ch = 5 * half; ch < (half ? kChunks : 5); ++ch)
+                tc::tma_load_2d_multicast_hint(sbase + slot * kPageBytes + ch * kChunkBytes, &kv_map, 64 * ch,
+                                               d->page * kPageSize, bar(BAR_PAGE_FULL + slot), kBoth, pol);
+            } else
             for (int ch = 0; ch < kChunks; ++ch)
               tc::tma_load_2d_hint(sbase + slot * kPageBytes + ch * kChunkBytes, &kv_map, 64 * ch,
                                    d->page * kPageSize, bar(BAR_PAGE_FULL + slot), pol);
@@ -270,6 +283,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int64_t jj = j > kSlots ? j - kSlots : 0; jj < j; ++jj)
           tc::mbar_wait(bar(BAR_PAGE_FULL + (int)(jj % kSlots)), (uint32_t)(jj / kSlots) & 1, kWaitNs);
         if (piece > 0) tc::mbar_wait(bar(BAR_Q_FULL), (uint32_t)(piece - 1) & 1, kWaitNs);
+        // nor may the other CTA's commits arrive here after that
+        if constexpr (kPair) {
+          for (int64_t jj = j > kSlots ? j - kSlots : 0; jj < j; ++jj)
+            tc::mbar_wait(bar(BAR_FREE + (int)(jj % kSlots)), (uint32_t)(jj / kSlots) & 1, kWaitNs);
+        }
       }
       __syncwarp();
     } else if (warp >= kQkWarp) {
@@ -325,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                va + (uint64_t)((2 * blk * kChunkBytes + s * 2048) >> 4),
                                pb + (uint64_t)((32 * s) >> 4), id_pv, 1);
             tc::mma_commit(bar(BAR_PV_DONE + slot));
+            if constexpr (kPair) tc::mma_commit_multicast(bar(BAR_FREE + slot), kBoth);
             if (pe) tc::mma_commit(bar(BAR_O_FULL));
           }
         }
@@ -378,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           atomicOr(p.ws.status, MLA_DEVICE_ERR_BAD_PAGE);
         }
         if (ps && !stop) {
-          nodes_seen = h < H ? tree_row_mask(plan, p.tree_mask, d.row, h) : 0;
-          row_live = h < H && tree_row_live(plan, d.row, h);
+          nodes_seen = h < H ? tree_row_mask(plan, p.tree_mask, d.row, row0 + h) : 0;
+          row_live = h < H && tree_row_live(plan, d.row, row0 + h);
           m = -INFINITY;
           lpart = 0.f;
         }
@@ -524,15 +543,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             linv_s[h] = l > 0.f ? p.kv_scale / l : 0.f;
             if (h < H)
               // (a NaN among the scores: lse = +inf, with which the merge makes the row NaN)
-              p.ws.part_lse[(int64_t)d.slot * H + h] = l > 0.f    ? (m + log2f(l)) * kLn2
+              p.ws.part_lse[(int64_t)d.slot * row_step + row0 + h] = l > 0.f    ? (m + log2f(l)) * kLn2
                                                        : l == 0.f ? -INFINITY
                                                                   : INFINITY;
           }
-          if (tid == 0) p.ws.piece_err[d.slot] = bad;
+          if (tid == 0 && half == 0) p.ws.piece_err[d.slot] = bad;  // (a pair's pages are the same)
           bar_softmax();
           // O^T lane = dim 128*blk + 32*(w%4) + lane; this warp writes rows 32g .. 32g+31
           if (32 * g < H) {
-            float* out = p.ws.part_out + (int64_t)d.slot * H * kDLatent + 32 * q4 + lane;
+            float* out = p.ws.part_out + ((int64_t)d.slot * row_step + row0) * kDLatent + 32 * q4 + lane;
 #pragma unroll 1
             for (int blk = 0; blk < 4; ++blk) {
               uint32_t rr[32];
@@ -552,8 +571,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
+  // (the other CTA's copies and commits go to this one's shared memory as long as it works)
+  if constexpr (kPair) tc::cluster_sync();
   tc::fence_after_sync();
   if (warp == kQkWarp) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <bool kPair>
+cudaError_t launch_kernel(const Bf16TreeParams& p, const CUtensorMap& kv_map, const CUtensorMap& q_map,
+                          cudaStream_t stream) {
+  static std::atomic<int> configured[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !configured[dev].load()) {
+    const cudaError_t e = cudaFuncSetAttribute(decode_bf16_tree_kernel<kPair>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) configured[dev].store(1);
+  }
+  cudaLaunchAttribute attr[2] = {pdl_attribute(), pair_attribute()};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(kPair ? 2 * p.G : p.G));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, decode_bf16_tree_kernel<kPair>, p, kv_map, q_map);
 }
 
 }  // namespace
@@ -569,15 +613,6 @@ cudaError_t launch_decode_bf16_tree(const DecodeLaunch& d, cudaStream_t stream) 
       return cudaErrorNotSupported;
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
-  static std::atomic<int> configured[64];
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !configured[dev].load()) {
-    const cudaError_t e = cudaFuncSetAttribute(decode_bf16_tree_kernel,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) configured[dev].store(1);
-  }
   // pages as rows of 576 dims, and the query rows: boxes of 64 dims, a page or a tile high
   CUtensorMap kv_map, q_map;
   const cuuint64_t strides[1] = {(cuuint64_t)kDEntry * 2};
@@ -590,7 +625,7 @@ cudaError_t launch_decode_bf16_tree(const DecodeLaunch& d, cudaStream_t stream) 
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   if (!map(&kv_map, d.kv, (d.num_pages > 0 ? d.num_pages : 1) * kPageSize, kPageSize) ||
-      !map(&q_map, d.q, (int64_t)d.batch * d.query_rows(), d.heads))
+      !map(&q_map, d.q, (int64_t)d.batch * d.query_rows(), d.heads > kTileRows ? kTileRows : d.heads))
     return cudaErrorInvalidValue;
   Bf16TreeParams p;
   p.num_pages = d.num_pages;
@@ -609,15 +644,8 @@ cudaError_t launch_decode_bf16_tree(const DecodeLaunch& d, cudaStream_t stream) 
   p.max_nodes = d.max_nodes;
   p.node_heads = d.node_heads;
   p.query_rows = d.query_rows();
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.G);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_bf16_tree_kernel, p, kv_map, q_map);
+  return d.heads > kTileRows ? launch_kernel<true>(p, kv_map, q_map, stream)
+                             : launch_kernel<false>(p, kv_map, q_map, stream);
 }
 
 }  // namespace mla
