@@ -90,15 +90,15 @@ __device__ __forceinline__ void merge_row(const float* __restrict__ out_base, in
 // Units are (row, head, quarter of the 512 dims). With few rows each may have many pieces,
 // and every unit is merged by a block (merge_unit: the slices staged by bulk copies).
 // Otherwise only the rows of more than kFewPieces pieces are, of which there are at most
-// `many_rows` (every CTA's range cuts one row at most), and the other units take a warp
-// each: a block would spend its barriers and its staging on a few pieces there. The grid
+// `many_rows` (every CTA's range cuts one row at most), and of the others a warp takes a
+// (row, head) each: a block would spend its barriers and its staging on a few pieces there. The grid
 // then starts with the blocks of the rows of many pieces; each looks for its row in the
 // row table and leaves if there is none. A decode call of 256 rows of 8 pages, 64 heads,
 // takes 84 us, with a block per unit throughout 178; 48 rows of one page 28 and 42; one
 // row of 100k tokens among 31 of one page 101 and 110. For the few rows the first kernel
 // stays: it has 32 registers a thread, the second 52 (8 rows of 20k tokens 47 us, 53).
 constexpr int kFewPieces = 16;
-constexpr int kWarpMergeLoads = 4;  // pieces whose loads are in flight (8: 95 us, 16: 168 on the 256 rows)
+constexpr int kWarpMergeLoads = 2;  // pieces whose loads are in flight (each all four quarters)
 
 struct MergeParams {
   const int32_t* row_base;
@@ -157,11 +157,10 @@ __device__ __forceinline__ int find_row_of_many(const MergeParams& p, int k) {
   return s_found;
 }
 
-// One unit by one warp: lane l keeps dims 4l .. 4l + 3 of its 128, and the weight of one of
-// 32 pieces at a time.
-__device__ __forceinline__ void merge_unit_by_warp(const MergeParams& p, int64_t unit, int lane) {
-  const int quarter = (int)(unit % kMergeQuarters);
-  const int64_t rh = unit / kMergeQuarters;
+// One (row, head) by one warp: lane l keeps dims 128 q + 4l .. + 3 of each quarter q, and the
+// weight of one of 32 pieces at a time. (A warp a quarter had four times the warps wait for the
+// same chain of reads: row table, lse, partials.)
+__device__ __forceinline__ void merge_row_by_warp(const MergeParams& p, int64_t rh, int lane) {
   const int r = (int)(rh / p.heads), h = (int)(rh - (int64_t)r * p.heads);
   const int np = __ldcg(p.row_np + r), base = __ldcg(p.row_base + r);
   const int64_t to = p.to_rows.of(r, h, p.heads);
@@ -176,36 +175,48 @@ __device__ __forceinline__ void merge_unit_by_warp(const MergeParams& p, int64_t
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const bool empty = np <= 0 || __any_sync(0xffffffffu, bad != 0) || !(m > -INFINITY);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc[kMergeQuarters];
+#pragma unroll
+  for (int q = 0; q < kMergeQuarters; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
   float total = 0.f;
   if (!empty) {
-    const float* src =
-        p.part_out + ((int64_t)base * p.heads + h) * kDLatent + 128 * quarter + 4 * lane;
+    const float* src = p.part_out + ((int64_t)base * p.heads + h) * kDLatent + 4 * lane;
     const int64_t step = (int64_t)p.heads * kDLatent;
     const float w_own = l_own > -INFINITY ? fast_exp2((l_own - m) * kLog2e) : 0.f;
     for (int k0 = 0; k0 < np; k0 += kWarpMergeLoads) {
-      float4 v[kWarpMergeLoads];
+      float4 v[kWarpMergeLoads][kMergeQuarters];
 #pragma unroll
       for (int k = 0; k < kWarpMergeLoads; ++k)
-        if (k0 + k < np) v[k] = __ldcg(reinterpret_cast<const float4*>(src + (k0 + k) * step));
+        if (k0 + k < np) {
+#pragma unroll
+          for (int q = 0; q < kMergeQuarters; ++q)
+            v[k][q] = __ldcg(reinterpret_cast<const float4*>(src + (k0 + k) * step + 128 * q));
+        }
 #pragma unroll
       for (int k = 0; k < kWarpMergeLoads; ++k) {
         if (k0 + k >= np) break;
         const float w = __shfl_sync(0xffffffffu, w_own, k0 + k);
         if (w == 0.f) continue;  // an empty piece: its slice may hold anything
-        acc.x += w * v[k].x; acc.y += w * v[k].y; acc.z += w * v[k].z; acc.w += w * v[k].w;
+#pragma unroll
+        for (int q = 0; q < kMergeQuarters; ++q) {
+          acc[q].x += w * v[k][q].x; acc[q].y += w * v[k][q].y;
+          acc[q].z += w * v[k][q].z; acc[q].w += w * v[k][q].w;
+        }
         total += w;
       }
     }
   }
   const float inv = empty ? 0.f : 1.0f / total;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  uint2 packed;
-  packed.x = *reinterpret_cast<const uint32_t*>(&lo);
-  packed.y = *reinterpret_cast<const uint32_t*>(&hi);
-  *reinterpret_cast<uint2*>(p.out + to * kDLatent + 128 * quarter + 4 * lane) = packed;
-  if (quarter == 0 && lane == 0) p.lse[to] = empty ? -INFINITY : m + logf(total);
+#pragma unroll
+  for (int q = 0; q < kMergeQuarters; ++q) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[q].x * inv, acc[q].y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[q].z * inv, acc[q].w * inv);
+    uint2 packed;
+    packed.x = *reinterpret_cast<const uint32_t*>(&lo);
+    packed.y = *reinterpret_cast<const uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(p.out + to * kDLatent + 128 * q + 4 * lane) = packed;
+  }
+  if (lane == 0) p.lse[to] = empty ? -INFINITY : m + logf(total);
 }
 
 // Unit `unit` by the whole block.
@@ -238,9 +249,8 @@ __global__ void __launch_bounds__(kMergeThreads) combine_rows_kernel(const Merge
   griddep_wait();
   griddep_launch_dependents();
   if (blockIdx.x >= p.many_blocks) {
-    const int64_t unit =
-        (int64_t)(blockIdx.x - p.many_blocks) * kMergeWarps + (threadIdx.x >> 5);
-    if (unit < p.units) merge_unit_by_warp(p, unit, threadIdx.x & 31);
+    const int64_t rh = (int64_t)(blockIdx.x - p.many_blocks) * kMergeWarps + (threadIdx.x >> 5);
+    if (rh < p.units / kMergeQuarters) merge_row_by_warp(p, rh, threadIdx.x & 31);
     return;
   }
   const unsigned per_row = (unsigned)p.heads * kMergeQuarters;
@@ -297,7 +307,8 @@ cudaError_t launch_combine_pieces(const DecodeWorkspace& ws, int rows, int heads
   p.to_rows = OutputRows{tiles, query_rows < tiles * heads ? query_rows : 0};
   p.stage_pieces = merge_stage_pieces(max_pieces_per_row, rows);
   const int64_t blocks =
-      few_rows ? p.units : p.many_blocks + (p.units + kMergeWarps - 1) / kMergeWarps;
+      few_rows ? p.units
+               : p.many_blocks + (p.units / kMergeQuarters + kMergeWarps - 1) / kMergeWarps;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cudaLaunchConfig_t cfg = {};
