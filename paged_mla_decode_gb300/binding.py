@@ -161,13 +161,14 @@ def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
 
-def _stream(stream) -> int:
-    """The stream's handle; the current stream of the current device by default.
+def _stream(stream, device: int | None = None) -> int:
+    """The stream's handle; the current stream of the current device (`device`, if it is known to
+    be) by default.
 
     (Read without a Stream object, which costs as much host time as a kernel launch.)
     """
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     return stream.cuda_stream
 
 
@@ -362,11 +363,11 @@ def mla_decode_tree(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.
         if num_nodes.numel() != batch:
             _refuse("num_nodes is [batch]")
     st = load_library().mla_decode_tree(
-        _ptr(q), _ptr(kv_pages), int(kv_pages.shape[0]), _page_size(kv_pages), dtype,
-        _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), _ptr(tree_mask),
-        _ptr(num_nodes), batch, nodes, heads, float(sm_scale), float(kv_scale), int(num_ctas),
-        _ptr(workspace), int(workspace.numel() * workspace.element_size()), _ptr(out), _ptr(lse),
-        _stream(stream))
+        q.data_ptr(), kv_pages.data_ptr(), kv_pages.shape[0], _page_size(kv_pages), dtype,
+        block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), tree_mask.data_ptr(),
+        _ptr(num_nodes), batch, nodes, heads, sm_scale, kv_scale, num_ctas, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), out.data_ptr(), lse.data_ptr(),
+        _stream(stream, device))
     _check(st, "mla_decode_tree")
 
 
@@ -653,7 +654,7 @@ def mla_logits_to_probs(logits: torch.Tensor, probs: torch.Tensor,
         logits.data_ptr(), in_stride, in_type, probs.data_ptr(), out_stride, out_type, batch, rows,
         vocab, _ptr(temperature), _ptr(num_rows), _ptr(node_tokens), _ptr(tree_mask),
         _ptr(token_counts), _ptr(prompt_mask), _ptr(repetition), _ptr(frequency), _ptr(presence),
-        _ptr(bias_tokens), _ptr(biases), num_biases, _ptr(allowed), _stream(stream))
+        _ptr(bias_tokens), _ptr(biases), num_biases, _ptr(allowed), _stream(stream, device))
     _check(st, "mla_logits_to_probs")
 
 
@@ -713,7 +714,7 @@ def mla_verify_tree(target_probs: torch.Tensor, draft_probs: torch.Tensor | None
         target_probs.data_ptr(), target_stride, _ptr(draft_probs), draft_stride, dtype,
         node_tokens.data_ptr(), tree_mask.data_ptr(), uniforms.data_ptr(), _ptr(num_nodes),
         _ptr(seq_lens), batch, nodes, vocab, out_tokens.data_ptr(), path.data_ptr(),
-        num_accepted.data_ptr(), _ptr(seq_lens_out), _ptr(token_counts), _stream(stream))
+        num_accepted.data_ptr(), _ptr(seq_lens_out), _ptr(token_counts), _stream(stream, device))
     _check(st, "mla_verify_tree")
 
 
@@ -725,20 +726,23 @@ def mla_kv_compact(kv_pages: torch.Tensor, block_table: torch.Tensor, seq_lens: 
     each layer contiguous. ``seq_lens`` are the lengths after verification, ``path [batch, N]`` and
     ``num_accepted [batch]`` as :func:`mla_verify_tree` writes them.
     """
-    # (the whole tensor's shape and type are looked at: taking a layer out of it costs more
-    # host time than the launch)
-    shape = kv_pages.shape
-    inner = 2 if shape[-1] == MLA_E2M1_PAGE_BYTES else 3
-    several = len(shape) == inner + 1
-    if not several or not kv_pages.is_contiguous() or shape[0] == 0:
-        if several and shape[0] == 0:
-            _refuse("kv_pages has no layer")
-        dtype = kv_dtype_code(kv_pages[0] if several else kv_pages)
-    elif inner == 2 and kv_pages.dtype is torch.uint8:
-        dtype = MLA_KV_E2M1
+    # (from the whole tensor's shape and type: taking a layer out of it costs more host time
+    # than the launch)
+    shape, kind = kv_pages.shape, kv_pages.dtype
+    width = shape[-1]
+    if width == 576 and (kind is torch.uint8 or kind is torch.bfloat16):
+        inner, dtype = 3, MLA_KV_E4M3 if kind is torch.uint8 else MLA_KV_BF16
+    elif width == MLA_E2M1_PAGE_BYTES and kind is torch.uint8:
+        inner, dtype = 2, MLA_KV_E2M1
     else:
-        dtype = kv_dtype_code(kv_pages.view(-1, *shape[-2:]))
-    layers = shape[0] if several else 1
+        _refuse("kv_pages are uint8 or bfloat16 [.., num_pages, 64, 576] or uint8 [.., num_pages, 19008]")
+    layers, layer_bytes = 1, 0
+    if len(shape) == inner + 1:
+        layers, layer_bytes = shape[0], kv_pages.stride(0) * kv_pages.element_size()
+        if layers == 0 or not (kv_pages.is_contiguous() or kv_pages[0].is_contiguous()):
+            _refuse("kv_pages has no layer, or layers that are not contiguous")
+    elif len(shape) != inner or not kv_pages.is_contiguous():
+        _refuse("kv_pages is not a contiguous cache, nor layers of one")
     device = _device_of(kv_pages)
     if block_table.dim() != 2:
         _refuse("block_table is [batch, max_pages]")
@@ -749,10 +753,9 @@ def mla_kv_compact(kv_pages: torch.Tensor, block_table: torch.Tensor, seq_lens: 
         _refuse("seq_lens and num_accepted are [batch]")
     _int32(device, block_table, seq_lens, path, num_accepted)
     st = load_library().mla_kv_compact(
-        kv_pages.data_ptr(), layers, kv_pages.stride(0) * kv_pages.element_size() if several else 0,
-        shape[-inner], 64 if inner == 2 else shape[-2], dtype, block_table.data_ptr(), max_pages,
-        seq_lens.data_ptr(), path.data_ptr(), num_accepted.data_ptr(), batch, int(path.shape[1]),
-        _stream(stream))
+        kv_pages.data_ptr(), layers, layer_bytes, shape[-inner], 64 if inner == 2 else shape[-2], dtype,
+        block_table.data_ptr(), max_pages, seq_lens.data_ptr(), path.data_ptr(),
+        num_accepted.data_ptr(), batch, path.shape[1], _stream(stream, device))
     _check(st, "mla_kv_compact")
 
 

@@ -72,6 +72,8 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(const CompactParam
   __shared__ int64_t s_from[kMaxMoves], s_to[kMaxMoves];  // slots
   __shared__ int s_count;
   const int b = blockIdx.x, tid = threadIdx.x;
+  griddep_wait();  // all earlier work in the stream is complete
+  griddep_launch_dependents();
   if (tid == 0) s_count = 0;
   const int a = p.accepted[b], L = p.seq_lens[b];
   if (a < 1 || a >= p.max_nodes || L < a + 1 || (int64_t)L > (int64_t)p.max_pages * kPageSize) return;
@@ -187,9 +189,14 @@ extern "C" mla_status mla_kv_compact(void* kv_pages, int num_layers, int64_t lay
   p.accepted = num_accepted;
   p.max_nodes = max_nodes;
   p.entry_bytes = entry;
-  const dim3 grid((unsigned)batch, (unsigned)((num_layers + p.layers_a_block - 1) / p.layers_a_block));
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (kv_dtype == MLA_KV_E2M1) kv_compact_kernel<true><<<grid, kThreads, 0, s>>>(p);
-  else kv_compact_kernel<false><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)batch, (unsigned)((num_layers + p.layers_a_block - 1) / p.layers_a_block));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, kv_dtype == MLA_KV_E2M1 ? kv_compact_kernel<true> : kv_compact_kernel<false>, p);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

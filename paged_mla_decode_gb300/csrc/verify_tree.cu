@@ -121,6 +121,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_tree_kernel(const TreePara
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / ranks, N = p.max_nodes, V = p.vocab;
+  griddep_wait();  // all earlier work in the stream is complete
+  griddep_launch_dependents();
   const int n = p.num_nodes ? p.num_nodes[b] : N;
   const int L = p.seq_lens ? p.seq_lens[b] : n;
   const T* target = static_cast<const T*>(p.target) + (int64_t)b * N * p.target_stride;
@@ -327,7 +329,8 @@ cudaError_t launch_verify_tree(const TreeParams& p, cudaStream_t stream) {
   constexpr int kTile = 32 * Wide<T, kVec>::kWide;
   const int64_t share = (int64_t)ranks * kWarps * kTile;
   const int run = (int)((p.vocab + share - 1) / share) * kTile;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1] = pdl_attribute();
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ranks;
   attr[0].val.clusterDim.y = 1;
@@ -337,7 +340,7 @@ cudaError_t launch_verify_tree(const TreeParams& p, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, verify_tree_kernel<T, kVec>, p, run);
 }
 
