@@ -11,13 +11,19 @@
 //   p = exp((x - max x) / temperature) / sum
 // A drafted token's row also counts the drafts on its own path (the node mask's bits).
 //
-// A row is read once and written once, so DRAM bounds many rows. A cluster of up to eight
-// blocks works a row in two passes over its logits: the first keeps a running maximum and
-// sum in every thread, which the blocks exchange through distributed shared memory; the second, which
-// finds the logits in L2, writes exp(x - max) / sum. Nothing is staged, so many blocks share an SM
-// and one's loads cover another's barriers. Tokens that a list names (biases, drafts) are left
-// out of the first pass, by a bit each, and worked out by a thread an entry, which adds up all of
-// its token's entries in order: two entries of a token come to the same value.
+// A row is read and written, and the SMs together get some 5.8 TB/s from L2, whether the bytes
+// come from DRAM or were there: bytes bound many rows. A cluster of up to eight blocks works a
+// row in two passes over its logits: the first sums exponentials in every thread, relative to a
+// reference that moves only when a logit lies far above it, and the blocks exchange references and
+// sums through distributed shared memory; the second writes exp(x - reference) / sum. (A row kept on
+// chip in between reads half, but leaves too few blocks an SM to cover the exchange.) The
+// counts are read once for several rows of a request: a block keeps a byte a token, which picks
+// the token's two factors and its difference from a table. A row whose sum is not a positive
+// finite number (infinities, NaNs, nothing allowed) is done again one token at a time, with a
+// running maximum and every case looked at.
+//
+// Tokens that a list names (biases, drafts) are left out of the passes, by a bit each, and
+// worked out by a thread an entry, which adds up all of its token's entries in order.
 #include <algorithm>
 #include <atomic>
 
@@ -32,15 +38,15 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kMaxCluster = 8;
-// Two shapes of block. With few rows a block has an SM to itself and most of its loads should
-// be in flight at once; with many, several smaller blocks an SM cover each other's waits.
+// Shapes of block. With few rows a block has an SM to itself and all of its loads should be in
+// flight at once; with many, several smaller blocks an SM cover each other's waits.
 struct Few {
   static constexpr int kThreads = 1024, kBlocksPerSm = 1, kUnroll = 2;
 };
 struct Many {
-  static constexpr int kThreads = 256, kBlocksPerSm = 5, kUnroll = 1;
+  static constexpr int kThreads = 256, kBlocksPerSm = 4, kUnroll = 1;
 };
-
+constexpr int kMaxGroup = 8;  // rows of a block, one after the other
 
 struct ProbsParams {
   const void* logits;
@@ -61,15 +67,15 @@ struct ProbsParams {
   const uint32_t* allowed;
   int words;  // of a row of `prompt` and `allowed`
   int run;    // tokens of a block
+  int group;  // rows of a block
   int penalties;
 };
 
-// What changes a row's logits, the same for all of its tokens.
+// What changes a request's logits, the same for all of its tokens.
 struct RowSettings {
   float repetition, inverse, frequency, presence;
   const int32_t* counts;     // of the request; may be null
   const uint32_t* prompt;    // may be null
-  const uint32_t* allowed;   // of the row; may be null
 };
 
 // (x / repetition is x times its rounded inverse: one more rounding of 2^-24, no division
@@ -128,55 +134,74 @@ __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// Running maximum and sum of exp((x - max) / t); greedy: the lowest token with the maximum.
+// A reference and the sum of exp((x - ref) / t): ref the maximum, or in the fast pass
+// something within 2^kSlack of it. Greedy: the maximum, and the lowest token with it.
 struct Stats {
-  float max, sum;
+  float ref, sum;
   int first;
 };
+constexpr float kSlack = 60.f;       // (a sum of 2^19 terms up to 2^60 is far from overflow)
+constexpr float kNoRef = -3.0e38f;   // before any token (weights relative to it are 0)
 
-// exp((x - m) / t) for x <= m < inf, m > -inf, with k = 2 log2(e) / t (of half the
-// difference, which does not overflow)
-__device__ __forceinline__ float weight_of(float x, float m, float k) {
-  return fast_exp2(fmaf(0.5f, x, -0.5f * m) * k);
-}
-// the same for any m: beside an infinite maximum only its equals have a weight
+// exp((x - m) / t) for any x and m, with k = 2 log2(e) / t (of half the difference, which does
+// not overflow); beside an infinite maximum only its equals have a weight
 __device__ __forceinline__ float weight_of_any(float x, float m, float k) {
   if (x == m) return m > -INFINITY ? 1.f : 0.f;
-  return m == INFINITY || x == -INFINITY ? 0.f : weight_of(x, m, k);
+  return m == INFINITY || x == -INFINITY ? 0.f : fast_exp2(fmaf(0.5f, x, -0.5f * m) * k);
 }
-
+// One token, every case looked at (x is no NaN).
+__device__ __forceinline__ void add_careful(Stats& s, float x, int token, bool greedy, float k) {
+  if (x > s.ref) {
+    s.sum *= weight_of_any(s.ref, x, k);
+    s.ref = x;
+    s.first = token;
+  } else if (x == s.ref && x > -INFINITY) {
+    s.first = min(s.first, token);
+  }
+  if (!greedy) s.sum += weight_of_any(x, s.ref, k);
+}
+// Tokens of finite logits (or -inf), k1 = log2(e) / t, slack = kSlack / k1.
 template <int kCount>
-__device__ __forceinline__ void add_tokens(Stats& s, const float (&x)[kCount], int token, bool greedy, float k) {
+__device__ __forceinline__ void add_fast(Stats& s, const float (&x)[kCount], float k1, float slack) {
   float top = x[0];
 #pragma unroll
   for (int e = 1; e < kCount; ++e) top = fmaxf(top, x[e]);
-  if (top > s.max) {
-    s.sum = s.max > -INFINITY ? s.sum * weight_of_any(s.max, top, k) : 0.f;
-    s.max = top;
-    if (greedy) {
+  if (top > s.ref + slack) {
+    s.sum *= fast_exp2((s.ref - top) * k1);
+    s.ref = top;
+  }
+  if constexpr (kCount == 1) {
+    s.sum += fast_exp2((x[0] - s.ref) * k1);
+  } else {
+    const float2 r2 = make_float2(-s.ref, -s.ref), k2 = make_float2(k1, k1);
+    float2 part = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = kCount - 1; e >= 0; --e)
-        if (x[e] == top) s.first = token + e;
+    for (int e = 0; e < kCount; e += 2) {
+      const float2 d = mul2(add2(make_float2(x[e], x[e + 1]), r2), k2);
+      part = add2(part, make_float2(fast_exp2(d.x), fast_exp2(d.y)));
     }
+    s.sum += part.x + part.y;
   }
-  if (greedy || s.max == -INFINITY) return;
-  if (s.max == INFINITY) {
+}
+template <int kCount>
+__device__ __forceinline__ void add_greedy(Stats& s, const float (&x)[kCount], int token) {
+  float top = x[0];
 #pragma unroll
-    for (int e = 0; e < kCount; ++e) s.sum += x[e] == INFINITY ? 1.f : 0.f;
-    return;
+  for (int e = 1; e < kCount; ++e) top = fmaxf(top, x[e]);
+  if (top > s.ref) {
+    s.ref = top;
+#pragma unroll
+    for (int e = kCount - 1; e >= 0; --e)
+      if (x[e] == top) s.first = token + e;
   }
-  float part = 0.f;
-#pragma unroll
-  for (int e = 0; e < kCount; ++e) part += weight_of(x[e], s.max, k);
-  s.sum += part;
 }
 // All lanes' together, the same in every lane.
-__device__ __forceinline__ Stats join(Stats s, float k) {
+__device__ __forceinline__ Stats join(const Stats& s, float k) {
   Stats r = s;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) r.max = fmaxf(r.max, __shfl_xor_sync(0xffffffffu, r.max, o));
-  r.sum = s.sum * weight_of_any(s.max, r.max, k);
-  r.first = s.max == r.max ? s.first : 0x7fffffff;
+  for (int o = 16; o > 0; o >>= 1) r.ref = fmaxf(r.ref, __shfl_xor_sync(0xffffffffu, r.ref, o));
+  r.sum = s.sum * weight_of_any(s.ref, r.ref, k);
+  r.first = s.ref == r.ref ? s.first : 0x7fffffff;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     r.sum += __shfl_xor_sync(0xffffffffu, r.sum, o);
@@ -185,237 +210,342 @@ __device__ __forceinline__ Stats join(Stats s, float k) {
   return r;
 }
 
-// Eight tokens' settings as loaded: the counts and a byte each of prompt and grammar.
-struct EightSettings {
-  int4 a, b;
-  uint32_t prompt, allowed;
-  __device__ __forceinline__ void load(const RowSettings& st, int i) {
-    a = b = make_int4(0, 0, 0, 0);
-    if (st.counts) {
-      a = __ldg(reinterpret_cast<const int4*>(st.counts + i));
-      b = __ldg(reinterpret_cast<const int4*>(st.counts + i) + 1);
-    }
-    prompt = st.prompt ? __ldg(st.prompt + (i >> 5)) >> (i & 31) : 0u;
-    allowed = st.allowed ? __ldg(st.allowed + (i >> 5)) >> (i & 31) : 0xffu;
+__device__ __forceinline__ uint32_t byte_of(const uint32_t* words, int i) {  // i: a multiple of 8
+  return (__ldg(words + (i >> 5)) >> (i & 31)) & 0xffu;
+}
+// A token's byte: 0 not seen, 1 in the prompt only, count + 1 up to 254, 255 beyond. By byte, a
+// table holds what it makes of a logit: x (x > 0 ? up : down) - off, as (up, down, off).
+constexpr uint32_t kCodeBeyond = 255;
+__device__ __forceinline__ uint2 codes_of(const int32_t* counts, const uint32_t* prompt, int i) {
+  uint32_t seen = prompt ? byte_of(prompt, i) : 0u, w[2] = {0, 0};
+  int4 a = make_int4(0, 0, 0, 0), b = a;
+  if (counts) {
+    a = __ldg(reinterpret_cast<const int4*>(counts + i));
+    b = __ldg(reinterpret_cast<const int4*>(counts + i) + 1);
   }
-  __device__ __forceinline__ void apply(float (&x)[8], const RowSettings& st, bool penalties) const {
-    if (penalties) {
-      const int c[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = penalised(x[e], c[e], (prompt >> e) & 1u, st);
-    }
+  if (seen != 0 || (a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w) != 0) {
+    const int n[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      x[e] = fmaxf(x[e], -INFINITY);  // (NaN: -inf)
-      if (!((allowed >> e) & 1u)) x[e] = -INFINITY;
+      const uint32_t code = n[e] > 0 ? min((uint32_t)n[e] + 1u, kCodeBeyond) : (seen >> e) & 1u;
+      w[e >> 2] |= code << (8 * (e & 3));
     }
   }
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void apply_codes(float (&x)[8], const uint2& codes, const float4* table,
+                                            const int32_t* counts, int i, const RowSettings& st) {
+  if ((codes.x | codes.y) == 0) return;
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const uint32_t w = e < 4 ? codes.x : codes.y;
+    const float4 a = table[(w >> (8 * (e & 3))) & 0xffu], b = table[(w >> (8 * (e & 3) + 8)) & 0xffu];
+    const float2 f = make_float2(x[e] > 0.f ? a.x : a.y, x[e + 1] > 0.f ? b.x : b.y);
+    const float2 v = add2(mul2(make_float2(x[e], x[e + 1]), f), make_float2(-a.z, -b.z));
+    x[e] = v.x;
+    x[e + 1] = v.y;
+  }
+  // (the table takes a count beyond it as 0: the rest of its difference)
+  if (((~codes.x - 0x01010101u) & codes.x & 0x80808080u) | ((~codes.y - 0x01010101u) & codes.y & 0x80808080u)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t code = ((e < 4 ? codes.x : codes.y) >> (8 * (e & 3))) & 0xffu;
+      if (code == kCodeBeyond) x[e] -= fmaf(st.frequency, (float)counts[i + e], st.presence);
+    }
+  }
+}
+// Tokens whose bit is not set: -inf.
+__device__ __forceinline__ void hide(float (&x)[8], uint32_t bits) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (!((bits >> e) & 1u)) x[e] = -INFINITY;
+}
+
+// A token that a bias or a draft names.
+struct Special {
+  uint64_t nodes;  // the drafts that are this token
+  int token;       // -1: another run's, or an earlier entry's
+  int count;       // without the drafts on a row's path
+  float bias;
+  int in_prompt;
 };
 
-// kVec: rows of logits, probabilities and counts allow 16-byte accesses.
-template <class In, class Out, bool kVec, class Shape>
+// kVec: rows of logits, probabilities and counts allow 16-byte accesses. (Without, every row goes
+// the careful way.) kPen: there are penalties.
+template <class In, class Out, bool kVec, bool kPen, class Shape>
 __global__ void __launch_bounds__(Shape::kThreads, Shape::kBlocksPerSm)
     logits_probs_kernel(const ProbsParams p) {
   constexpr int kThreads = Shape::kThreads, kWarps = kThreads / 32, kUnroll = Shape::kUnroll;
-  extern __shared__ uint32_t s_lists[];
-  __shared__ Stats s_stats;  // read by the cluster
+  extern __shared__ __align__(16) uint8_t s_all[];
+  __shared__ Stats s_stats[2];  // by exchange; read by the cluster
   __shared__ Stats s_warp[kWarps];
+  __shared__ float4 s_table[kPen ? 256 : 1];
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = blockIdx.x / ranks;
-  const int b = (int)(row / p.rows), j = (int)(row - (int64_t)b * p.rows), V = p.vocab;
-  if (p.num_rows && j >= p.num_rows[b]) return;  // (every block of the cluster)
-  const In* logits = static_cast<const In*>(p.logits) + row * p.logit_stride;
-  Out* probs = static_cast<Out*>(p.probs) + row * p.prob_stride;
+  const int groups = (p.rows + p.group - 1) / p.group;  // of a request
+  const int unit = blockIdx.x / ranks;
+  const int b = unit / groups, j0 = (unit - b * groups) * p.group, V = p.vocab;
+  griddep_wait();  // all earlier work in the stream is complete
+  griddep_launch_dependents();
+  const int j1 = min(j0 + p.group, p.num_rows ? min(p.num_rows[b], p.rows) : p.rows);
+  if (j0 >= j1) return;  // (every block of the cluster)
   RowSettings st;
-  st.repetition = p.repetition ? p.repetition[b] : 1.f;
+  st.repetition = kPen && p.repetition ? p.repetition[b] : 1.f;
   st.inverse = 1.f / st.repetition;
-  st.frequency = p.frequency ? p.frequency[b] : 0.f;
-  st.presence = p.presence ? p.presence[b] : 0.f;
-  st.counts = p.counts ? p.counts + (int64_t)b * V : nullptr;
-  st.prompt = p.prompt ? p.prompt + (int64_t)b * p.words : nullptr;
-  st.allowed = p.allowed ? p.allowed + row * p.words : nullptr;
+  st.frequency = kPen && p.frequency ? p.frequency[b] : 0.f;
+  st.presence = kPen && p.presence ? p.presence[b] : 0.f;
+  st.counts = kPen && p.counts ? p.counts + (int64_t)b * V : nullptr;
+  st.prompt = kPen && p.prompt ? p.prompt + (int64_t)b * p.words : nullptr;
   const float temperature = p.temperature ? p.temperature[b] : 1.f;
-  const bool greedy = !(temperature > 0.f), penalties = p.penalties != 0;
+  const bool greedy = !(temperature > 0.f);
   // (within the positive floats: 0 or infinity times a difference could be NaN)
   const float k = fminf(fmaxf(2.f * kLog2e / temperature, 0x1p-149f), 0x1.fffffep127f);
+  const float k1 = 0.5f * k, slack = kSlack / k1;
   const int lo = (int)min((int64_t)rank * p.run, (int64_t)V);
   const int hi = (int)min((int64_t)lo + p.run, (int64_t)V);
   const int all8 = kVec ? lo + ((hi - lo) & ~7) : lo;  // tokens from here on go one by one
-  Stats mine{-INFINITY, 0.f, 0x7fffffff};
+  const int64_t row0 = (int64_t)b * p.rows;
+  // the run's bytes, written and read by the thread that has the tokens; then the lists
+  uint2* s_codes = reinterpret_cast<uint2*>(s_all);
+  uint8_t* s_lists = s_all + (kVec && kPen ? p.run : 0);
+  if constexpr (kPen && kVec) {
+    for (int c = tid; c < 256; c += kThreads) {
+      const bool counted = c > 1 && c < (int)kCodeBeyond;
+      s_table[c] = c == 0 ? make_float4(1.f, 1.f, 0.f, 0.f)
+                          : make_float4(st.inverse, st.repetition,
+                                        counted ? fmaf(st.frequency, (float)(c - 1), st.presence) : 0.f, 0.f);
+    }
+    __syncthreads();
+  }
 
-  // ---- the lists: biases, and the drafts on this row's path ----
-  const uint64_t on_path =
-      p.tree_mask && penalties ? p.tree_mask[row] & ~1ull & (~0ull >> (64 - p.rows)) : 0;
-  const int paths = __popcll(on_path), entries = p.num_biases + paths;
-  int32_t* s_token = reinterpret_cast<int32_t*>(s_lists);       // [entries]
-  float* s_bias = reinterpret_cast<float*>(s_token + p.num_biases + 64);  // [num_biases]
-  float* s_x = s_bias + p.num_biases;                            // [entries]
-  uint32_t* s_listed = reinterpret_cast<uint32_t*>(s_x + p.num_biases + 64);  // [run / 32]
-  if (entries > 0) {
+  // ---- the lists: biases and drafts ----
+  const int nodes = kPen && p.tree_mask ? p.rows : 0;  // (<= 64)
+  const int specials = p.num_biases + nodes;
+  Special* s_special = reinterpret_cast<Special*>(s_lists);                        // [specials]
+  float* s_special_x = reinterpret_cast<float*>(s_special + p.num_biases + 64);    // [specials], of the row
+  uint32_t* s_listed = reinterpret_cast<uint32_t*>(s_special_x + p.num_biases + 64);  // [run / 32]
+  int32_t* s_bias_token = reinterpret_cast<int32_t*>(s_listed + p.run / 32);       // [specials]
+  float* s_bias = reinterpret_cast<float*>(s_bias_token + p.num_biases + 64);      // [num_biases]
+  if (specials > 0) {
     for (int i = tid; i < p.num_biases; i += kThreads) {
-      s_token[i] = p.bias_tokens[(int64_t)b * p.num_biases + i];
+      s_bias_token[i] = p.bias_tokens[(int64_t)b * p.num_biases + i];
       s_bias[i] = p.biases[(int64_t)b * p.num_biases + i];
     }
-    if (tid < 64 && ((on_path >> tid) & 1u))
-      s_token[p.num_biases + __popcll(on_path & ((1ull << tid) - 1))] =
-          p.node_tokens[(int64_t)b * p.rows + tid];
+    if (tid < nodes)  // (node 0's token is among the counted)
+      s_bias_token[p.num_biases + tid] = tid > 0 ? p.node_tokens[row0 + tid] : -1;
     for (int i = tid; i < p.run / 32; i += kThreads) s_listed[i] = 0u;
     __syncthreads();
-    for (int e = tid; e < entries; e += kThreads) {
-      const int v = s_token[e];
-      if (v < lo || v >= hi) continue;
-      int count = st.counts ? max(st.counts[v], 0) : 0;
-      float x = as_float(logits[v]);
-      for (int i = 0; i < paths; ++i) count += s_token[p.num_biases + i] == v;
-      if (penalties) x = penalised(x, count, st.prompt && bit_of(st.prompt, v), st);
-      for (int i = 0; i < p.num_biases; ++i)
-        if (s_token[i] == v) x += s_bias[i];
-      x = fmaxf(x, -INFINITY);
-      if (st.allowed && !bit_of(st.allowed, v)) x = -INFINITY;
-      s_x[e] = x;
-      const uint32_t bit = 1u << ((v - lo) & 31);
-      if (atomicOr(&s_listed[(v - lo) >> 5], bit) & bit) continue;  // its token is in the sum
-      const float one[1] = {x};
-      // (greedy: a thread's entries come in no order of tokens)
-      if (greedy && x == mine.max && x > -INFINITY) mine.first = min(mine.first, v);
-      else add_tokens(mine, one, v, greedy, k);
+    for (int e = tid; e < specials; e += kThreads) {
+      const int v = s_bias_token[e];
+      Special t{0, -1, 0, 0.f, 0};
+      if (v >= lo && v < hi) {
+        int entry = specials;  // the first one of this token
+        for (int i = specials - 1; i >= p.num_biases; --i)
+          if (s_bias_token[i] == v) t.nodes |= 1ull << (i - p.num_biases), entry = i;
+        for (int i = p.num_biases - 1; i >= 0; --i)
+          if (s_bias_token[i] == v) entry = i;
+        if (entry == e) {
+          t.token = v;
+          t.count = st.counts ? max(st.counts[v], 0) : 0;
+          t.in_prompt = st.prompt ? bit_of(st.prompt, v) : 0;
+          for (int i = e; i < p.num_biases; ++i)
+            if (s_bias_token[i] == v) t.bias += s_bias[i];
+          atomicOr(&s_listed[(v - lo) >> 5], 1u << ((v - lo) & 31));
+        }
+      }
+      s_special[e] = t;
     }
     __syncthreads();
   }
+  auto listed8 = [&](int i) -> uint32_t { return s_listed[(i - lo) >> 5] >> ((i - lo) & 31); };
 
-  // ---- first pass: the row's maximum and sum ----
-  Stats dense{-INFINITY, 0.f, 0x7fffffff};
-  if constexpr (kVec) {
-    for (int i0 = lo + 8 * tid; i0 < all8; i0 += kUnroll * 8 * kThreads) {
-      Eight<In> in[kUnroll];
-      EightSettings set[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + u * 8 * kThreads;
-        if (i < all8) {
-          in[u].load(logits + i);
-          set[u].load(st, i);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + u * 8 * kThreads;
-        if (i < all8) {
-          float x[8];
-          in[u].get(x);
-          if (entries > 0) set[u].allowed &= ~(s_listed[(i - lo) >> 5] >> ((i - lo) & 31));
-          set[u].apply(x, st, penalties);
-          add_tokens(dense, x, i, greedy, k);
-        }
+  int exchanges = 0;
+  for (int j = j0; j < j1; ++j) {
+    const In* logits = static_cast<const In*>(p.logits) + (row0 + j) * p.logit_stride;
+    Out* probs = static_cast<Out*>(p.probs) + (row0 + j) * p.prob_stride;
+    const uint32_t* allowed = p.allowed ? p.allowed + (row0 + j) * p.words : nullptr;
+    auto final_of = [&](float x, int v) -> float {  // (NaN: -inf)
+      return allowed && !bit_of(allowed, v) ? -INFINITY : fmaxf(x, -INFINITY);
+    };
+    if (specials > 0) {  // their logits with everything, each read back by the thread that wrote it
+      const uint64_t on_path = nodes > 0 ? p.tree_mask[row0 + j] : 0;
+      for (int e = tid; e < specials; e += kThreads) {
+        const Special t = s_special[e];
+        if (t.token < 0) continue;
+        float x = as_float(logits[t.token]);
+        if (kPen) x = penalised(x, t.count + __popcll(t.nodes & on_path), t.in_prompt, st);
+        s_special_x[e] = final_of(x + t.bias, t.token);
       }
     }
-  }
-  auto one_token = [&](int i) -> float {
-    float x = as_float(logits[i]);
-    if (penalties)
-      x = penalised(x, st.counts ? st.counts[i] : 0, st.prompt && bit_of(st.prompt, i), st);
-    x = fmaxf(x, -INFINITY);
-    return st.allowed && !bit_of(st.allowed, i) ? -INFINITY : x;
-  };
-  for (int i = all8 + tid; i < hi; i += kThreads) {
-    if (entries > 0 && ((s_listed[(i - lo) >> 5] >> ((i - lo) & 31)) & 1u)) continue;
-    const float one[1] = {one_token(i)};
-    add_tokens(dense, one, i, greedy, k);
-  }
-  // the entries' and the others'
-  {
-    const float top = fmaxf(mine.max, dense.max);
-    mine.first = min(mine.max == top ? mine.first : 0x7fffffff, dense.max == top ? dense.first : 0x7fffffff);
-    mine.sum = mine.sum * weight_of_any(mine.max, top, k) + dense.sum * weight_of_any(dense.max, top, k);
-    mine.max = top;
-  }
-  mine = join(mine, k);
-  if (lane == 0) s_warp[warp] = mine;
-  __syncthreads();
-  if (warp == 0) {
-    mine = lane < kWarps ? s_warp[lane] : Stats{-INFINITY, 0.f, 0x7fffffff};
-    mine = join(mine, k);
-    if (lane == 0) s_stats = mine;
-  }
-  cluster.sync();
-
-  // ---- all blocks': lane r looks at block r's ----
-  Stats all{-INFINITY, 0.f, 0x7fffffff};
-  if (lane < ranks) all = *cluster.map_shared_rank(&s_stats, lane);
-  cluster.barrier_arrive();  // (nobody leaves before the others have read its numbers)
-  all = join(all, k);
-  // ---- second pass: exp((x - max) / t) / sum ----
-  // (a row with nothing allowed has no maximum above -inf: all of it is 0)
-  const bool none = !(all.max > -INFINITY), infinite = all.max == INFINITY;
-  const float factor = none ? 0.f : 1.f / all.sum;
-  auto value = [&](float x, int i) -> float {
-    if (greedy) return i == all.first && !none ? 1.f : 0.f;
-    if (none) return 0.f;
-    return (infinite ? (x == INFINITY ? 1.f : 0.f) : weight_of(x, all.max, k)) * factor;
-  };
-  if constexpr (kVec) {
-    for (int i0 = lo + 8 * tid; i0 < all8; i0 += kUnroll * 8 * kThreads) {
-      Eight<In> in[kUnroll];
-      EightSettings set[kUnroll];
+    auto each_listed = [&](auto use) {
+      for (int e = tid; e < specials; e += kThreads)
+        if (s_special[e].token >= 0) use(s_special_x[e], s_special[e].token);
+    };
+    auto one_token = [&](int i) -> float {
+      float x = as_float(logits[i]);
+      if (kPen)
+        x = penalised(x, st.counts ? st.counts[i] : 0, st.prompt && bit_of(st.prompt, i), st);
+      return final_of(x, i);
+    };
+    // a thread's tokens by eights, to `use(x, i)`; `apart`: without the listed; `fresh`: the
+    // first time for this request, when their bytes are made
+    auto each8 = [&](bool apart, bool fresh, auto use) {
+      if constexpr (kVec) {
+        for (int i0 = lo + 8 * tid; i0 < all8; i0 += kUnroll * 8 * kThreads) {
+          Eight<In> in[kUnroll];
+          uint32_t bits[kUnroll];
+          [[maybe_unused]] uint2 codes[kUnroll];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + u * 8 * kThreads;
-        if (i < all8) {
-          in[u].load(logits + i);
-          set[u].load(st, i);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + u * 8 * kThreads;
-        if (i < all8) {
-          float x[8];
-          in[u].get(x);
-          set[u].apply(x, st, penalties);
-          if (greedy || none || infinite) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = value(x[e], i + e);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = weight_of(x[e], all.max, k) * factor;
+          for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + u * 8 * kThreads;
+            if (u == 0 || i < all8) {
+              in[u].load(logits + i);
+              bits[u] = allowed ? byte_of(allowed, i) : 0xffu;
+            }
           }
-          Eight<Out>::store(probs + i, x);
+          if constexpr (kPen) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+              const int i = i0 + u * 8 * kThreads;
+              if (u == 0 || i < all8)
+                codes[u] = fresh ? codes_of(st.counts, st.prompt, i) : s_codes[(i - lo) >> 3];
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + u * 8 * kThreads;
+            if (u == 0 || i < all8) {
+              float x[8];
+              in[u].get(x);
+              if constexpr (kPen) {
+                if (fresh) s_codes[(i - lo) >> 3] = codes[u];
+                apply_codes(x, codes[u], s_table, st.counts, i, st);
+              }
+              if (allowed || apart) hide(x, apart ? bits[u] & ~listed8(i) : bits[u]);
+              use(x, i);
+            }
+          }
         }
       }
+    };
+
+  Stats mine, all;
+    // the blocks' numbers together: lane r looks at block r's
+    auto exchange = [&]() {
+      mine = join(mine, k);
+      __syncthreads();  // (the last exchange's have been read)
+      if (lane == 0) s_warp[warp] = mine;
+      __syncthreads();
+      if (warp == 0) {
+        Stats r = lane < kWarps ? s_warp[lane] : Stats{-INFINITY, 0.f, 0x7fffffff};
+        r = join(r, k);
+        if (lane == 0) s_stats[exchanges & 1] = r;
+      }
+      // (the numbers of two exchanges ago were read before the last such barrier)
+      cluster.sync();
+      all = Stats{-INFINITY, 0.f, 0x7fffffff};
+      if (lane < ranks) all = *cluster.map_shared_rank(&s_stats[exchanges & 1], lane);
+      all = join(all, k);
+      ++exchanges;
+    };
+
+    // ---- first pass ----
+    bool careful = !kVec || greedy || k1 < 0x1p-60f;
+    const bool fresh = j == j0;
+    if (!careful) {
+      mine = Stats{kNoRef, 0.f, 0};
+      each8(specials > 0, fresh, [&](const float(&x)[8], int) { add_fast(mine, x, k1, slack); });
+      auto add = [&](float x, int) {
+        const float one[1] = {x};
+        add_fast(mine, one, k1, slack);
+      };
+      for (int i = all8 + tid; i < hi; i += kThreads)
+        if (specials == 0 || !(listed8(i) & 1u)) add(one_token(i), i);
+      if (specials > 0) each_listed(add);
+      exchange();
+      careful = !(all.sum > 0.f && all.sum < INFINITY);
+    }
+    if (careful) {
+      mine = Stats{-INFINITY, 0.f, 0x7fffffff};
+      if (greedy) each8(specials > 0, fresh, [&](const float(&x)[8], int i) { add_greedy(mine, x, i); });
+      for (int i = (greedy ? all8 : lo) + tid; i < hi; i += kThreads)
+        if (specials == 0 || !(listed8(i) & 1u)) add_careful(mine, one_token(i), i, greedy, k);
+      if (specials > 0) each_listed([&](float x, int v) { add_careful(mine, x, v, greedy, k); });
+      exchange();
+    }
+
+    // ---- second pass: exp((x - ref) / t) / sum ----
+    // (a row with nothing allowed has no reference above -inf: all of it is 0)
+    const bool none = !(all.ref > -INFINITY);
+    const float factor = none ? 0.f : 1.f / all.sum;
+    auto value = [&](float x, int i) -> float {
+      if (greedy) return i == all.first && !none ? 1.f : 0.f;
+      if (!careful) return fast_exp2((x - all.ref) * k1) * factor;
+      return none ? 0.f : weight_of_any(x, all.ref, k) * factor;
+    };
+    if (!careful) {
+      const float2 k2 = make_float2(k1, k1), r2 = make_float2(-all.ref, -all.ref), f2 = make_float2(factor, factor);
+      each8(false, false, [&](float(&x)[8], int i) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float2 d = mul2(add2(make_float2(x[e], x[e + 1]), r2), k2);
+          const float2 w = mul2(make_float2(fast_exp2(d.x), fast_exp2(d.y)), f2);
+          x[e] = w.x;
+          x[e + 1] = w.y;
+        }
+        Eight<Out>::store(probs + i, x);
+      });
+    } else if (kVec && greedy) {
+      for (int i = lo + 8 * tid; i < all8; i += 8 * kThreads) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = value(0.f, i + e);
+        Eight<Out>::store(probs + i, x);
+      }
+    }
+    for (int i = (!careful || greedy ? all8 : lo) + tid; i < hi; i += kThreads)
+      put(probs + i, value(greedy ? 0.f : one_token(i), i));
+    if (specials > 0 && !greedy) {
+      __syncthreads();  // (what was written for the listed tokens is written again)
+      each_listed([&](float x, int v) { put(probs + v, value(x, v)); });
     }
   }
-  for (int i = all8 + tid; i < hi; i += kThreads) put(probs + i, value(one_token(i), i));
-  if (entries > 0) {
-    __syncthreads();  // (what was written for the listed tokens is written again)
-    for (int e = tid; e < entries; e += kThreads) {
-      const int v = s_token[e];
-      if (v < lo || v >= hi) continue;
-      put(probs + v, value(s_x[e], v));
-    }
-  }
-  cluster.barrier_wait();
+  cluster.sync();  // nobody leaves before the others have read its numbers
 }
 
-template <class In, class Out, bool kVec, class Shape>
+template <class In, class Out, bool kVec, bool kPen, class Shape>
 cudaError_t launch_probs(const ProbsParams& p, int ranks, cudaStream_t stream) {
-  const size_t bytes = p.num_biases > 0 || p.tree_mask
-                           ? 4 * (size_t)(3 * p.num_biases + 2 * 64) + (size_t)p.run / 8
-                           : 0;
-  cudaLaunchAttribute attr[1];
+  const size_t entries = (size_t)p.num_biases + 64;
+  const size_t bytes = (kVec && kPen ? p.run : 0) +
+                       (p.num_biases > 0 || (kPen && p.tree_mask)
+                            ? (sizeof(Special) + 12) * entries + (size_t)p.run / 8
+                            : 0);
+  if (bytes > 40 * 1024) {
+    static std::atomic<int> configured[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !configured[dev].load()) {
+      const cudaError_t e = cudaFuncSetAttribute(logits_probs_kernel<In, Out, kVec, kPen, Shape>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) configured[dev].store(1);
+    }
+  }
+  cudaLaunchAttribute attr[2];
+  attr[1] = pdl_attribute();
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ranks;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.batch * p.rows * ranks));
+  cfg.gridDim = dim3((unsigned)((int64_t)p.batch * ((p.rows + p.group - 1) / p.group) * ranks));
   cfg.blockDim = dim3(Shape::kThreads);
-  cfg.dynamicSmemBytes = bytes;  // at most 18 KB
+  cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logits_probs_kernel<In, Out, kVec, Shape>, p);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, logits_probs_kernel<In, Out, kVec, kPen, Shape>, p);
 }
 
 template <class In, class Out>
@@ -424,16 +554,21 @@ cudaError_t launch_probs(ProbsParams p, cudaStream_t stream) {
   int ranks = 1;
   while (ranks < kMaxCluster && p.vocab >= 2 * ranks * 2048) ranks *= 2;
   p.run = ((p.vocab + ranks - 1) / ranks + 31) / 32 * 32;
-  const bool few = (int64_t)p.batch * p.rows * ranks <= device_sm_count();
   const uintptr_t at = reinterpret_cast<uintptr_t>(p.logits) | reinterpret_cast<uintptr_t>(p.probs) |
                        (uintptr_t)(p.logit_stride * (int64_t)sizeof(In)) |
                        (uintptr_t)(p.prob_stride * (int64_t)sizeof(Out)) |
                        (p.counts ? reinterpret_cast<uintptr_t>(p.counts) | (uintptr_t)((int64_t)p.vocab * 4) : 0);
-  if ((at & 15u) == 0)
-    return few ? launch_probs<In, Out, true, Few>(p, ranks, stream)
-               : launch_probs<In, Out, true, Many>(p, ranks, stream);
-  return few ? launch_probs<In, Out, false, Few>(p, ranks, stream)
-             : launch_probs<In, Out, false, Many>(p, ranks, stream);
+  const int64_t blocks = (int64_t)p.batch * p.rows * ranks;
+  const int sms = device_sm_count();
+  // rows that share their request's counts, as long as that leaves several blocks an SM
+  p.group = p.counts || p.prompt ? (int)std::min<int64_t>(std::max<int64_t>(blocks / (3 * sms), 1), kMaxGroup) : 1;
+  p.group = std::min(p.group, p.rows);
+  if ((at & 15u) != 0) return launch_probs<In, Out, false, true, Many>(p, ranks, stream);
+  if (blocks <= sms)
+    return p.penalties ? launch_probs<In, Out, true, true, Few>(p, ranks, stream)
+                       : launch_probs<In, Out, true, false, Few>(p, ranks, stream);
+  return p.penalties ? launch_probs<In, Out, true, true, Many>(p, ranks, stream)
+                     : launch_probs<In, Out, true, false, Many>(p, ranks, stream);
 }
 
 }  // namespace
@@ -492,7 +627,7 @@ extern "C" mla_status mla_logits_to_probs(
   p.num_biases = num_biases;
   p.allowed = allowed;
   p.words = (vocab + 31) / 32;
-  p.run = 0;
+  p.run = p.group = 0;
   // (without a penalty the counts, the prompt and the paths change nothing)
   p.penalties = repetition || frequency || presence;
   if (!p.penalties) p.counts = nullptr, p.prompt = nullptr;
