@@ -47,6 +47,8 @@ constexpr int kChunks = kDEntry / 64;               // 9 chunks of 64 dims
 constexpr int kChunkBytes = kPageSize * 128;        // 8192
 constexpr int kPageBytes = kChunks * kChunkBytes;   // 73,728
 constexpr int kSlots = 2;
+constexpr int kGroups = 3;                          // QK starts on a third of a page
+constexpr int kPrefetch = 4;                        // pages ahead that L2 is asked for
 constexpr float kRescaleThresh = 7.0f;              // log2 units
 constexpr uint64_t kWaitNs = 2000000000ull;         // every wait
 constexpr int kDescRing = 64;    // page descriptors in flight
@@ -66,8 +68,8 @@ constexpr int kOffPlan = kOffFlags + 16;                 // int64 [6]
 constexpr int kOffDesc = kOffPlan + 48;                  // PageDesc [kDescRing]
 constexpr int kOffBar = kOffDesc + 16 * kDescRing;
 enum Bar {
-  BAR_PAGE_FULL = 0,                  // [2] the page's bytes landed (or there are none)
-  BAR_PV_DONE = BAR_PAGE_FULL + 2,    // [2] PV of the page in the slot: slot, P and O^T free
+  BAR_PAGE_FULL = 0,                  // [2][3] three of the page's chunks landed (or there are none)
+  BAR_PV_DONE = BAR_PAGE_FULL + 2 * kGroups,    // [2] PV of the page in the slot: slot, P and O^T free
   BAR_S_FULL = BAR_PV_DONE + 2,       // [2] page j: buffer j % 2
   BAR_S_EMPTY = BAR_S_FULL + 2,       // [2] (softmax warps)
   BAR_P_FULL = BAR_S_EMPTY + 2,       // [2] (softmax warps)
@@ -86,6 +88,7 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory map exceeds 227 KB");
 enum Flag { F_ABORT = 0, F_PIECE_BAD = 1 };
 
 struct Bf16TreeParams {
+  const uint8_t* kv;
   int64_t num_pages;
   const int32_t* block_table;
   int max_pages;
@@ -230,13 +233,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           pw.next();
           ++jn;
         };
-        while (jn < kSlots && jn < npages) describe_next();
-        int64_t j = 0;
+        // (pages whose ids are waited for at page j: it and those that L2 is asked for)
+        while (jn <= kPrefetch && jn < npages) describe_next();
+        int64_t j = 0, asked = 0;
         int piece = 0;
         bool ok = true;
         for (; j < npages; ++j) {
-          cp_async_wait_upto<kTableAhead>((int)(jn - j - 1));
+          cp_async_wait_upto<kTableAhead>((int)max(jn - j - 1 - kPrefetch, (int64_t)0));
           PageDesc* d = ring + j % kDescRing;
+          for (; asked < jn && asked <= j + kPrefetch; ++asked) {
+            const int32_t ahead = ring[asked % kDescRing].page;
+            if (asked >= j + kSlots && half == 0 && ahead >= 0 && (int64_t)ahead < p.num_pages)
+              tc::prefetch_l2_bulk(p.kv + (int64_t)ahead * kPageBytes, (uint32_t)kPageBytes);
+          }
           const bool page_ok = d->page >= 0 && (int64_t)d->page < p.num_pages;
           if (page_ok) d->flags |= kDescPageOk;
           if (d->flags & kDescPieceStart) {
@@ -262,18 +271,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           if (page_ok) {
-            tc::mbar_arrive_expect_tx(bar(BAR_PAGE_FULL + slot), (uint32_t)kPageBytes);
-            if constexpr (kPair) {  // (the other half's bytes count here too)
-              for (int ch = 5 * half; ch < (half ? kChunks : 5); ++ch)
-                tc::tma_load_2d_multicast_hint(sbase + slot * kPageBytes + ch * kChunkBytes, &kv_map, 64 * ch,
-                                               d->page * kPageSize, bar(BAR_PAGE_FULL + slot), kBoth, pol);
-            } else
-            for (int ch = 0; ch < kChunks; ++ch)
-              tc::tma_load_2d_hint(sbase + slot * kPageBytes + ch * kChunkBytes, &kv_map, 64 * ch,
-                                   d->page * kPageSize, bar(BAR_PAGE_FULL + slot), pol);
+            for (int g = 0; g < kGroups; ++g)
+              tc::mbar_arrive_expect_tx(bar(BAR_PAGE_FULL + kGroups * slot + g), (uint32_t)(kPageBytes / kGroups));
+            const uint32_t to = sbase + slot * kPageBytes;
+            const int y = d->page * kPageSize;
+            if constexpr (kPair) {  // every other chunk; the other half's bytes count here too
+              for (int ch = half; ch < kChunks; ch += 2)
+                tc::tma_load_2d_multicast_hint(to + ch * kChunkBytes, &kv_map, 64 * ch, y,
+                                               bar(BAR_PAGE_FULL + kGroups * slot + ch / 3), kBoth, pol);
+            } else {
+              for (int ch = 0; ch < kChunks; ++ch)
+                tc::tma_load_2d_hint(to + ch * kChunkBytes, &kv_map, 64 * ch, y,
+                                     bar(BAR_PAGE_FULL + kGroups * slot + ch / 3), pol);
+            }
           } else {
             // bad id: no copy; every token of the page is masked, its value rows zeroed
-            tc::mbar_arrive(bar(BAR_PAGE_FULL + slot));
+            for (int g = 0; g < kGroups; ++g) tc::mbar_arrive(bar(BAR_PAGE_FULL + kGroups * slot + g));
           }
           for (int u = 0; u < 2 && jn < npages && jn <= j + kTableAhead; ++u) describe_next();
         }
@@ -281,7 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) abort_cta();
         // no copy may land after the CTA exits: wait for the last issued pages and query
         for (int64_t jj = j > kSlots ? j - kSlots : 0; jj < j; ++jj)
-          tc::mbar_wait(bar(BAR_PAGE_FULL + (int)(jj % kSlots)), (uint32_t)(jj / kSlots) & 1, kWaitNs);
+          for (int g = 0; g < kGroups; ++g)
+            tc::mbar_wait(bar(BAR_PAGE_FULL + kGroups * (int)(jj % kSlots) + g), (uint32_t)(jj / kSlots) & 1, kWaitNs);
         if (piece > 0) tc::mbar_wait(bar(BAR_Q_FULL), (uint32_t)(piece - 1) & 1, kWaitNs);
         // nor may the other CTA's commits arrive here after that
         if constexpr (kPair) {
@@ -316,17 +330,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++piece;
           }
           if (is_qk) {
-            if (ok) ok = wait(BAR_PAGE_FULL + slot, par);
             if (ok && k >= 2) ok = wait(BAR_S_EMPTY + slot, (uint32_t)((k >> 1) - 1) & 1);
-            if (!ok) break;
-            tc::fence_after_sync();
             const uint64_t kb = tc::smem_desc_sw128(page, 16, 1024);
             const uint32_t d_s = tmem + s_col((uint32_t)k & 1u);
 #pragma unroll
-            for (int s = 0; s < 4 * kChunks; ++s) {
-              const uint64_t at = (uint64_t)(((s >> 2) * kChunkBytes + (s & 3) * 32) >> 4);
-              tc::mma_f16_ss(d_s, qa + at, kb + at, id_qk, s > 0);
+            for (int g = 0; g < kGroups; ++g) {
+              if (ok) ok = wait(BAR_PAGE_FULL + kGroups * slot + g, par);
+              if (!ok) break;
+              tc::fence_after_sync();
+#pragma unroll
+              for (int s = 4 * kChunks / kGroups * g; s < 4 * kChunks / kGroups * (g + 1); ++s) {
+                const uint64_t at = (uint64_t)(((s >> 2) * kChunkBytes + (s & 3) * 32) >> 4);
+                tc::mma_f16_ss(d_s, qa + at, kb + at, id_qk, s > 0);
+              }
             }
+            if (!ok) break;
             tc::mma_commit(bar(BAR_S_FULL + (int)(k & 1)));
             if (pe) tc::mma_commit(bar(BAR_Q_EMPTY));
           } else {
@@ -382,11 +400,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t page_base = sbase + slot * kPageBytes;
         // (a failed wait, like a stop by another role, is acted on at the block barrier below)
         bool stop = flags[F_ABORT] != 0;
-        if (!tc::mbar_wait(bar(BAR_PAGE_FULL + slot), par, kWaitNs) ||
-            !tc::mbar_wait(bar(BAR_S_FULL + slot), par, kWaitNs)) {
+        // (S_FULL: all of the page has landed; the chunks' barriers make it visible here too)
+        if (!tc::mbar_wait(bar(BAR_S_FULL + slot), par, kWaitNs)) {
           flags[F_ABORT] = 1;
           stop = true;
         }
+#pragma unroll
+        for (int third = 0; third < kGroups; ++third)
+          if (!tc::mbar_wait(bar(BAR_PAGE_FULL + kGroups * slot + third), par, kWaitNs)) {
+            flags[F_ABORT] = 1;
+            stop = true;
+          }
         const PageDesc d = desc[j % kDescRing];
         const bool ps = d.flags & kDescPieceStart, pe = d.flags & kDescPieceEnd;
         const bool page_ok = d.flags & kDescPageOk;
@@ -628,6 +652,7 @@ cudaError_t launch_decode_bf16_tree(const DecodeLaunch& d, cudaStream_t stream) 
       !map(&q_map, d.q, (int64_t)d.batch * d.query_rows(), d.heads > kTileRows ? kTileRows : d.heads))
     return cudaErrorInvalidValue;
   Bf16TreeParams p;
+  p.kv = d.kv;
   p.num_pages = d.num_pages;
   p.block_table = d.block_table;
   p.max_pages = d.max_pages;

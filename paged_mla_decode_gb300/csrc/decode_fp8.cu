@@ -402,6 +402,22 @@ __device__ __forceinline__ bool e4m3x4_has_nan(uint32_t w) {
   return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
 }
 
+// A NaN in a node's entry is one for the rows that see it, which their scores make NaN already.
+// For the others it would be 0 * NaN in PV, so of tokens first .. last - 1 of a page 16-byte
+// pieces with a NaN code become zeros (QK has read them). Out of line, as the page loop wants
+// to stay short: the roles' loops share the instruction cache.
+static __device__ __noinline__ void zero_nan_chunks(uint32_t page_base, int first, int last, int t) {
+  for (int i = t; i < (last - first) * 32; i += kSmThreads) {
+    const int row = first + (i >> 5), u = i & 31;
+    const uint32_t a = page_base + (u >> 3) * kLatBlock + row * 128 + (u & 7) * 16;
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+    if (e4m3x4_has_nan(w[0]) || e4m3x4_has_nan(w[1]) || e4m3x4_has_nan(w[2]) || e4m3x4_has_nan(w[3]))
+      asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(a), "r"(0u));
+  }
+}
+
 // kGrouped: the grouped decode (GroupPlan): this CTA's shared-prefix range, then
 // its suffix range; otherwise mla_decode's single plan (Plan).
 // kE2m1: a 4-bit cache, expanded to e4m3 pages by seven more warps; otherwise e4m3.
@@ -1084,23 +1100,8 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
                          "r"(0u));
           }
         }
-        if (has_nodes && page_ok) {
-          // A NaN in a node's entry is one for the rows that see it, which their scores
-          // make NaN already. For the others it would be 0 * NaN in PV, so chunks with a
-          // NaN code become zeros.
-          const uint32_t page_base = sbase + kOffPages + slot * kPageBytes;
-          const int first = max((int)d.context, 0);
-          for (int i = t; i < (nvis - first) * 32; i += kSmThreads) {
-            const int rrow = first + (i >> 5), u = i & 31;
-            const uint32_t a = page_base + (u >> 3) * kLatBlock + rrow * 128 + (u & 7) * 16;
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
-            if (e4m3x4_has_nan(w[0]) || e4m3x4_has_nan(w[1]) || e4m3x4_has_nan(w[2]) ||
-                e4m3x4_has_nan(w[3]))
-              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(a), "r"(0u));
-          }
-        }
+        if (has_nodes && page_ok)
+          zero_nan_chunks(sbase + kOffPages + slot * kPageBytes, max((int)d.context, 0), nvis, t);
         tc::fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
