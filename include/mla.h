@@ -260,7 +260,8 @@ MLA_API mla_status mla_decode_grouped(const void* q, const void* kv_pages, int64
  * node sees. A chain of drafts is the mask 2^(j + 1) - 1.
  *
  * The max_nodes * num_heads query rows of a request are cut into tiles of 64, whatever
- * nodes they belong to, which share each page that is read. Arithmetic as mla_decode's;
+ * nodes they belong to; a tile's rows share each page that is read, and where that is faster
+ * two tiles do. Arithmetic as mla_decode's;
  * so a NaN in an entry makes the rows that see it NaN, and no others. (A cached bf16
  * infinity makes the rows that see it NaN, or drops out where its score is -inf.)
  *
@@ -498,7 +499,7 @@ MLA_API mla_status mla_verify_drafts(const void* target_probs, int64_t target_st
  * logits        device, [batch][rows] rows of `vocab`, logit_stride >= vocab elements apart
  * probs         device, likewise, prob_stride apart; may be `logits` (same type and stride)
  * logit_dtype, prob_dtype  MLA_PROB_F32 or MLA_PROB_BF16
- * vocab         1 .. MLA_MAX_PROBS_VOCAB (UNSUPPORTED beyond: a row is kept on chip)
+ * vocab         1 .. MLA_MAX_PROBS_VOCAB (UNSUPPORTED beyond: a byte a token is kept on chip)
  * temperature   device, fp32 [batch]; NULL: 1
  * num_rows      device, int32 [batch]; rows j >= num_rows[b] are left as they were; NULL: none
  * node_tokens   device, int32 [batch][rows]; NULL exactly if tree_mask is (then no drafts

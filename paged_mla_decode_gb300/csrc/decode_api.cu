@@ -52,15 +52,25 @@ namespace {
 struct TreeShape {
   int tiles, tile_rows, workers;
 };
-TreeShape tree_shape(int max_nodes, int num_heads, int num_ctas, bool may_pair) {
+TreeShape tree_shape(int max_nodes, int num_heads, int num_ctas, bool pairs) {
   const int rows = max_nodes * num_heads;
   if (rows <= 64) return TreeShape{1, rows, num_ctas};
   const int tiles = (rows + 63) / 64;
-  // a pair takes 0.8 of the time that its CTAs would take one by one, and an odd number of
-  // tiles costs it a half that has no rows
-  if (may_pair && num_ctas >= 2 && (tiles % 2 == 0 || tiles >= 5))
-    return TreeShape{(tiles + 1) / 2, 128, num_ctas / 2};
-  return TreeShape{tiles, 64, num_ctas};
+  return pairs ? TreeShape{(tiles + 1) / 2, 128, num_ctas / 2} : TreeShape{tiles, 64, num_ctas};
+}
+// Whether pairs are the faster. An odd number of tiles costs them one that has no rows. Measured
+// in turn, pairs and single CTAs, us a call:
+//   e4m3, even: 8 nodes of 64 heads, 8 sessions of 20k-100k 337, 366; 31 of 32, 32 requests of up
+//     to 4k 255, 322; 16 of 64, one of 100k 181, 185
+//   e4m3, odd: 5 tiles 223, 208; 9: 304, 289; 11: 361, 352; 17: 659, 671; 35: 533, 546
+//   bf16, even: the three of above 668, 695; 305, 333; 349, 346-361
+//   bf16, odd: 5 tiles 440, 386; 11: 728, 690; 17: 1,365, 1,350; 35: 1,082, 1,066
+// 4-bit pages are expanded by each CTA for itself (expanding each half for both took 1.7 times as
+// long).
+bool tree_by_pairs(int max_nodes, int num_heads, int num_ctas, int kv_dtype) {
+  const int tiles = (max_nodes * num_heads + 63) / 64;
+  if (tiles < 2 || num_ctas < 2 || kv_dtype == MLA_KV_E2M1) return false;
+  return tiles % 2 == 0 || (kv_dtype == MLA_KV_E4M3 && tiles >= 13);
 }
 bool tree_shape_ok(int batch, int max_nodes, int num_heads) {
   return batch >= 0 && max_nodes >= 1 && max_nodes <= MLA_MAX_TREE_NODES &&
@@ -191,8 +201,9 @@ extern "C" size_t mla_decode_tree_workspace_size(int batch, int max_nodes, int n
   if (num_ctas == 0) num_ctas = mla::device_sm_count();
   if (num_ctas <= 0) return 0;
   size_t most = 0;  // (the cache's type is not known here)
-  for (const bool may_pair : {false, true}) {
-    const TreeShape t = tree_shape(max_nodes, num_heads, num_ctas, may_pair);
+  for (const bool pairs : {false, true}) {
+    if (pairs && num_ctas < 2) break;
+    const TreeShape t = tree_shape(max_nodes, num_heads, num_ctas, pairs);
     const size_t n = mla::workspace_layout((int64_t)batch * t.tiles, t.tile_rows, t.workers).total;
     most = n > most ? n : most;
   }
@@ -227,8 +238,7 @@ extern "C" mla_status mla_decode_tree(const void* q, const void* kv_pages, int64
   if ((int64_t)batch * max_pages > 0x7fffffffLL) return MLA_ERR_UNSUPPORTED;
   const int G = num_ctas ? num_ctas : device_sm_count();
   if (G <= 0) return MLA_ERR_CUDA;
-  // (a 4-bit cache's pages are expanded by each CTA for itself)
-  const TreeShape t = tree_shape(max_nodes, num_heads, G, kv_dtype != MLA_KV_E2M1);
+  const TreeShape t = tree_shape(max_nodes, num_heads, G, tree_by_pairs(max_nodes, num_heads, G, kv_dtype));
   const int64_t rows = (int64_t)batch * t.tiles;
   if (rows * t.tile_rows > 0x7fffffffLL) return MLA_ERR_UNSUPPORTED;
   const WorkspaceLayout L = workspace_layout(rows, t.tile_rows, t.workers);

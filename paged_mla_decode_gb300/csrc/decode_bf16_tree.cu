@@ -13,7 +13,7 @@
 // (bf16, 8 KB) takes the place of its own page's rotary chunk, which QK has read by then.
 // P = 2^(s - m) with m a running maximum that rises when a page's lies more than 2^7 above it:
 // bf16 has float's range, so P of a page far below m keeps its 8 bits (each rounded once,
-// 2^-9 of itself; the normaliser sums the exact P).
+// 2^-8 of itself at most; the normaliser sums the exact P).
 //
 // Warp roles (352 threads):
 //   warps 0-7  softmax and epilogue: row h of S is TMEM lane 32*(h/16) + h%16 (M = 64); thread
