@@ -69,8 +69,8 @@ TreeShape tree_shape(int max_nodes, int num_heads, int num_ctas, bool pairs) {
 // long).
 bool tree_by_pairs(int max_nodes, int num_heads, int num_ctas, int kv_dtype) {
   const int tiles = (max_nodes * num_heads + 63) / 64;
-  if (tiles < 2 || num_ctas < 2 || kv_dtype == MLA_KV_E2M1) return false;
-  return tiles % 2 == 0 || (kv_dtype == MLA_KV_E4M3 && tiles >= 13);
+  if (tiles < 2 || num_ctas < 2) return false;
+  return tiles % 2 == 0 || (kv_dtype != MLA_KV_BF16 && tiles >= 13);
 }
 bool tree_shape_ok(int batch, int max_nodes, int num_heads) {
   return batch >= 0 && max_nodes >= 1 && max_nodes <= MLA_MAX_TREE_NODES &&

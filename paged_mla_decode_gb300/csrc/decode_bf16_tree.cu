@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffTmem);
   auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * (uint32_t)i; };
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (the compiler sees that it is a warp's)
   const int c = kPair ? blockIdx.x >> 1 : blockIdx.x;
   const int half = kPair ? (int)tc::cluster_rank() : 0;  // of the tile's rows
   constexpr uint16_t kBoth = 3;
@@ -305,72 +306,84 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp >= kQkWarp) {
-      // =================== MMA issuers (lane 0 of two warps) ===================
+      // =================== MMA issuers (two warps) ===================
+      // The whole warp runs the loop, with values that the compiler knows to be a warp's (an MMA
+      // takes its operands from uniform registers), and one elected thread issues the MMAs: a
+      // loop of lane 0 alone took 70 cycles for each.
       constexpr uint32_t id_qk = tc::idesc_f16(64, 64, true, false, false);
       constexpr uint32_t id_pv = tc::idesc_f16(128, 64, true, true, false);  // A = V^T, MN-major
       const bool is_qk = warp == kQkWarp;
-      if (lane == 0) {
-        auto wait = [&](int b, uint32_t parity) -> bool { return tc::mbar_wait(bar(b), parity, kWaitNs); };
-        int piece = 0;
-        bool ok = true;
-        PageWalker<TreePlan> pw;  // piece boundaries
-        pw.init(plan, cur0, c, x_begin, x_end);
-        const uint64_t qa = tc::smem_desc_sw128(sbase + kOffQ, 16, 1024);
-        for (int64_t k = 0; k < npages && ok; ++k, pw.next()) {
-          if (flags[F_ABORT]) {
-            ok = false;
-            break;
-          }
-          const bool ps = pw.piece_start(), pe = pw.piece_end();
-          const int slot = (int)(k % kSlots);
-          const uint32_t par = (uint32_t)(k / kSlots) & 1;
-          const uint32_t page = sbase + slot * kPageBytes;
-          if (ps) {
-            ok = wait(is_qk ? BAR_Q_FULL : BAR_O_EMPTY, (uint32_t)piece & 1);
-            ++piece;
-          }
-          if (is_qk) {
-            if (ok && k >= 2) ok = wait(BAR_S_EMPTY + slot, (uint32_t)((k >> 1) - 1) & 1);
-            const uint64_t kb = tc::smem_desc_sw128(page, 16, 1024);
-            const uint32_t d_s = tmem + s_col((uint32_t)k & 1u);
+      auto wait = [&](int b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, tc::mbar_wait(bar(b), parity, kWaitNs));
+      };
+      int piece = 0, left = 0, in_piece = 0;  // pages of the piece
+      bool ok = true;
+      PageWalker<TreePlan> pw;  // piece boundaries
+      pw.init(plan, cur0, c, x_begin, x_end);
+      const uint64_t qa = tc::smem_desc_sw128(sbase + kOffQ, 16, 1024);
+      const uint32_t pages = __shfl_sync(0xffffffffu, (uint32_t)npages, 0);
+      for (uint32_t k = 0; k < pages && ok; ++k) {
+        if (__any_sync(0xffffffffu, flags[F_ABORT])) {
+          ok = false;
+          break;
+        }
+        const uint32_t slot = k % kSlots, par = (k / kSlots) & 1;
+        const uint32_t page = sbase + slot * kPageBytes;
+        if (left == 0) {
+          left = in_piece = __shfl_sync(0xffffffffu, pw.piece_pages(), 0);
+          ok = wait(is_qk ? BAR_Q_FULL : BAR_O_EMPTY, (uint32_t)piece & 1);
+          ++piece;
+        }
+        if (is_qk) {
+          if (ok && k >= 2) ok = wait(BAR_S_EMPTY + slot, ((k >> 1) - 1) & 1);
+          const uint64_t kb = tc::smem_desc_sw128(page, 16, 1024);
+          const uint32_t d_s = tmem + s_col(k & 1u);
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-              if (ok) ok = wait(BAR_PAGE_FULL + kGroups * slot + g, par);
-              if (!ok) break;
-              tc::fence_after_sync();
-#pragma unroll
-              for (int s = 4 * kChunks / kGroups * g; s < 4 * kChunks / kGroups * (g + 1); ++s) {
-                const uint64_t at = (uint64_t)(((s >> 2) * kChunkBytes + (s & 3) * 32) >> 4);
-                tc::mma_f16_ss(d_s, qa + at, kb + at, id_qk, s > 0);
-              }
-            }
-            if (!ok) break;
-            tc::mma_commit(bar(BAR_S_FULL + (int)(k & 1)));
-            if (pe) tc::mma_commit(bar(BAR_Q_EMPTY));
-          } else {
-            if (ok) ok = wait(BAR_P_FULL + slot, par);
+          for (int g = 0; g < kGroups; ++g) {
+            if (ok) ok = wait(BAR_PAGE_FULL + kGroups * slot + g, par);
             if (!ok) break;
             tc::fence_after_sync();
-            const uint64_t va = tc::smem_desc_sw128(page, kChunkBytes, 1024);
-            const uint64_t pb = tc::smem_desc_sw128(page + (kChunks - 1) * kChunkBytes, 16, 1024);
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int s = 4 * kChunks / kGroups * g; s < 4 * kChunks / kGroups * (g + 1); ++s) {
+                const uint32_t at = (s >> 2) * kChunkBytes + (s & 3) * 32;
+                tc::mma_f16_ss(d_s, tc::desc_at(qa, at), tc::desc_at(kb, at), id_qk, s > 0);
+              }
+            }
+          }
+          if (!ok) break;
+          if (tc::elect_one()) {
+            tc::mma_commit(bar(BAR_S_FULL + (int)(k & 1)));
+            if (left == 1) tc::mma_commit(bar(BAR_Q_EMPTY));
+          }
+        } else {
+          if (ok) ok = wait(BAR_P_FULL + slot, par);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint64_t va = tc::smem_desc_sw128(page, kChunkBytes, 1024);
+          const uint64_t pb = tc::smem_desc_sw128(page + (kChunks - 1) * kChunkBytes, 16, 1024);
+          if (tc::elect_one()) {
 #pragma unroll
             for (int blk = 0; blk < 4; ++blk)
 #pragma unroll
               for (int s = 0; s < 4; ++s)
-                tc::mma_f16_ss(tmem + kOCol + 64 * blk,
-                               va + (uint64_t)((2 * blk * kChunkBytes + s * 2048) >> 4),
-                               pb + (uint64_t)((32 * s) >> 4), id_pv, 1);
+                tc::mma_f16_ss(tmem + kOCol + 64 * blk, tc::desc_at(va, 2 * blk * kChunkBytes + s * 2048),
+                               tc::desc_at(pb, 32 * s), id_pv, 1);
             tc::mma_commit(bar(BAR_PV_DONE + slot));
             if constexpr (kPair) tc::mma_commit_multicast(bar(BAR_FREE + slot), kBoth);
-            if (pe) tc::mma_commit(bar(BAR_O_FULL));
+            if (left == 1) tc::mma_commit(bar(BAR_O_FULL));
           }
         }
-        if (!ok) abort_cta();
-        // drain: every MMA this thread issued has finished before TMEM is freed
-        const int db = BAR_DRAIN + (is_qk ? 0 : 1);
-        tc::mma_commit(bar(db));
-        if (!tc::mbar_wait(bar(db), 0, kWaitNs)) atomicOr(p.ws.status, MLA_DEVICE_ERR_TIMEOUT);
+        if (--left == 0) {
+          pw.to_piece_end(in_piece);
+          pw.next();
+        }
       }
+      if (!ok && lane == 0) abort_cta();
+      // drain: every MMA this warp issued has finished before TMEM is freed
+      const int db = BAR_DRAIN + (is_qk ? 0 : 1);
+      if (tc::elect_one()) tc::mma_commit(bar(db));
+      if (!tc::mbar_wait(bar(db), 0, kWaitNs)) atomicOr(p.ws.status, MLA_DEVICE_ERR_TIMEOUT);
       __syncwarp();
     } else {
       // =================== softmax + epilogue (warps 0-7) ===================

@@ -33,7 +33,7 @@
 // with shared memory at three quarters of its rate: a page's MMAs read 140 KB of operands
 // (V twice, for P's two terms), the P buffers and page copies move 35 KB, the expansion 55.
 //
-// Warp roles (416 threads; 640 with the expanders):
+// Warp roles (352 threads; 576 with the expanders):
 //   warps 0-7  q loading, softmax and epilogue. Row t of A and S is (head
 //              16*(t/32) + t%16, part (t/16)%2), part 0 = hi, 1 = lo. Warp w reads
 //              TMEM lanes 32*(w%4) .. +31; thread (w, lane) handles head
@@ -45,14 +45,14 @@
 //   warp 8     TMA producer (lane 0): page ids from the block table a window of
 //              pages ahead, pages into a ring of kRing shared-memory slots
 //              (128-byte swizzled latent blocks, 64-byte swizzled rope block).
-//   warps 9-10 issue QK of even / odd pages (lane 0); warp 9 allocates TMEM.
-//   warps 11-12 issue PV of even / odd pages (lane 0).
-//   warps 13-19 (4-bit cache only) expand raw pages into the ring. More than 20 warps
+//   warp 9     issues QK and allocates TMEM; warp 10 issues PV. The whole warp runs the loop, with
+//              values that the compiler knows to be a warp's (an MMA takes its operands from
+//              uniform registers), and one elected thread issues a page's MMAs: 27 cycles an
+//              MMA. A loop of lane 0 alone took 70, and two such warps for each contraction
+//              kept the pipe fed no better.
+//   warps 11-17 (4-bit cache only) expand raw pages into the ring. More than 20 warps
 //              would leave a thread 80 registers, with which the softmax takes twice as
 //              long; up to 20 it has 96.
-// A thread that issues MMAs stalls for a while after each batch (until the
-// tensor pipe's queue has room), so two issuers per contraction keep the pipe
-// fed: one issues while the other waits.
 // TMEM (512 columns): A latent part [0,128), S buffers [128,192) [192,256),
 // O^T [256,512). The rope part of A is in shared memory.
 //
@@ -87,13 +87,12 @@ enum StampPoint {
 constexpr int kSmWarps = 8;                          // softmax / epilogue warps
 constexpr int kSmThreads = 32 * kSmWarps;            // 256
 constexpr int kTmaWarp = kSmWarps;                   // 8
-// MMA issuers: two QK warps and two PV warps, each issuing every other page
-// (page k goes to warp k % 2 of its kind), so that one warp's stall after a batch
-// of MMAs (an issuing thread waits on its MMA queue) overlaps the other's issue.
-constexpr int kQkWarp0 = kSmWarps + 1;               // 9: also allocates TMEM
-constexpr int kPvWarp0 = kSmWarps + 3;               // 11
-constexpr int kExpWarp0 = kSmWarps + 5;              // 13: expanders of a 4-bit cache
+constexpr int kQkWarp = kSmWarps + 1;                // 9: also allocates TMEM
+constexpr int kPvWarp = kSmWarps + 2;                // 10
+constexpr int kExpWarp0 = kSmWarps + 3;              // 11: expanders of a 4-bit cache
 constexpr int kExpWarps = 7;
+constexpr int kShares = 9;                           // of a half page, expanded by a pair's CTA
+constexpr uint32_t kShareBytes = 2048;
 constexpr int kPageBytes = kPageSize * kDEntry;      // 36864
 constexpr int kLatBlock = kPageSize * 128;           // 8192: 64 rows x 128 dims
 constexpr int kRopeOff = 4 * kLatBlock;              // rope block within a page slot
@@ -129,7 +128,7 @@ constexpr int kTableAhead = 32;  // pages described (block-table read started) b
 // Shared memory map (offsets from a 1024-aligned base) and barriers.
 template <bool kE2m1>
 struct Map {
-  static constexpr int kThreads = 32 * (kE2m1 ? kExpWarp0 + kExpWarps : kSmWarps + 5);  // 640, 416
+  static constexpr int kThreads = 32 * (kExpWarp0 + (kE2m1 ? kExpWarps : 0));  // 576, 352
   static constexpr int kRing = kE2m1 ? 4 : 5;          // e4m3 pages in flight
   static constexpr int kRawRing = kE2m1 ? 2 : 0;       // 4-bit pages in flight
   static constexpr int kOffPages = 0;
@@ -147,7 +146,7 @@ struct Map {
   static constexpr int kOffDesc = kOffPlan + 48;                    // PageDesc [kDescRing]
   static constexpr int kOffBar = kOffDesc + 16 * kDescRing;
   // the page is readable in its ring slot: its TMA bytes landed (or there are none), or
-  // every expander warp has written its part
+  // every expander warp has written its part (a pair: its own shares, and the other CTA's bytes)
   static constexpr int BAR_PAGE_FULL = 0;                 // [kRing]
   // PV(k) completes barrier BAR_PV_DONE + k % kRing (one commit per page): it frees
   // page slot k % kRing for the TMA warp (the expanders), P buffer k % 3 for the softmax
@@ -162,8 +161,8 @@ struct Map {
   static constexpr int BAR_O_EMPTY = BAR_O_FULL + 1;      // (softmax warps)
   static constexpr int BAR_Q_READY = BAR_O_EMPTY + 1;     // (softmax warps)
   static constexpr int BAR_Q_EMPTY = BAR_Q_READY + 1;
-  static constexpr int BAR_DRAIN = BAR_Q_EMPTY + 1;       // [4] one per issuer warp
-  static constexpr int BAR_RAW_FULL = BAR_DRAIN + 4;      // [kRawRing] bulk-copy bytes landed
+  static constexpr int BAR_DRAIN = BAR_Q_EMPTY + 1;       // [2] one per issuer warp
+  static constexpr int BAR_RAW_FULL = BAR_DRAIN + 2;      // [kRawRing] bulk-copy bytes landed
   static constexpr int BAR_RAW_EMPTY = BAR_RAW_FULL + kRawRing;  // [kRawRing] (expander warps)
   // pairs of CTAs only: both CTAs' PVs have read the page in the slot
   static constexpr int BAR_FREE = BAR_RAW_EMPTY + kRawRing;      // [kRing]
@@ -177,14 +176,13 @@ struct Map {
   static constexpr int kNumBars = BAR_FREE + kRing;
 #endif
   // arrivals that complete a phase of barrier i
-  static __device__ __forceinline__ uint32_t bar_count(int i) {
+  static __device__ __forceinline__ uint32_t bar_count(int i, bool pair) {
     if ((i >= BAR_S_EMPTY && i < BAR_S_EMPTY + 2) || (i >= BAR_P_FULL && i < BAR_P_FULL + kPBufs) ||
         i == BAR_O_EMPTY || i == BAR_Q_READY)
       return kSmWarps;
-    if (i == BAR_Q_EMPTY || i == BAR_O_FULL) return 2;  // both issuer warps of the kind commit
     if (i >= BAR_FREE && i < BAR_FREE + kRing) return 2;  // both CTAs' commits
     if (kE2m1 && (i < kRing || (i >= BAR_RAW_EMPTY && i < BAR_RAW_EMPTY + kRawRing)))
-      return kExpWarps;
+      return pair ? kShares : kExpWarps;
     return 1;
   }
   static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
@@ -397,6 +395,35 @@ __device__ __forceinline__ void expand_page(const Expander& x, uint32_t raw, uin
   }
 }
 
+// A pair's CTAs expand half of a page each and copy it to each other: CTA `half` blocks
+// 8 * half .. + 7 and the rope blocks of tokens 32 * half .. + 31. A share is what lies together
+// in the page: four blocks of 16 tokens (shares 0-7) or the rope's two of 32 (share 8).
+__device__ __forceinline__ uint32_t share_offset(uint32_t share, int half) {
+  return share < 8 ? (2 * half + (share >> 2)) * kLatBlock + (share & 3) * kShareBytes
+                   : kRopeOff + half * kShareBytes;
+}
+__device__ __forceinline__ void expand_share(uint32_t share, int half, int lane, uint32_t raw,
+                                             uint32_t page, uint32_t lut) {
+  const bool rope = share == 8;
+  const int token = rope ? 32 * half + lane : 16 * (int)(share & 3) + (lane & 15);
+  const int block = rope ? 16 : 4 * (2 * half + (int)(share >> 2)) + (lane >> 4);  // and + step
+  const int step = rope ? 1 : 2;
+  uint32_t n[2];  // the blocks' nibbles, at bit 3
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int b = block + step * k;
+    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(n[k]) : "r"(raw + e2m1_exp_offset(b, token)));
+    n[k] = (b & 1) ? n[k] >> 1 : n[k] << 3;
+  }
+  ExpandUnit x[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) expand_load(x[k], raw + e2m1_code_offset(block + step * k, token), lut, n[k]);
+  const uint32_t sw = (rope ? (token >> 1) & 3 : token & 7) << 4;
+  const uint32_t row = page + token * (rope ? 64 : 128) + (block / 4) * kLatBlock;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) expand_write(x[k], row + (((32u * (block + step * k)) & 96u) ^ sw));
+}
+
 // Whether one of four e4m3 codes is a NaN (0x7f, 0xff).
 __device__ __forceinline__ bool e4m3x4_has_nan(uint32_t w) {
   return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
@@ -456,7 +483,8 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::kOffTmem);
   auto bar = [&](int i) -> uint32_t { return sbase + M::kOffBar + 8u * (uint32_t)i; };
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (the compiler sees that it is a warp's)
   if (tid == 0) MLA_STAMP(kStEntry, 0);
 
   // ---- planning (shared by all roles) ----
@@ -466,7 +494,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
   // itself needs the split kernel to have completed (griddep_wait before q_op).
   using RowPlan = std::conditional_t<kTree, TreePlan, Plan>;
   RowPlan plan = row_plan<RowPlan>(p);
-  static_assert(!kPair || (kTree && !kE2m1), "pairs are the tree decode's, over e4m3 pages");
+  static_assert(!kPair || kTree, "pairs are the tree decode's");
   const int c = kPair ? blockIdx.x >> 1 : blockIdx.x;
   const int half = kPair ? (int)tc::cluster_rank() : 0;  // of the tile's rows
   constexpr uint16_t kBoth = 3;
@@ -514,7 +542,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
       tc::prefetch_tensormap(&lat_map);
       tc::prefetch_tensormap(&rope_map);
     }
-    for (int i = 0; i < M::kNumBars; ++i) tc::mbar_init(bar(i), M::bar_count(i));
+    for (int i = 0; i < M::kNumBars; ++i) tc::mbar_init(bar(i), M::bar_count(i, kPair));
     tc::fence_mbar_init();
     flags[F_ABORT] = 0;
     flags[F_PIECE_BAD] = 0;
@@ -523,7 +551,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
     if (warp == kExpWarp0 && lane < 16)
       reinterpret_cast<uint64_t*>(smem + M::kOffLut)[lane] = kE2m1Lut[lane];
   }
-  if (warp == kQkWarp0) {
+  if (warp == kQkWarp) {
     tc::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tc::tmem_relinquish();
   }
@@ -686,7 +714,12 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
         for (int64_t jj = j > kLanding ? j - kLanding : 0; jj < j; ++jj)
           tc::mbar_wait(bar(kLandBar + (int)(jj % kLanding)), (uint32_t)(jj / kLanding) & 1,
                         kDrainWaitNs);
-        // nor may the other CTA's commits arrive here after that
+        // nor may the other CTA's copies and commits arrive here after that
+        if constexpr (kPair && kE2m1) {
+          for (int64_t jj = j > kRing ? j - kRing : 0; jj < j; ++jj)
+            if (!tc::mbar_wait(bar(BAR_PAGE_FULL + (int)(jj % kRing)), (uint32_t)(jj / kRing) & 1, kDrainWaitNs))
+              break;
+        }
         if constexpr (kPair) {
           for (int64_t jj = j > kRing ? j - kRing : 0; jj < j; ++jj)
             tc::mbar_wait(bar(M::BAR_FREE + (int)(jj % kRing)), (uint32_t)(jj / kRing) & 1, kDrainWaitNs);
@@ -695,7 +728,39 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
       __syncwarp();
     } else if (kE2m1 && warp >= kExpWarp0) {
       // =================== expanders of a 4-bit cache (7 warps) ===================
-      if constexpr (kE2m1) {
+      if constexpr (kE2m1 && kPair) {
+        // the shares of all pages' halves go round the warps
+        bool ok = true;
+        const uint32_t lut = sbase + M::kOffLut;
+        const uint32_t shares = (uint32_t)npages * kShares;
+        for (uint32_t u = warp - kExpWarp0; u < shares; u += kExpWarps) {
+          const uint32_t j = u / kShares, rs = j % M::kRawRing, slot = j % kRing;
+          ok = tc::mbar_wait(bar(M::BAR_RAW_FULL + rs), (j / M::kRawRing) & 1, kWaitNs);
+          // both CTAs' PVs have read the page that held the slot
+          if (ok && j >= kRing) ok = tc::mbar_wait(bar(M::BAR_FREE + slot), (j / kRing - 1) & 1, kWaitNs);
+          ok = __all_sync(0xffffffffu, ok && !flags[F_ABORT]);
+          if (!ok) break;
+          const bool page_ok = desc[j % kDescRing].flags & kDescPageOk;
+          const uint32_t page = sbase + kOffPages + slot * kPageBytes;
+          const uint32_t share = page + share_offset(u - j * kShares, half);
+          if (page_ok)
+            expand_share(u - j * kShares, half, lane, sbase + M::kOffRaw + rs * kE2m1PageBytes, page, lut);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (page_ok) {
+              // (as many bytes come from the other CTA)
+              tc::mbar_arrive_expect_tx(bar(BAR_PAGE_FULL + slot), kShareBytes);
+              tc::bulk_copy_to_cta(tc::cluster_address(share, 1 - half), share, kShareBytes,
+                                   tc::cluster_address(bar(BAR_PAGE_FULL + slot), 1 - half));
+            } else {
+              tc::mbar_arrive(bar(BAR_PAGE_FULL + slot));
+            }
+            tc::mbar_arrive(bar(M::BAR_RAW_EMPTY + rs));
+          }
+        }
+        if (!ok && lane == 0) abort_cta();
+      } else if constexpr (kE2m1) {
         bool ok = true;
         const Expander x = expander<M>(warp - kExpWarp0, lane);
         const uint32_t lut = sbase + M::kOffLut;
@@ -721,114 +786,113 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
         }
         if (!ok && lane == 0) abort_cta();
       }
-    } else if (warp >= kQkWarp0) {
-      // ============ MMA issuers: two QK warps, two PV warps; lane 0 issues ============
-      // Page k's QK is issued by QK warp k % 2 (into S buffer k % 2, which is that
-      // warp's own) and its PV by PV warp k % 2. MMAs of different threads complete
-      // in no particular order relative to each other, so every wait names the page
-      // it needs (PV_DONE per page) and the once-per-piece barriers count both warps
-      // of a kind: each passes every piece start (QK: the piece's q is loaded; PV:
-      // O^T is zero) and commits at every piece end (Q_EMPTY, O_FULL), whether or not
-      // it issued a page of that piece. PV always accumulates: the softmax warps zero
-      // O^T before a piece starts. A PV issues its e4m3 (hi) MMAs before its e5m2
-      // (lo) ones: MMAs that alternate B formats run at half rate.
+    } else if (warp >= kQkWarp) {
+      // ============ MMA issuers: a QK warp and a PV warp ============
+      // MMAs of different threads complete in no particular order relative to each other,
+      // so every wait names the page it needs (PV_DONE per page). PV always accumulates:
+      // the softmax warps zero O^T before a piece starts. A PV issues its e4m3 (hi) MMAs
+      // before its e5m2 (lo) ones: MMAs that alternate B formats run at half rate.
       constexpr uint32_t id_qk = tc::idesc_f8(128, 64, tc::kFmtE4M3, tc::kFmtE4M3, false, false);
       // PV: A = V^T (e4m3, MN-major); B = P^T hi (e4m3) or lo (e5m2), K-major
       constexpr uint32_t id_pv_hi = tc::idesc_f8(128, 64, tc::kFmtE4M3, tc::kFmtE4M3, true, false);
       constexpr uint32_t id_pv_lo = tc::idesc_f8(128, 64, tc::kFmtE4M3, tc::kFmtE5M2, true, false);
-      const bool is_qk = warp < kPvWarp0;
-      const int mine = warp - (is_qk ? kQkWarp0 : kPvWarp0);  // pages k with k % 2 == mine
-      // Only lane 0 runs the issue loop: MMA issue stalls while the tensor pipe's
-      // queue is full, so any other work between batches (warp votes, shuffles,
-      // warp barriers) leaves the pipe idle.
-      if (lane == 0) {
-        auto wait = [&](int b, uint32_t parity) -> bool {
-          return tc::mbar_wait(bar(b), parity, kWaitNs);
-        };
-        const uint64_t qrope_desc = tc::smem_desc(sbase + kOffQRope, 16, 512, tc::kSwizzle64);
-        int piece_n = 0;
-        bool ok = true;
-        Walker pw;  // piece boundaries without reading the shared descriptors
-        start_walker(pw);
-        for (int64_t k = 0; k < npages && ok; ++k, pw.next()) {
-          // (another role's stop is seen here every 8 pages, or as a wait that runs out)
-          if ((k & 7) == 0 && flags[F_ABORT]) {
+      const bool is_qk = warp == kQkWarp;
+      auto wait = [&](int b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, tc::mbar_wait(bar(b), parity, kWaitNs));
+      };
+      const uint64_t qrope_desc = tc::smem_desc(sbase + kOffQRope, 16, 512, tc::kSwizzle64);
+      int piece_n = 0;
+      bool ok = true;
+      Walker pw;  // piece boundaries without reading the shared descriptors
+      start_walker(pw);
+      const uint32_t pages = __shfl_sync(0xffffffffu, (uint32_t)npages, 0);
+      uint32_t slot = 0, par = 0, pb_i = 0, pb_par = 0;  // page k's, counted
+      int left = 0, in_piece = 0;                        // pages of the piece
+      for (uint32_t k = 0; k < pages && ok; ++k) {
+        // (another role's stop is seen here every 8 pages, or as a wait that runs out)
+        if ((k & 7) == 0 && __any_sync(0xffffffffu, flags[F_ABORT])) {
+          ok = false;
+          break;
+        }
+        if (left == 0) {
+          left = in_piece = __shfl_sync(0xffffffffu, pw.piece_pages(), 0);
+          ok = wait(is_qk ? BAR_Q_READY : BAR_O_EMPTY, (uint32_t)piece_n & 1);
+          ++piece_n;
+          if (!ok) break;
+        }
+        const uint32_t page_base = sbase + kOffPages + slot * kPageBytes;
+        if (is_qk) {
+          // ---- S(k) = A . page(k)^T: latent part of A from TMEM, rope from shared memory ----
+#ifdef MLA_TEST_STALL_QK
+          if (k == 2 && !wait(M::BAR_TEST_STALL, 0)) {
             ok = false;
             break;
           }
-          const bool ps = pw.piece_start(), pe = pw.piece_end();
-          if (ps) {
-            ok = wait(is_qk ? BAR_Q_READY : BAR_O_EMPTY, (uint32_t)piece_n & 1);
-            ++piece_n;
-            if (!ok) break;
-          }
-          if ((int)(k & 1) == mine) {
-            const int slot = (int)(k % kRing);
-            const uint32_t page_base = sbase + kOffPages + slot * kPageBytes;
-            if (is_qk) {
-              // ---- S(k) = A . page(k)^T: latent part of A from TMEM, rope from shared memory ----
-#ifdef MLA_TEST_STALL_QK
-              if (k == 2 && !wait(M::BAR_TEST_STALL, 0)) {
-                ok = false;
-                break;
-              }
 #endif
-              MLA_STAMP(kStQkTop, k);
-              ok = wait(BAR_PAGE_FULL + slot, (uint32_t)(k / kRing) & 1);
-              MLA_STAMP(kStQkPage, k);
-              // S buffer k % 2 last held S(k - 2), issued by this warp
-              if (ok && k >= 2) ok = wait(BAR_S_EMPTY + (int)(k & 1), (uint32_t)((k >> 1) - 1) & 1);
-              if (!ok) break;
-              MLA_STAMP(kStQkGo, k);
-              tc::fence_after_sync();
-              const uint64_t kb = tc::smem_desc(page_base, 16, 1024, tc::kSwizzle128);
-              const uint64_t rb = tc::smem_desc(page_base + kRopeOff, 16, 512, tc::kSwizzle64);
-              const uint32_t d_s = tmem + s_col((int)(k & 1));
+          MLA_STAMP(kStQkTop, k);
+          ok = wait(BAR_PAGE_FULL + slot, par);
+          MLA_STAMP(kStQkPage, k);
+          // S buffer k % 2 last held S(k - 2)
+          if (ok && k >= 2) ok = wait(BAR_S_EMPTY + (int)(k & 1), ((k >> 1) - 1) & 1);
+          if (!ok) break;
+          MLA_STAMP(kStQkGo, k);
+          tc::fence_after_sync();
+          const uint64_t kb = tc::smem_desc(page_base, 16, 1024, tc::kSwizzle128);
+          const uint64_t rb = tc::smem_desc(page_base + kRopeOff, 16, 512, tc::kSwizzle64);
+          const uint32_t d_s = tmem + s_col((int)(k & 1));
+          if (tc::elect_one()) {
 #pragma unroll
-              for (int s = 0; s < 16; ++s)
-                tc::mma_f8_ts(d_s, tmem + kQCol + 8 * s,
-                              kb + (uint64_t)(((s >> 2) * kLatBlock + (s & 3) * 32) >> 4), id_qk,
-                              s > 0);
+            for (int s = 0; s < 16; ++s)
+              tc::mma_f8_ts(d_s, tmem + kQCol + 8 * s, tc::desc_at(kb, (s >> 2) * kLatBlock + (s & 3) * 32),
+                            id_qk, s > 0);
 #pragma unroll
-              for (int s = 0; s < 2; ++s)
-                tc::mma_f8_ss(d_s, qrope_desc + (uint64_t)((32 * s) >> 4),
-                              rb + (uint64_t)((32 * s) >> 4), id_qk, 1);
-              MLA_STAMP(kStQkMma, k);
-              tc::mma_commit(bar(BAR_S_FULL + (int)(k & 1)));
-              MLA_STAMP(kStQkIssued, k);
-            } else {
-              // ---- O^T += V^T P^T (V read in place through an MN-major descriptor) ----
-              const int pb_i = (int)(k % kPBufs);
-              ok = wait(BAR_P_FULL + pb_i, (uint32_t)(k / kPBufs) & 1);
-              if (!ok) break;
-              MLA_STAMP(kStPvP, k);
-              tc::fence_after_sync();
-              const uint64_t va = tc::smem_desc(page_base, kLatBlock, 1024, tc::kSwizzle128);
-              const uint64_t pb =
-                  tc::smem_desc(sbase + kOffP + pb_i * kPBytes, 16, 1024, tc::kSwizzle128);
-#pragma unroll
-              for (int part = 0; part < 2; ++part)
-#pragma unroll
-                for (int blk = 0; blk < 4; ++blk)
-#pragma unroll
-                  for (int s = 0; s < 2; ++s)
-                    tc::mma_f8_ss(tmem + kOCol + 64 * blk,
-                                  va + (uint64_t)((blk * kLatBlock + s * 4096) >> 4),
-                                  pb + (uint64_t)((64 * part + 32 * s) >> 4),
-                                  part ? id_pv_lo : id_pv_hi, 1);
-              tc::mma_commit(bar(BAR_PV_DONE + slot));
-              if constexpr (kPair) tc::mma_commit_multicast(bar(M::BAR_FREE + slot), kBoth);
-              MLA_STAMP(kStPvIssued, k);
-            }
+            for (int s = 0; s < 2; ++s)
+              tc::mma_f8_ss(d_s, tc::desc_at(qrope_desc, 32 * s), tc::desc_at(rb, 32 * s), id_qk, 1);
+            MLA_STAMP(kStQkMma, k);
+            tc::mma_commit(bar(BAR_S_FULL + (int)(k & 1)));
           }
-          if (pe) tc::mma_commit(bar(is_qk ? BAR_Q_EMPTY : BAR_O_FULL));
+          MLA_STAMP(kStQkIssued, k);
+        } else {
+          // ---- O^T += V^T P^T (V read in place through an MN-major descriptor) ----
+          ok = wait(BAR_P_FULL + pb_i, pb_par);
+          if (!ok) break;
+          MLA_STAMP(kStPvP, k);
+          tc::fence_after_sync();
+          const uint64_t va = tc::smem_desc(page_base, kLatBlock, 1024, tc::kSwizzle128);
+          const uint64_t pb = tc::smem_desc(sbase + kOffP + pb_i * kPBytes, 16, 1024, tc::kSwizzle128);
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int blk = 0; blk < 4; ++blk)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                  tc::mma_f8_ss(tmem + kOCol + 64 * blk, tc::desc_at(va, blk * kLatBlock + s * 4096),
+                                tc::desc_at(pb, 64 * part + 32 * s), part ? id_pv_lo : id_pv_hi, 1);
+            tc::mma_commit(bar(BAR_PV_DONE + slot));
+            if constexpr (kPair) tc::mma_commit_multicast(bar(M::BAR_FREE + slot), kBoth);
+          }
+          MLA_STAMP(kStPvIssued, k);
         }
-        if (!ok) abort_cta();
-        // drain: every MMA this thread issued has finished before TMEM is freed
-        const int db = BAR_DRAIN + (warp - kQkWarp0);
-        tc::mma_commit(bar(db));
-        if (!tc::mbar_wait(bar(db), 0, kDrainWaitNs)) atomicOr(p.ws.status, MLA_DEVICE_ERR_TIMEOUT);
+        if (--left == 0) {
+          if (tc::elect_one()) tc::mma_commit(bar(is_qk ? BAR_Q_EMPTY : BAR_O_FULL));
+          pw.to_piece_end(in_piece);
+          pw.next();
+        }
+        if (++slot == kRing) {
+          slot = 0;
+          par ^= 1u;
+        }
+        if (++pb_i == kPBufs) {
+          pb_i = 0;
+          pb_par ^= 1u;
+        }
       }
+      if (!ok && lane == 0) abort_cta();
+      // drain: every MMA this warp issued has finished before TMEM is freed
+      const int db = BAR_DRAIN + (warp - kQkWarp);
+      if (tc::elect_one()) tc::mma_commit(bar(db));
+      if (!tc::mbar_wait(bar(db), 0, kDrainWaitNs)) atomicOr(p.ws.status, MLA_DEVICE_ERR_TIMEOUT);
       __syncwarp();
     } else {
       // =================== softmax + epilogue (warps 0-7) ===================
@@ -1040,8 +1104,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
           }
           if (g == 0 && lane < 16) alpha_s[h] = alpha;
           if (named_bar_softmax_or(grow)) {
-            // bring O^T (PVs of the previous two pages done: they come from the two PV
-            // warps) to the new maxima (up or down)
+            // bring O^T (PVs of the previous two pages done) to the new maxima (up or down)
             bool got = tc::mbar_wait(bar(BAR_PV_DONE + (j - 1) % kRing), ((j - 1) / kRing) & 1, kWaitNs);
             if (got && j >= 2)
               got = tc::mbar_wait(bar(BAR_PV_DONE + (j - 2) % kRing), ((j - 2) / kRing) & 1, kWaitNs);
@@ -1191,7 +1254,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
   // (the other CTA's copies and commits go to this one's shared memory as long as it works)
   if constexpr (kPair) tc::cluster_sync();
   tc::fence_after_sync();
-  if (warp == kQkWarp0) tc::tmem_dealloc(tmem, kTmemCols);
+  if (warp == kQkWarp) tc::tmem_dealloc(tmem, kTmemCols);
   if (tid == 0) MLA_STAMP(kStExit, 0);
 }
 
@@ -1461,7 +1524,8 @@ cudaError_t launch_decode_fp8(const DecodeLaunch& d, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   if (d.tree_mask != nullptr)
-    return d.e2m1 ? launch_variant<false, true, true>(p, lat_map, rope_map, stream)
+    return d.e2m1 ? (pair ? launch_variant<false, true, true, true>(p, lat_map, rope_map, stream)
+                          : launch_variant<false, true, true>(p, lat_map, rope_map, stream))
            : pair ? launch_variant<false, false, true, true>(p, lat_map, rope_map, stream)
                   : launch_variant<false, false, true>(p, lat_map, rope_map, stream);
   if (d.e2m1)

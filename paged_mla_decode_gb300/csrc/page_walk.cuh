@@ -69,6 +69,12 @@ struct PageWalker {
   __device__ bool piece_end() const { return x + 1 == x_end || x + 1 == cur.rt + cur.t; }
   __device__ int valid_tokens() const { return min(kPageSize, cur.n - page_in_row() * kPageSize); }
   __device__ void next() { ++x; settle(); }
+  // From a piece's first page: how many it has, and on to its last.
+  __device__ int piece_pages() const {
+    const int64_t row_end = cur.rt + cur.t;
+    return (int)((x_end < row_end ? x_end : row_end) - x);
+  }
+  __device__ void to_piece_end(int pages) { x += pages - 1; }
   __device__ bool shared() const { return false; }
 };
 

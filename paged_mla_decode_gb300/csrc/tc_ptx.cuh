@@ -71,6 +71,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t addr, uint32_t parity, uint64
   return mbar_wait_slow(addr, parity, limit_ns);
 }
 
+// True in one thread of a warp whose threads all call it.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one = 0;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n @p mov.u32 %0, 1;\n}\n"
+      : "+r"(one));
+  return one != 0;
+}
+
 // Arrives on the mbarrier and raises its expected transaction bytes (TMA).
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t addr, uint32_t bytes) {
   asm volatile(
@@ -272,6 +281,21 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
   return r;
 }
+// The address, in the cluster's window, of what lies at `addr` of this CTA's in CTA `rank`'s
+// shared memory.
+__device__ __forceinline__ uint32_t cluster_address(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// Bulk copy from this CTA's shared memory to another's (16-byte aligned addresses and size);
+// `dst` and `mbar`, which counts the bytes, are that CTA's cluster_address.
+__device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+      "r"(src), "r"(bytes), "r"(mbar)
+      : "memory");
+}
 // Barrier over all threads of the cluster's CTAs (every path of a kernel that has clusters
 // gets there in bounded time).
 __device__ __forceinline__ void cluster_sync() {
@@ -302,6 +326,13 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
 }
 __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return smem_desc(saddr, lbo, sbo, kSwizzle128);
+}
+
+// `bytes` further (a multiple of 16) in shared memory: only the address in the low word changes.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(d) : "r"((uint32_t)desc + (bytes >> 4)), "r"((uint32_t)(desc >> 32)));
+  return d;
 }
 
 // Instruction descriptor with fp32 accumulation. For kind::f16 the format codes
