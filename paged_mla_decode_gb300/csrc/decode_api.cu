@@ -60,17 +60,17 @@ TreeShape tree_shape(int max_nodes, int num_heads, int num_ctas, bool pairs) {
 }
 // Whether pairs are the faster. An odd number of tiles costs them one that has no rows. Measured
 // in turn, pairs and single CTAs, us a call:
-//   e4m3, even: 8 nodes of 64 heads, 8 sessions of 20k-100k 337, 366; 31 of 32, 32 requests of up
-//     to 4k 255, 322; 16 of 64, one of 100k 181, 185
-//   e4m3, odd: 5 tiles 223, 208; 9: 304, 289; 11: 361, 352; 17: 659, 671; 35: 533, 546
-//   bf16, even: the three of above 668, 695; 305, 333; 349, 346-361
-//   bf16, odd: 5 tiles 440, 386; 11: 728, 690; 17: 1,365, 1,350; 35: 1,082, 1,066
-// 4-bit pages are expanded by each CTA for itself (expanding each half for both took 1.7 times as
-// long).
+//   e4m3, even: 8 nodes of 64 heads, 8 sessions of 20k-100k 330, 374; 31 of 32, 32 requests of up
+//     to 4k 246, 333; 16 of 64, one of 100k 174, 176
+//   e4m3, odd: 5 tiles 212, 204; 9: 288, 277; 11: 343, 337; 17: 626, 646; 35: 509, 526
+//   bf16, even: the three of above 600, 629; 277, 304; 312, 310
+//   bf16, odd: 5 tiles 393, 349; 11: 651, 620; 17: 1,216, 1,219; 35: 966, 960
+// 4-bit pages are expanded by each CTA for itself (pairs that expand half of each page and copy it
+// to each other: 433, 419 without).
 bool tree_by_pairs(int max_nodes, int num_heads, int num_ctas, int kv_dtype) {
   const int tiles = (max_nodes * num_heads + 63) / 64;
-  if (tiles < 2 || num_ctas < 2) return false;
-  return tiles % 2 == 0 || (kv_dtype != MLA_KV_BF16 && tiles >= 13);
+  if (tiles < 2 || num_ctas < 2 || kv_dtype == MLA_KV_E2M1) return false;
+  return tiles % 2 == 0 || (kv_dtype == MLA_KV_E4M3 && tiles >= 13);
 }
 bool tree_shape_ok(int batch, int max_nodes, int num_heads) {
   return batch >= 0 && max_nodes >= 1 && max_nodes <= MLA_MAX_TREE_NODES &&

@@ -91,8 +91,6 @@ constexpr int kQkWarp = kSmWarps + 1;                // 9: also allocates TMEM
 constexpr int kPvWarp = kSmWarps + 2;                // 10
 constexpr int kExpWarp0 = kSmWarps + 3;              // 11: expanders of a 4-bit cache
 constexpr int kExpWarps = 7;
-constexpr int kShares = 9;                           // of a half page, expanded by a pair's CTA
-constexpr uint32_t kShareBytes = 2048;
 constexpr int kPageBytes = kPageSize * kDEntry;      // 36864
 constexpr int kLatBlock = kPageSize * 128;           // 8192: 64 rows x 128 dims
 constexpr int kRopeOff = 4 * kLatBlock;              // rope block within a page slot
@@ -146,7 +144,7 @@ struct Map {
   static constexpr int kOffDesc = kOffPlan + 48;                    // PageDesc [kDescRing]
   static constexpr int kOffBar = kOffDesc + 16 * kDescRing;
   // the page is readable in its ring slot: its TMA bytes landed (or there are none), or
-  // every expander warp has written its part (a pair: its own shares, and the other CTA's bytes)
+  // every expander warp has written its part
   static constexpr int BAR_PAGE_FULL = 0;                 // [kRing]
   // PV(k) completes barrier BAR_PV_DONE + k % kRing (one commit per page): it frees
   // page slot k % kRing for the TMA warp (the expanders), P buffer k % 3 for the softmax
@@ -176,13 +174,13 @@ struct Map {
   static constexpr int kNumBars = BAR_FREE + kRing;
 #endif
   // arrivals that complete a phase of barrier i
-  static __device__ __forceinline__ uint32_t bar_count(int i, bool pair) {
+  static __device__ __forceinline__ uint32_t bar_count(int i) {
     if ((i >= BAR_S_EMPTY && i < BAR_S_EMPTY + 2) || (i >= BAR_P_FULL && i < BAR_P_FULL + kPBufs) ||
         i == BAR_O_EMPTY || i == BAR_Q_READY)
       return kSmWarps;
     if (i >= BAR_FREE && i < BAR_FREE + kRing) return 2;  // both CTAs' commits
     if (kE2m1 && (i < kRing || (i >= BAR_RAW_EMPTY && i < BAR_RAW_EMPTY + kRawRing)))
-      return pair ? kShares : kExpWarps;
+      return kExpWarps;
     return 1;
   }
   static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
@@ -395,35 +393,6 @@ __device__ __forceinline__ void expand_page(const Expander& x, uint32_t raw, uin
   }
 }
 
-// A pair's CTAs expand half of a page each and copy it to each other: CTA `half` blocks
-// 8 * half .. + 7 and the rope blocks of tokens 32 * half .. + 31. A share is what lies together
-// in the page: four blocks of 16 tokens (shares 0-7) or the rope's two of 32 (share 8).
-__device__ __forceinline__ uint32_t share_offset(uint32_t share, int half) {
-  return share < 8 ? (2 * half + (share >> 2)) * kLatBlock + (share & 3) * kShareBytes
-                   : kRopeOff + half * kShareBytes;
-}
-__device__ __forceinline__ void expand_share(uint32_t share, int half, int lane, uint32_t raw,
-                                             uint32_t page, uint32_t lut) {
-  const bool rope = share == 8;
-  const int token = rope ? 32 * half + lane : 16 * (int)(share & 3) + (lane & 15);
-  const int block = rope ? 16 : 4 * (2 * half + (int)(share >> 2)) + (lane >> 4);  // and + step
-  const int step = rope ? 1 : 2;
-  uint32_t n[2];  // the blocks' nibbles, at bit 3
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int b = block + step * k;
-    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(n[k]) : "r"(raw + e2m1_exp_offset(b, token)));
-    n[k] = (b & 1) ? n[k] >> 1 : n[k] << 3;
-  }
-  ExpandUnit x[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) expand_load(x[k], raw + e2m1_code_offset(block + step * k, token), lut, n[k]);
-  const uint32_t sw = (rope ? (token >> 1) & 3 : token & 7) << 4;
-  const uint32_t row = page + token * (rope ? 64 : 128) + (block / 4) * kLatBlock;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) expand_write(x[k], row + (((32u * (block + step * k)) & 96u) ^ sw));
-}
-
 // Whether one of four e4m3 codes is a NaN (0x7f, 0xff).
 __device__ __forceinline__ bool e4m3x4_has_nan(uint32_t w) {
   return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
@@ -494,7 +463,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
   // itself needs the split kernel to have completed (griddep_wait before q_op).
   using RowPlan = std::conditional_t<kTree, TreePlan, Plan>;
   RowPlan plan = row_plan<RowPlan>(p);
-  static_assert(!kPair || kTree, "pairs are the tree decode's");
+  static_assert(!kPair || (kTree && !kE2m1), "pairs are the tree decode's, over e4m3 pages");
   const int c = kPair ? blockIdx.x >> 1 : blockIdx.x;
   const int half = kPair ? (int)tc::cluster_rank() : 0;  // of the tile's rows
   constexpr uint16_t kBoth = 3;
@@ -542,7 +511,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
       tc::prefetch_tensormap(&lat_map);
       tc::prefetch_tensormap(&rope_map);
     }
-    for (int i = 0; i < M::kNumBars; ++i) tc::mbar_init(bar(i), M::bar_count(i, kPair));
+    for (int i = 0; i < M::kNumBars; ++i) tc::mbar_init(bar(i), M::bar_count(i));
     tc::fence_mbar_init();
     flags[F_ABORT] = 0;
     flags[F_PIECE_BAD] = 0;
@@ -714,12 +683,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
         for (int64_t jj = j > kLanding ? j - kLanding : 0; jj < j; ++jj)
           tc::mbar_wait(bar(kLandBar + (int)(jj % kLanding)), (uint32_t)(jj / kLanding) & 1,
                         kDrainWaitNs);
-        // nor may the other CTA's copies and commits arrive here after that
-        if constexpr (kPair && kE2m1) {
-          for (int64_t jj = j > kRing ? j - kRing : 0; jj < j; ++jj)
-            if (!tc::mbar_wait(bar(BAR_PAGE_FULL + (int)(jj % kRing)), (uint32_t)(jj / kRing) & 1, kDrainWaitNs))
-              break;
-        }
+        // nor may the other CTA's commits arrive here after that
         if constexpr (kPair) {
           for (int64_t jj = j > kRing ? j - kRing : 0; jj < j; ++jj)
             tc::mbar_wait(bar(M::BAR_FREE + (int)(jj % kRing)), (uint32_t)(jj / kRing) & 1, kDrainWaitNs);
@@ -728,39 +692,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
       __syncwarp();
     } else if (kE2m1 && warp >= kExpWarp0) {
       // =================== expanders of a 4-bit cache (7 warps) ===================
-      if constexpr (kE2m1 && kPair) {
-        // the shares of all pages' halves go round the warps
-        bool ok = true;
-        const uint32_t lut = sbase + M::kOffLut;
-        const uint32_t shares = (uint32_t)npages * kShares;
-        for (uint32_t u = warp - kExpWarp0; u < shares; u += kExpWarps) {
-          const uint32_t j = u / kShares, rs = j % M::kRawRing, slot = j % kRing;
-          ok = tc::mbar_wait(bar(M::BAR_RAW_FULL + rs), (j / M::kRawRing) & 1, kWaitNs);
-          // both CTAs' PVs have read the page that held the slot
-          if (ok && j >= kRing) ok = tc::mbar_wait(bar(M::BAR_FREE + slot), (j / kRing - 1) & 1, kWaitNs);
-          ok = __all_sync(0xffffffffu, ok && !flags[F_ABORT]);
-          if (!ok) break;
-          const bool page_ok = desc[j % kDescRing].flags & kDescPageOk;
-          const uint32_t page = sbase + kOffPages + slot * kPageBytes;
-          const uint32_t share = page + share_offset(u - j * kShares, half);
-          if (page_ok)
-            expand_share(u - j * kShares, half, lane, sbase + M::kOffRaw + rs * kE2m1PageBytes, page, lut);
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (page_ok) {
-              // (as many bytes come from the other CTA)
-              tc::mbar_arrive_expect_tx(bar(BAR_PAGE_FULL + slot), kShareBytes);
-              tc::bulk_copy_to_cta(tc::cluster_address(share, 1 - half), share, kShareBytes,
-                                   tc::cluster_address(bar(BAR_PAGE_FULL + slot), 1 - half));
-            } else {
-              tc::mbar_arrive(bar(BAR_PAGE_FULL + slot));
-            }
-            tc::mbar_arrive(bar(M::BAR_RAW_EMPTY + rs));
-          }
-        }
-        if (!ok && lane == 0) abort_cta();
-      } else if constexpr (kE2m1) {
+      if constexpr (kE2m1) {
         bool ok = true;
         const Expander x = expander<M>(warp - kExpWarp0, lane);
         const uint32_t lut = sbase + M::kOffLut;
@@ -1524,8 +1456,7 @@ cudaError_t launch_decode_fp8(const DecodeLaunch& d, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   if (d.tree_mask != nullptr)
-    return d.e2m1 ? (pair ? launch_variant<false, true, true, true>(p, lat_map, rope_map, stream)
-                          : launch_variant<false, true, true>(p, lat_map, rope_map, stream))
+    return d.e2m1 ? launch_variant<false, true, true>(p, lat_map, rope_map, stream)
            : pair ? launch_variant<false, false, true, true>(p, lat_map, rope_map, stream)
                   : launch_variant<false, false, true>(p, lat_map, rope_map, stream);
   if (d.e2m1)

@@ -281,21 +281,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
   return r;
 }
-// The address, in the cluster's window, of what lies at `addr` of this CTA's in CTA `rank`'s
-// shared memory.
-__device__ __forceinline__ uint32_t cluster_address(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-// Bulk copy from this CTA's shared memory to another's (16-byte aligned addresses and size);
-// `dst` and `mbar`, which counts the bytes, are that CTA's cluster_address.
-__device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t mbar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
-      "r"(src), "r"(bytes), "r"(mbar)
-      : "memory");
-}
 // Barrier over all threads of the cluster's CTAs (every path of a kernel that has clusters
 // gets there in bounded time).
 __device__ __forceinline__ void cluster_sync() {
