@@ -94,9 +94,11 @@ __device__ __forceinline__ void merge_row(const float* __restrict__ out_base, in
 // (row, head) each: a block would spend its barriers and its staging on a few pieces there. The grid
 // then starts with the blocks of the rows of many pieces; each looks for its row in the
 // row table and leaves if there is none. A decode call of 256 rows of 8 pages, 64 heads,
-// takes 84 us, with a block per unit throughout 178; 48 rows of one page 28 and 42; one
-// row of 100k tokens among 31 of one page 101 and 110. For the few rows the first kernel
-// stays: it has 32 registers a thread, the second 52 (8 rows of 20k tokens 47 us, 53).
+// takes 74 us (84 when a warp took a quarter of the dims and 178 with a block per unit
+// throughout, both beside an earlier decode kernel); 48 rows of one page 21 (28, 42); one
+// row of 100k tokens among 31 of one page 91 (101, 110). A tree decode's 32 x 992 rows
+// merge in 25 us by a warp a row, 48 by a warp a quarter. For the few rows the first kernel
+// stays: it has 40 registers a thread, the second 72.
 constexpr int kFewPieces = 16;
 constexpr int kWarpMergeLoads = 2;  // pieces whose loads are in flight (each all four quarters)
 

@@ -298,14 +298,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         cp_async_wait<0>();
         if (!ok) abort_cta();
         // no copy may land after the CTA exits: wait for the last issued pages and query
+        // (a wait that runs out, after a stop of a pair's other CTA, has been long enough for all)
+        bool landed = true;
         for (int64_t jj = j > kSlots ? j - kSlots : 0; jj < j; ++jj)
           for (int g = 0; g < kGroups; ++g)
-            tc::mbar_wait(bar(BAR_PAGE_FULL + kGroups * (int)(jj % kSlots) + g), (uint32_t)(jj / kSlots) & 1, kWaitNs);
+            landed = landed && tc::mbar_wait(bar(BAR_PAGE_FULL + kGroups * (int)(jj % kSlots) + g),
+                                             (uint32_t)(jj / kSlots) & 1, kWaitNs);
         if (piece > 0) tc::mbar_wait(bar(BAR_Q_FULL), (uint32_t)(piece - 1) & 1, kWaitNs);
         // nor may the other CTA's commits arrive here after that
         if constexpr (kPair) {
           for (int64_t jj = j > kSlots ? j - kSlots : 0; jj < j; ++jj)
-            tc::mbar_wait(bar(BAR_FREE + (int)(jj % kSlots)), (uint32_t)(jj / kSlots) & 1, kWaitNs);
+            if (!tc::mbar_wait(bar(BAR_FREE + (int)(jj % kSlots)), (uint32_t)(jj / kSlots) & 1, kWaitNs))
+              break;
         }
       }
       __syncwarp();

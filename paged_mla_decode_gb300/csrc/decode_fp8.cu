@@ -677,16 +677,19 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
         }
         cp_async_wait<0>();
         if (!ok) abort_cta();
-        // no copy may land after the CTA exits: wait for the last issued pages
+        // no copy may land after the CTA exits: wait for the last issued pages (a wait that runs
+        // out, after a stop of a pair's other CTA, has been long enough for all of them)
         constexpr int kLanding = kE2m1 ? M::kRawRing : kRing;
         constexpr int kLandBar = kE2m1 ? M::BAR_RAW_FULL : BAR_PAGE_FULL;
         for (int64_t jj = j > kLanding ? j - kLanding : 0; jj < j; ++jj)
-          tc::mbar_wait(bar(kLandBar + (int)(jj % kLanding)), (uint32_t)(jj / kLanding) & 1,
-                        kDrainWaitNs);
+          if (!tc::mbar_wait(bar(kLandBar + (int)(jj % kLanding)), (uint32_t)(jj / kLanding) & 1,
+                             kDrainWaitNs))
+            break;
         // nor may the other CTA's commits arrive here after that
         if constexpr (kPair) {
           for (int64_t jj = j > kRing ? j - kRing : 0; jj < j; ++jj)
-            tc::mbar_wait(bar(M::BAR_FREE + (int)(jj % kRing)), (uint32_t)(jj / kRing) & 1, kDrainWaitNs);
+            if (!tc::mbar_wait(bar(M::BAR_FREE + (int)(jj % kRing)), (uint32_t)(jj / kRing) & 1, kDrainWaitNs))
+              break;
         }
       }
       __syncwarp();

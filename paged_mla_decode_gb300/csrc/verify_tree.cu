@@ -19,8 +19,8 @@
 // compares in double, where u q is exact.
 //
 // A rejection's pass reads p and q of one node, a float each a token, and the next one cannot
-// begin before it: 64 requests of up to 16 nodes over 163,840 tokens take 37 us, 2.7 passes a
-// request on average, of 84 MB for all of them; one request over 131,072 tokens 10 us, latency.
+// begin before it: 64 requests of up to 16 nodes over 163,840 tokens take 37 us for the 157 MB
+// that their passes read one after the other; one request over 131,072 tokens 10 us, latency.
 //
 // A request is worked by a cluster of up to eight blocks, each summing a run of the
 // vocabulary. Every block walks the tree by itself, from the same numbers: the probabilities
