@@ -63,14 +63,14 @@ TreeShape tree_shape(int max_nodes, int num_heads, int num_ctas, bool pairs) {
 //   e4m3, even: 8 nodes of 64 heads, 8 sessions of 20k-100k 330, 374; 31 of 32, 32 requests of up
 //     to 4k 246, 333; 16 of 64, one of 100k 174, 176
 //   e4m3, odd: 5 tiles 212, 204; 9: 288, 277; 11: 343, 337; 17: 626, 646; 35: 509, 526
-//   bf16, even: the three of above 600, 629; 277, 304; 312, 310
-//   bf16, odd: 5 tiles 393, 349; 11: 651, 620; 17: 1,216, 1,219; 35: 966, 960
+//   bf16, even: the three of above 562, 612; 270, 298; 294, 293
+//   bf16, odd: 5 tiles 370, 339; 9: 512, 482; 11: 609, 600; 17: 1,133, 1,188; 35: 901, 909
 // 4-bit pages are expanded by each CTA for itself (pairs that expand half of each page and copy it
 // to each other: 433, 419 without).
 bool tree_by_pairs(int max_nodes, int num_heads, int num_ctas, int kv_dtype) {
   const int tiles = (max_nodes * num_heads + 63) / 64;
   if (tiles < 2 || num_ctas < 2 || kv_dtype == MLA_KV_E2M1) return false;
-  return tiles % 2 == 0 || (kv_dtype == MLA_KV_E4M3 && tiles >= 13);
+  return tiles % 2 == 0 || tiles >= 13;
 }
 bool tree_shape_ok(int batch, int max_nodes, int num_heads) {
   return batch >= 0 && max_nodes >= 1 && max_nodes <= MLA_MAX_TREE_NODES &&

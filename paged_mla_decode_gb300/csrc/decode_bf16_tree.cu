@@ -12,9 +12,11 @@
 // A page is 73,728 bytes and the tile's query as many, so two pages fit beside it, and P
 // (bf16, 8 KB) takes the place of its own page's rotary chunk, which QK has read by then.
 // That bounds it: copy, QK, softmax and PV of a page follow each other in its slot. 16 sessions
-// of 32k-140k tokens, 12 nodes of 64 heads: 1.75 us a page and SM, 770 TFLOP/s; 32 requests of
-// up to 4k, 31 nodes of 32 heads: 2.5 us, 515. QK starts on the first third of a page, and L2 is
-// asked for pages four ahead (200 us, now 198, when the issue of MMAs took longer).
+// of 32k-140k tokens, 12 nodes of 64 heads: 1.64 us a page and SM, 830 TFLOP/s; 32 requests of
+// up to 4k, 31 nodes of 32 heads: 2.4 us, 530. So QK starts on the first third of a page (200 us
+// for such 32 requests, 198 with it, when the issue of MMAs took longer), a third of the next page
+// comes as soon as PV has passed the one in its place (3,157 us, 2,961 with it, for the 16
+// sessions; five groups instead of three 4,479), and L2 is asked for pages four ahead.
 // P = 2^(s - m) with m a running maximum that rises when a page's lies more than 2^7 above it:
 // bf16 has float's range, so P of a page far below m keeps its 8 bits (each rounded once,
 // 2^-8 of itself at most; the normaliser sums the exact P).
@@ -82,8 +84,9 @@ enum Bar {
   BAR_Q_FULL = BAR_O_EMPTY + 1,       // the query tile's bytes landed
   BAR_Q_EMPTY = BAR_Q_FULL + 1,       // QK of the piece's last page is done
   BAR_DRAIN = BAR_Q_EMPTY + 1,        // [2] one per issuer warp
-  BAR_FREE = BAR_DRAIN + 2,           // [2] pairs: both CTAs' PVs have read the page in the slot
-  kNumBars = BAR_FREE + 2
+  // [2][kGroups] the page's PV (a pair: both CTAs') has read the third in the slot
+  BAR_FREE = BAR_DRAIN + 2,
+  kNumBars = BAR_FREE + 2 * kGroups
 };
 constexpr int kOffTmem = kOffBar + 8 * kNumBars;
 constexpr int kSmemBytes = kOffTmem + 16 + 1024;  // slack for the 1024 alignment
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::prefetch_tensormap(&q_map);
     for (int i = 0; i < kNumBars; ++i) {
       const bool by_softmax = (i >= BAR_S_EMPTY && i < BAR_P_FULL + 2) || i == BAR_O_EMPTY;
-      tc::mbar_init(bar(i), by_softmax ? kSmWarps : i >= BAR_FREE ? 2 : 1);
+      tc::mbar_init(bar(i), by_softmax ? kSmWarps : kPair && i >= BAR_FREE ? 2 : 1);
     }
     tc::fence_mbar_init();
     flags[F_ABORT] = 0;
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (pages whose ids are waited for at page j: it and those that L2 is asked for)
         while (jn <= kPrefetch && jn < npages) describe_next();
         int64_t j = 0, asked = 0;
-        int piece = 0;
+        int piece = 0, part = 0;  // thirds of page j that are on their way
         bool ok = true;
         for (; j < npages; ++j) {
           cp_async_wait_upto<kTableAhead>((int)max(jn - j - 1 - kPrefetch, (int64_t)0));
@@ -269,30 +272,32 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::tma_load_2d(sbase + kOffQ + ch * kChunkBytes, &q_map, 64 * ch, y, bar(BAR_Q_FULL));
           }
           const int slot = (int)(j % kSlots);
-          if (j >= kSlots &&
-              (!tc::mbar_wait(bar((kPair ? BAR_FREE : BAR_PV_DONE) + slot), (uint32_t)(j / kSlots - 1) & 1, kWaitNs) ||
-               flags[F_ABORT])) {
-            ok = false;
-            break;
-          }
-          if (page_ok) {
-            for (int g = 0; g < kGroups; ++g)
-              tc::mbar_arrive_expect_tx(bar(BAR_PAGE_FULL + kGroups * slot + g), (uint32_t)(kPageBytes / kGroups));
+          for (int g = 0; g < kGroups && ok; ++g) {  // a third at a time, as it becomes free
+            const uint32_t full = bar(BAR_PAGE_FULL + kGroups * slot + g);
+            if (j >= kSlots && (!tc::mbar_wait(bar(BAR_FREE + kGroups * slot + g), (uint32_t)(j / kSlots - 1) & 1, kWaitNs) ||
+                                flags[F_ABORT])) {
+              ok = false;
+              break;
+            }
+            ++part;
+            if (!page_ok) {  // no copy; every token of the page is masked, its value rows zeroed
+              tc::mbar_arrive(full);
+              continue;
+            }
+            tc::mbar_arrive_expect_tx(full, (uint32_t)(kPageBytes / kGroups));
             const uint32_t to = sbase + slot * kPageBytes;
             const int y = d->page * kPageSize;
-            if constexpr (kPair) {  // every other chunk; the other half's bytes count here too
-              for (int ch = half; ch < kChunks; ch += 2)
-                tc::tma_load_2d_multicast_hint(to + ch * kChunkBytes, &kv_map, 64 * ch, y,
-                                               bar(BAR_PAGE_FULL + kGroups * slot + ch / 3), kBoth, pol);
-            } else {
-              for (int ch = 0; ch < kChunks; ++ch)
-                tc::tma_load_2d_hint(to + ch * kChunkBytes, &kv_map, 64 * ch, y,
-                                     bar(BAR_PAGE_FULL + kGroups * slot + ch / 3), pol);
+            for (int ch = 3 * g; ch < 3 * g + 3; ++ch) {
+              if constexpr (kPair) {  // every other chunk; the other half's bytes count here too
+                if ((ch & 1) == half)
+                  tc::tma_load_2d_multicast_hint(to + ch * kChunkBytes, &kv_map, 64 * ch, y, full, kBoth, pol);
+              } else {
+                tc::tma_load_2d_hint(to + ch * kChunkBytes, &kv_map, 64 * ch, y, full, pol);
+              }
             }
-          } else {
-            // bad id: no copy; every token of the page is masked, its value rows zeroed
-            for (int g = 0; g < kGroups; ++g) tc::mbar_arrive(bar(BAR_PAGE_FULL + kGroups * slot + g));
           }
+          if (!ok) break;
+          part = 0;
           for (int u = 0; u < 2 && jn < npages && jn <= j + kTableAhead; ++u) describe_next();
         }
         cp_async_wait<0>();
@@ -304,11 +309,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int g = 0; g < kGroups; ++g)
             landed = landed && tc::mbar_wait(bar(BAR_PAGE_FULL + kGroups * (int)(jj % kSlots) + g),
                                              (uint32_t)(jj / kSlots) & 1, kWaitNs);
+        for (int g = 0; g < part; ++g)
+          landed = landed && tc::mbar_wait(bar(BAR_PAGE_FULL + kGroups * (int)(j % kSlots) + g),
+                                           (uint32_t)(j / kSlots) & 1, kWaitNs);
         if (piece > 0) tc::mbar_wait(bar(BAR_Q_FULL), (uint32_t)(piece - 1) & 1, kWaitNs);
         // nor may the other CTA's commits arrive here after that
         if constexpr (kPair) {
           for (int64_t jj = j > kSlots ? j - kSlots : 0; jj < j; ++jj)
-            if (!tc::mbar_wait(bar(BAR_FREE + (int)(jj % kSlots)), (uint32_t)(jj / kSlots) & 1, kWaitNs))
+            if (!tc::mbar_wait(bar(BAR_FREE + kGroups * (int)(jj % kSlots) + kGroups - 1), (uint32_t)(jj / kSlots) & 1, kWaitNs))
               break;
         }
       }
@@ -372,13 +380,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t pb = tc::smem_desc_sw128(page + (kChunks - 1) * kChunkBytes, 16, 1024);
           if (tc::elect_one()) {
 #pragma unroll
-            for (int blk = 0; blk < 4; ++blk)
+            for (int blk = 0; blk < 4; ++blk) {  // (two chunks a block: chunks 3g .. 3g + 2 are read by g + 2 of them)
 #pragma unroll
               for (int s = 0; s < 4; ++s)
                 tc::mma_f16_ss(tmem + kOCol + 64 * blk, tc::desc_at(va, 2 * blk * kChunkBytes + s * 2048),
                                tc::desc_at(pb, 32 * s), id_pv, 1);
+              if (blk == 0) continue;
+              const uint32_t free = bar(BAR_FREE + kGroups * slot + blk - 1);
+              if constexpr (kPair) tc::mma_commit_multicast(free, kBoth);
+              else tc::mma_commit(free);
+            }
             tc::mma_commit(bar(BAR_PV_DONE + slot));
-            if constexpr (kPair) tc::mma_commit_multicast(bar(BAR_FREE + slot), kBoth);
             if (left == 1) tc::mma_commit(bar(BAR_O_FULL));
           }
         }
