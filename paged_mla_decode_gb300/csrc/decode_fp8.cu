@@ -26,8 +26,8 @@
 // smaller ring as stored, seven expander warps rewrite each as the swizzled e4m3 page
 // that the contractions read (a table lookup, exact), and everything after that is
 // the e4m3 kernel. It trades one ring slot for the raw pages (kRing 4 + 2 raw). 31
-// requests of 60k-140k tokens with 64 heads (307 pages a CTA) take 382 us, 327 from an
-// e4m3 cache. The difference is the expansion: without it (a probe) the kernels are even,
+// requests of 60k-140k tokens with 64 heads (307 pages a CTA) took 382 us, 327 from an
+// e4m3 cache (377 now, with whole warps that issue MMAs). The difference is the expansion: without it (a probe) the kernels are even,
 // whether the pages come from L2 or not. Its 1,900 cycles a page run beside a softmax that
 // takes some 1,900 itself, on the same schedulers and the same integer pipe (61% busy),
 // with shared memory at three quarters of its rate: a page's MMAs read 140 KB of operands
