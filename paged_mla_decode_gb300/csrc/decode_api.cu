@@ -47,30 +47,13 @@ extern "C" size_t mla_decode_grouped_workspace_size(int batch, int num_queries, 
 }
 
 namespace {
-// The query rows of a tree decode's requests, as TreePlan cuts them, and its workers: CTAs with
-// a tile of up to 64 rows each, or pairs of CTAs with 128.
+// The query rows of a tree decode's requests, as TreePlan cuts them.
 struct TreeShape {
-  int tiles, tile_rows, workers;
+  int tiles, tile_rows;
 };
-TreeShape tree_shape(int max_nodes, int num_heads, int num_ctas, bool pairs) {
+TreeShape tree_shape(int max_nodes, int num_heads) {
   const int rows = max_nodes * num_heads;
-  if (rows <= 64) return TreeShape{1, rows, num_ctas};
-  const int tiles = (rows + 63) / 64;
-  return pairs ? TreeShape{(tiles + 1) / 2, 128, num_ctas / 2} : TreeShape{tiles, 64, num_ctas};
-}
-// Whether pairs are the faster. An odd number of tiles costs them one that has no rows. Measured
-// in turn, pairs and single CTAs, us a call:
-//   e4m3, even: 8 nodes of 64 heads, 8 sessions of 20k-100k 330, 374; 31 of 32, 32 requests of up
-//     to 4k 246, 333; 16 of 64, one of 100k 174, 176
-//   e4m3, odd: 5 tiles 212, 204; 9: 288, 277; 11: 343, 337; 17: 626, 646; 35: 509, 526
-//   bf16, even: the three of above 562, 612; 270, 298; 294, 293
-//   bf16, odd: 5 tiles 370, 339; 9: 512, 482; 11: 609, 600; 17: 1,133, 1,188; 35: 901, 909
-// 4-bit pages are expanded by each CTA for itself (pairs that expand half of each page and copy it
-// to each other: 433, 419 without).
-bool tree_by_pairs(int max_nodes, int num_heads, int num_ctas, int kv_dtype) {
-  const int tiles = (max_nodes * num_heads + 63) / 64;
-  if (tiles < 2 || num_ctas < 2 || kv_dtype == MLA_KV_E2M1) return false;
-  return tiles % 2 == 0 || tiles >= 13;
+  return rows <= 64 ? TreeShape{1, rows} : TreeShape{(rows + 63) / 64, 64};
 }
 bool tree_shape_ok(int batch, int max_nodes, int num_heads) {
   return batch >= 0 && max_nodes >= 1 && max_nodes <= MLA_MAX_TREE_NODES &&
@@ -200,14 +183,8 @@ extern "C" size_t mla_decode_tree_workspace_size(int batch, int max_nodes, int n
   if (!tree_shape_ok(batch, max_nodes, num_heads) || num_ctas < 0) return 0;
   if (num_ctas == 0) num_ctas = mla::device_sm_count();
   if (num_ctas <= 0) return 0;
-  size_t most = 0;  // (the cache's type is not known here)
-  for (const bool pairs : {false, true}) {
-    if (pairs && num_ctas < 2) break;
-    const TreeShape t = tree_shape(max_nodes, num_heads, num_ctas, pairs);
-    const size_t n = mla::workspace_layout((int64_t)batch * t.tiles, t.tile_rows, t.workers).total;
-    most = n > most ? n : most;
-  }
-  return most;
+  const TreeShape t = tree_shape(max_nodes, num_heads);
+  return mla::workspace_layout((int64_t)batch * t.tiles, t.tile_rows, num_ctas).total;
 }
 
 extern "C" mla_status mla_decode_tree(const void* q, const void* kv_pages, int64_t num_pages,
@@ -238,10 +215,10 @@ extern "C" mla_status mla_decode_tree(const void* q, const void* kv_pages, int64
   if ((int64_t)batch * max_pages > 0x7fffffffLL) return MLA_ERR_UNSUPPORTED;
   const int G = num_ctas ? num_ctas : device_sm_count();
   if (G <= 0) return MLA_ERR_CUDA;
-  const TreeShape t = tree_shape(max_nodes, num_heads, G, tree_by_pairs(max_nodes, num_heads, G, kv_dtype));
+  const TreeShape t = tree_shape(max_nodes, num_heads);
   const int64_t rows = (int64_t)batch * t.tiles;
   if (rows * t.tile_rows > 0x7fffffffLL) return MLA_ERR_UNSUPPORTED;
-  const WorkspaceLayout L = workspace_layout(rows, t.tile_rows, t.workers);
+  const WorkspaceLayout L = workspace_layout(rows, t.tile_rows, G);
   if (workspace_bytes < L.total) return MLA_ERR_WORKSPACE;
 
   DecodeLaunch p;
@@ -258,7 +235,7 @@ extern "C" mla_status mla_decode_tree(const void* q, const void* kv_pages, int64
   p.e2m1 = kv_dtype == MLA_KV_E2M1;
   p.score_mul = sm_scale * kLog2e * kv_scale;
   p.kv_scale = kv_scale;
-  p.G = t.workers;
+  p.G = G;
   carve_workspace(p.ws, workspace, L);
   p.tree_mask = tree_mask;
   p.num_nodes = num_nodes;
@@ -269,7 +246,7 @@ extern "C" mla_status mla_decode_tree(const void* q, const void* kv_pages, int64
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = p.bf16 ? launch_decode_bf16_tree(p, s) : launch_decode_fp8(p, s);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
-  e = launch_combine_pieces(p.ws, (int)rows, t.tile_rows, 1, t.workers,
+  e = launch_combine_pieces(p.ws, (int)rows, t.tile_rows, 1, G,
                             static_cast<__nv_bfloat16*>(out), lse, s, t.tiles, p.query_rows());
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

@@ -12,11 +12,11 @@
 // A page is 73,728 bytes and the tile's query as many, so two pages fit beside it, and P
 // (bf16, 8 KB) takes the place of its own page's rotary chunk, which QK has read by then.
 // That bounds it: copy, QK, softmax and PV of a page follow each other in its slot. 16 sessions
-// of 32k-140k tokens, 12 nodes of 64 heads: 1.64 us a page and SM, 830 TFLOP/s; 32 requests of
-// up to 4k, 31 nodes of 32 heads: 2.4 us, 530. So QK starts on the first third of a page (200 us
-// for such 32 requests, 198 with it, when the issue of MMAs took longer), a third of the next page
-// comes as soon as PV has passed the one in its place (3,157 us, 2,961 with it, for the 16
-// sessions; five groups instead of three 4,479), and L2 is asked for pages four ahead.
+// of 32k-140k tokens, 12 nodes of 64 heads: a call of 3,248 us, 1.8 us a page and SM, 756
+// TFLOP/s; 32 requests of up to 4k, 31 nodes of 32 heads: 300 us, 477. So QK starts on the first
+// third of a page (1% of such 32 requests, when the issue of MMAs took longer), a third of the next
+// page comes as soon as PV has passed the one in its place (6% of the 16 sessions; five groups
+// instead of three cost them 50%), and L2 is asked for pages four ahead.
 // P = 2^(s - m) with m a running maximum that rises when a page's lies more than 2^7 above it:
 // bf16 has float's range, so P of a page far below m keeps its 8 bits (each rounded once,
 // 2^-8 of itself at most; the normaliser sums the exact P).
@@ -84,7 +84,7 @@ enum Bar {
   BAR_Q_FULL = BAR_O_EMPTY + 1,       // the query tile's bytes landed
   BAR_Q_EMPTY = BAR_Q_FULL + 1,       // QK of the piece's last page is done
   BAR_DRAIN = BAR_Q_EMPTY + 1,        // [2] one per issuer warp
-  // [2][kGroups] the page's PV (a pair: both CTAs') has read the third in the slot
+  // [2][kGroups] the page's PV has read the third in the slot
   BAR_FREE = BAR_DRAIN + 2,
   kNumBars = BAR_FREE + 2 * kGroups
 };
@@ -133,9 +133,6 @@ __device__ __forceinline__ bool bf16x2_not_finite(uint32_t w) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-// kPair: two CTAs of a cluster walk the same pages for the two halves of a 128-row tile, each
-// bringing half of every page into both CTAs' shared memory (as in decode_fp8.cu).
-template <bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_bf16_tree_kernel(const Bf16TreeParams p, const __grid_constant__ CUtensorMap kv_map,
                             const __grid_constant__ CUtensorMap q_map) {
@@ -154,9 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (the compiler sees that it is a warp's)
-  const int c = kPair ? blockIdx.x >> 1 : blockIdx.x;
-  const int half = kPair ? (int)tc::cluster_rank() : 0;  // of the tile's rows
-  constexpr uint16_t kBoth = 3;
+  const int c = blockIdx.x;
   griddep_wait();  // all earlier work in the stream is complete
   TreePlan plan{p.seq_lens, p.num_nodes, p.batch, p.max_nodes, p.node_heads, p.tiles, p.tile_rows,
                 p.max_pages, kPageSize, p.G, 0};
@@ -164,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     TreePlan pl = plan;
     pl.set_total(plan_total_tiles_warp(pl));
     const int64_t xb = c < pl.G ? pl.cta_start(c) : 0;
-    const RowCursor f = plan_find_row_warp(pl, xb, c == 0 && half == 0, p.ws.row_base, p.ws.row_np, p.ws.status);
+    const RowCursor f = plan_find_row_warp(pl, xb, c == 0, p.ws.row_base, p.ws.row_np, p.ws.status);
     if (lane == 0) {
       s_plan[0] = pl.T;
       s_plan[1] = f.r;
@@ -179,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::prefetch_tensormap(&q_map);
     for (int i = 0; i < kNumBars; ++i) {
       const bool by_softmax = (i >= BAR_S_EMPTY && i < BAR_P_FULL + 2) || i == BAR_O_EMPTY;
-      tc::mbar_init(bar(i), by_softmax ? kSmWarps : kPair && i >= BAR_FREE ? 2 : 1);
+      tc::mbar_init(bar(i), by_softmax ? kSmWarps : 1);
     }
     tc::fence_mbar_init();
     flags[F_ABORT] = 0;
@@ -190,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_relinquish();
   }
   // rows that TMA does not write (a request of fewer than 64) are zeros
-  if (!kPair && p.tile_rows < kTileRows) {
+  if (p.tile_rows < kTileRows) {
     const int units = (kTileRows - p.tile_rows) * 8;  // 16-byte pieces of a chunk
     for (int i = tid; i < kChunks * units; i += kThreads) {
       const int ch = i / units, u = i - ch * units;
@@ -202,7 +197,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if constexpr (kPair) tc::cluster_sync();  // both CTAs' barriers are there
   tc::fence_after_sync();
   griddep_launch_dependents();  // the merge may be scheduled (it waits for this grid)
   plan.set_total(s_plan[0]);
@@ -210,8 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t x_begin = works ? plan.cta_start(c) : 0, x_end = works ? plan.cta_start(c + 1) : 0;
   const uint32_t tmem = *tmem_slot;
   const RowCursor cur0{(int)s_plan[1], s_plan[2], (int)s_plan[3], (int)s_plan[4], (int)s_plan[5]};
-  const int H = kPair ? kTileRows : p.tile_rows;  // rows of this CTA
-  const int row_step = kPair ? 2 * H : H, row0 = H * half;  // in a piece's partials
+  const int H = p.tile_rows;
   auto abort_cta = [&]() {
     flags[F_ABORT] = 1;
     atomicOr(p.ws.status, MLA_DEVICE_ERR_TIMEOUT);
@@ -251,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           PageDesc* d = ring + j % kDescRing;
           for (; asked < jn && asked <= j + kPrefetch; ++asked) {
             const int32_t ahead = ring[asked % kDescRing].page;
-            if (asked >= j + kSlots && half == 0 && ahead >= 0 && (int64_t)ahead < p.num_pages)
+            if (asked >= j + kSlots && ahead >= 0 && (int64_t)ahead < p.num_pages)
               tc::prefetch_l2_bulk(p.kv + (int64_t)ahead * kPageBytes, (uint32_t)kPageBytes);
           }
           const bool page_ok = d->page >= 0 && (int64_t)d->page < p.num_pages;
@@ -266,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++piece;
             const int b = d->row / p.tiles;
-            const int y = b * p.query_rows + (d->row - b * p.tiles) * row_step + row0;
+            const int y = b * p.query_rows + (d->row - b * p.tiles) * H;
             tc::mbar_arrive_expect_tx(bar(BAR_Q_FULL), (uint32_t)(kChunks * H * 128));
             for (int ch = 0; ch < kChunks; ++ch)
               tc::tma_load_2d(sbase + kOffQ + ch * kChunkBytes, &q_map, 64 * ch, y, bar(BAR_Q_FULL));
@@ -287,14 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_arrive_expect_tx(full, (uint32_t)(kPageBytes / kGroups));
             const uint32_t to = sbase + slot * kPageBytes;
             const int y = d->page * kPageSize;
-            for (int ch = 3 * g; ch < 3 * g + 3; ++ch) {
-              if constexpr (kPair) {  // every other chunk; the other half's bytes count here too
-                if ((ch & 1) == half)
-                  tc::tma_load_2d_multicast_hint(to + ch * kChunkBytes, &kv_map, 64 * ch, y, full, kBoth, pol);
-              } else {
-                tc::tma_load_2d_hint(to + ch * kChunkBytes, &kv_map, 64 * ch, y, full, pol);
-              }
-            }
+            for (int ch = 3 * g; ch < 3 * g + 3; ++ch)
+              tc::tma_load_2d_hint(to + ch * kChunkBytes, &kv_map, 64 * ch, y, full, pol);
           }
           if (!ok) break;
           part = 0;
@@ -302,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         cp_async_wait<0>();
         if (!ok) abort_cta();
-        // no copy may land after the CTA exits: wait for the last issued pages and query
-        // (a wait that runs out, after a stop of a pair's other CTA, has been long enough for all)
+        // no copy may land after the CTA exits: wait for the last issued pages and query (a wait
+        // that runs out has been long enough for all)
         bool landed = true;
         for (int64_t jj = j > kSlots ? j - kSlots : 0; jj < j; ++jj)
           for (int g = 0; g < kGroups; ++g)
@@ -313,12 +300,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           landed = landed && tc::mbar_wait(bar(BAR_PAGE_FULL + kGroups * (int)(j % kSlots) + g),
                                            (uint32_t)(j / kSlots) & 1, kWaitNs);
         if (piece > 0) tc::mbar_wait(bar(BAR_Q_FULL), (uint32_t)(piece - 1) & 1, kWaitNs);
-        // nor may the other CTA's commits arrive here after that
-        if constexpr (kPair) {
-          for (int64_t jj = j > kSlots ? j - kSlots : 0; jj < j; ++jj)
-            if (!tc::mbar_wait(bar(BAR_FREE + kGroups * (int)(jj % kSlots) + kGroups - 1), (uint32_t)(jj / kSlots) & 1, kWaitNs))
-              break;
-        }
       }
       __syncwarp();
     } else if (warp >= kQkWarp) {
@@ -385,10 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int s = 0; s < 4; ++s)
                 tc::mma_f16_ss(tmem + kOCol + 64 * blk, tc::desc_at(va, 2 * blk * kChunkBytes + s * 2048),
                                tc::desc_at(pb, 32 * s), id_pv, 1);
-              if (blk == 0) continue;
-              const uint32_t free = bar(BAR_FREE + kGroups * slot + blk - 1);
-              if constexpr (kPair) tc::mma_commit_multicast(free, kBoth);
-              else tc::mma_commit(free);
+              if (blk > 0) tc::mma_commit(bar(BAR_FREE + kGroups * slot + blk - 1));
             }
             tc::mma_commit(bar(BAR_PV_DONE + slot));
             if (left == 1) tc::mma_commit(bar(BAR_O_FULL));
@@ -454,8 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           atomicOr(p.ws.status, MLA_DEVICE_ERR_BAD_PAGE);
         }
         if (ps && !stop) {
-          nodes_seen = h < H ? tree_row_mask(plan, p.tree_mask, d.row, row0 + h) : 0;
-          row_live = h < H && tree_row_live(plan, d.row, row0 + h);
+          nodes_seen = h < H ? tree_row_mask(plan, p.tree_mask, d.row, h) : 0;
+          row_live = h < H && tree_row_live(plan, d.row, h);
           m = -INFINITY;
           lpart = 0.f;
         }
@@ -600,15 +578,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             linv_s[h] = l > 0.f ? p.kv_scale / l : 0.f;
             if (h < H)
               // (a NaN among the scores: lse = +inf, with which the merge makes the row NaN)
-              p.ws.part_lse[(int64_t)d.slot * row_step + row0 + h] = l > 0.f    ? (m + log2f(l)) * kLn2
+              p.ws.part_lse[(int64_t)d.slot * H + h] = l > 0.f    ? (m + log2f(l)) * kLn2
                                                        : l == 0.f ? -INFINITY
                                                                   : INFINITY;
           }
-          if (tid == 0 && half == 0) p.ws.piece_err[d.slot] = bad;  // (a pair's pages are the same)
+          if (tid == 0) p.ws.piece_err[d.slot] = bad;
           bar_softmax();
           // O^T lane = dim 128*blk + 32*(w%4) + lane; this warp writes rows 32g .. 32g+31
           if (32 * g < H) {
-            float* out = p.ws.part_out + ((int64_t)d.slot * row_step + row0) * kDLatent + 32 * q4 + lane;
+            float* out = p.ws.part_out + (int64_t)d.slot * H * kDLatent + 32 * q4 + lane;
 #pragma unroll 1
             for (int blk = 0; blk < 4; ++blk) {
               uint32_t rr[32];
@@ -628,33 +606,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  // (the other CTA's copies and commits go to this one's shared memory as long as it works)
-  if constexpr (kPair) tc::cluster_sync();
   tc::fence_after_sync();
   if (warp == kQkWarp) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-template <bool kPair>
 cudaError_t launch_kernel(const Bf16TreeParams& p, const CUtensorMap& kv_map, const CUtensorMap& q_map,
                           cudaStream_t stream) {
   static std::atomic<int> configured[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !configured[dev].load()) {
-    const cudaError_t e = cudaFuncSetAttribute(decode_bf16_tree_kernel<kPair>,
+    const cudaError_t e = cudaFuncSetAttribute(decode_bf16_tree_kernel,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev].store(1);
   }
-  cudaLaunchAttribute attr[2] = {pdl_attribute(), pair_attribute()};
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(kPair ? 2 * p.G : p.G));
+  cfg.gridDim = dim3((unsigned)p.G);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = kPair ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, decode_bf16_tree_kernel<kPair>, p, kv_map, q_map);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_bf16_tree_kernel, p, kv_map, q_map);
 }
 
 }  // namespace
@@ -682,7 +657,7 @@ cudaError_t launch_decode_bf16_tree(const DecodeLaunch& d, cudaStream_t stream) 
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   if (!map(&kv_map, d.kv, (d.num_pages > 0 ? d.num_pages : 1) * kPageSize, kPageSize) ||
-      !map(&q_map, d.q, (int64_t)d.batch * d.query_rows(), d.heads > kTileRows ? kTileRows : d.heads))
+      !map(&q_map, d.q, (int64_t)d.batch * d.query_rows(), d.heads))
     return cudaErrorInvalidValue;
   Bf16TreeParams p;
   p.kv = d.kv;
@@ -702,8 +677,7 @@ cudaError_t launch_decode_bf16_tree(const DecodeLaunch& d, cudaStream_t stream) 
   p.max_nodes = d.max_nodes;
   p.node_heads = d.node_heads;
   p.query_rows = d.query_rows();
-  return d.heads > kTileRows ? launch_kernel<true>(p, kv_map, q_map, stream)
-                             : launch_kernel<false>(p, kv_map, q_map, stream);
+  return launch_kernel(p, kv_map, q_map, stream);
 }
 
 }  // namespace mla

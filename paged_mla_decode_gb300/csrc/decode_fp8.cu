@@ -162,23 +162,20 @@ struct Map {
   static constexpr int BAR_DRAIN = BAR_Q_EMPTY + 1;       // [2] one per issuer warp
   static constexpr int BAR_RAW_FULL = BAR_DRAIN + 2;      // [kRawRing] bulk-copy bytes landed
   static constexpr int BAR_RAW_EMPTY = BAR_RAW_FULL + kRawRing;  // [kRawRing] (expander warps)
-  // pairs of CTAs only: both CTAs' PVs have read the page in the slot
-  static constexpr int BAR_FREE = BAR_RAW_EMPTY + kRawRing;      // [kRing]
 #ifdef MLA_TEST_STALL_QK
   // Test build only: a barrier that nothing ever completes. The MMA issuer waits on
   // it before the QK of its third page, so the wait runs out and the CTA takes the
   // timeout path (stop every role, drain the copies and MMAs in flight, free TMEM).
-  static constexpr int BAR_TEST_STALL = BAR_FREE + kRing;
+  static constexpr int BAR_TEST_STALL = BAR_RAW_EMPTY + kRawRing;
   static constexpr int kNumBars = BAR_TEST_STALL + 1;
 #else
-  static constexpr int kNumBars = BAR_FREE + kRing;
+  static constexpr int kNumBars = BAR_RAW_EMPTY + kRawRing;
 #endif
   // arrivals that complete a phase of barrier i
   static __device__ __forceinline__ uint32_t bar_count(int i) {
     if ((i >= BAR_S_EMPTY && i < BAR_S_EMPTY + 2) || (i >= BAR_P_FULL && i < BAR_P_FULL + kPBufs) ||
         i == BAR_O_EMPTY || i == BAR_Q_READY)
       return kSmWarps;
-    if (i >= BAR_FREE && i < BAR_FREE + kRing) return 2;  // both CTAs' commits
     if (kE2m1 && (i < kRing || (i >= BAR_RAW_EMPTY && i < BAR_RAW_EMPTY + kRawRing)))
       return kExpWarps;
     return 1;
@@ -418,15 +415,11 @@ static __device__ __noinline__ void zero_nan_chunks(uint32_t page_base, int firs
 // its suffix range; otherwise mla_decode's single plan (Plan).
 // kE2m1: a 4-bit cache, expanded to e4m3 pages by seven more warps; otherwise e4m3.
 // kTree: the tree decode (TreePlan): a row is a tile of a request's query rows, each of
-// which sees the context and, of the nodes' tokens, those in its mask.
-// kPair: two CTAs of a cluster walk the same pages for the two halves of a 128-row tile. Each
-// brings half of every page into both CTAs' shared memory (TMA multicast), so a page crosses
-// from L2 once for 128 rows. (The SMs get some 5.8 TB/s together from L2, which is what one CTA a
-// tile asks for at 1 us a page. With half of that the page still takes 1.0 us: its 34 MMAs of
-// N = 64 at some 45 cycles each and the softmax's chain. 16 sessions of 32k-140k tokens, 12
-// nodes: 1,430 TFLOP/s, 1,320 without pairs. Two sets of softmax warps that take pages in turn
-// were slower.)
-template <bool kGrouped, bool kE2m1, bool kTree, bool kPair>
+// which sees the context and, of the nodes' tokens, those in its mask. 16 sessions of 32k-140k
+// tokens, 12 nodes of 64 heads: a call of 1,920 us over an e4m3 cache, 1.06 us a page and SM, 1,279
+// TFLOP/s: the page's 34 MMAs of N = 64 at some 45 cycles each and the softmax's chain. (Two sets of
+// softmax warps that take pages in turn were no faster.)
+template <bool kGrouped, bool kE2m1, bool kTree>
 __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
     decode_fp8_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap lat_map,
                       const __grid_constant__ CUtensorMap rope_map) {
@@ -463,10 +456,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
   // itself needs the split kernel to have completed (griddep_wait before q_op).
   using RowPlan = std::conditional_t<kTree, TreePlan, Plan>;
   RowPlan plan = row_plan<RowPlan>(p);
-  static_assert(!kPair || (kTree && !kE2m1), "pairs are the tree decode's, over e4m3 pages");
-  const int c = kPair ? blockIdx.x >> 1 : blockIdx.x;
-  const int half = kPair ? (int)tc::cluster_rank() : 0;  // of the tile's rows
-  constexpr uint16_t kBoth = 3;
+  const int c = blockIdx.x;
   int64_t* s_plan_x = reinterpret_cast<int64_t*>(smem + M::kOffPlanX);  // kGrouped only
   if (warp == 0) {
     if constexpr (kGrouped) {
@@ -495,7 +485,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
       RowPlan pl = plan;
       pl.set_total(plan_total_tiles_warp(pl));
       const int64_t xb = c < pl.G ? pl.cta_start(c) : 0;
-      RowCursor f = plan_find_row_warp(pl, xb, c == 0 && half == 0, p.ws.row_base, p.ws.row_np, p.ws.status);
+      RowCursor f = plan_find_row_warp(pl, xb, c == 0, p.ws.row_base, p.ws.row_np, p.ws.status);
       if (lane == 0) {
         s_plan[0] = pl.T;
         s_plan[1] = f.r;
@@ -526,7 +516,6 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if constexpr (kPair) tc::cluster_sync();  // both CTAs' barriers are there
   tc::fence_after_sync();
   griddep_launch_dependents();  // the combine kernel may be scheduled (it waits for this grid)
   if (tid == 0) MLA_STAMP(kStPrologue, 0);
@@ -542,8 +531,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const RowCursor cur0{(int)s_plan[1], s_plan[2], (int)s_plan[3], (int)s_plan[4],
                        (int)s_plan[5]};
-  const int H = kPair ? 64 : p.heads;  // rows of this CTA
-  const int row_step = kPair ? 2 * H : H, row0 = H * half;  // in a piece's partials
+  const int H = p.heads;
   auto abort_cta = [&]() {
     flags[F_ABORT] = 1;
     atomicOr(p.ws.status, MLA_DEVICE_ERR_TIMEOUT);
@@ -641,7 +629,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
           const uint32_t round = (uint32_t)(j / kRing);
           const uint32_t page_base = sbase + kOffPages + slot * kPageBytes;
           if (j >= kRing &&
-              (!tc::mbar_wait(bar((kPair ? M::BAR_FREE : BAR_PV_DONE) + slot), (round - 1) & 1, kWaitNs) ||
+              (!tc::mbar_wait(bar(BAR_PV_DONE + slot), (round - 1) & 1, kWaitNs) ||
                flags[F_ABORT])) {
             ok = false;
             break;
@@ -651,22 +639,12 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
             const int y = page * kPageSize;
             // (a grouped decode's shared page is read by the other forks' CTAs a
             // few pages' time later, well within the life of an evict-first line)
-            if constexpr (kPair) {
-              // this CTA's half of the page to both (the other half's bytes count here too)
-              for (int b = 2 * half; b < 2 * half + 2; ++b)
-                tc::tma_load_2d_multicast_hint(page_base + b * kLatBlock, &lat_map, 128 * b, y,
-                                               bar(BAR_PAGE_FULL + slot), kBoth, pol);
-              if (half == 0)
-                tc::tma_load_2d_multicast_hint(page_base + kRopeOff, &rope_map, kDLatent, y,
-                                               bar(BAR_PAGE_FULL + slot), kBoth, pol);
-            } else {
 #pragma unroll
-              for (int b = 0; b < 4; ++b)
-                tc::tma_load_2d_hint(page_base + b * kLatBlock, &lat_map, 128 * b, y,
-                                     bar(BAR_PAGE_FULL + slot), pol);
-              tc::tma_load_2d_hint(page_base + kRopeOff, &rope_map, kDLatent, y,
+            for (int b = 0; b < 4; ++b)
+              tc::tma_load_2d_hint(page_base + b * kLatBlock, &lat_map, 128 * b, y,
                                    bar(BAR_PAGE_FULL + slot), pol);
-            }
+            tc::tma_load_2d_hint(page_base + kRopeOff, &rope_map, kDLatent, y,
+                                 bar(BAR_PAGE_FULL + slot), pol);
             MLA_STAMP(kStTmaIssue, j);
           } else {
             // bad id: no copy; every token of the page is masked and the softmax
@@ -677,20 +655,12 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
         }
         cp_async_wait<0>();
         if (!ok) abort_cta();
-        // no copy may land after the CTA exits: wait for the last issued pages (a wait that runs
-        // out, after a stop of a pair's other CTA, has been long enough for all of them)
+        // no copy may land after the CTA exits: wait for the last issued pages
         constexpr int kLanding = kE2m1 ? M::kRawRing : kRing;
         constexpr int kLandBar = kE2m1 ? M::BAR_RAW_FULL : BAR_PAGE_FULL;
         for (int64_t jj = j > kLanding ? j - kLanding : 0; jj < j; ++jj)
-          if (!tc::mbar_wait(bar(kLandBar + (int)(jj % kLanding)), (uint32_t)(jj / kLanding) & 1,
-                             kDrainWaitNs))
-            break;
-        // nor may the other CTA's commits arrive here after that
-        if constexpr (kPair) {
-          for (int64_t jj = j > kRing ? j - kRing : 0; jj < j; ++jj)
-            if (!tc::mbar_wait(bar(M::BAR_FREE + (int)(jj % kRing)), (uint32_t)(jj / kRing) & 1, kDrainWaitNs))
-              break;
-        }
+          tc::mbar_wait(bar(kLandBar + (int)(jj % kLanding)), (uint32_t)(jj / kLanding) & 1,
+                        kDrainWaitNs);
       }
       __syncwarp();
     } else if (kE2m1 && warp >= kExpWarp0) {
@@ -805,7 +775,6 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
                   tc::mma_f8_ss(tmem + kOCol + 64 * blk, tc::desc_at(va, blk * kLatBlock + s * 4096),
                                 tc::desc_at(pb, 64 * part + 32 * s), part ? id_pv_lo : id_pv_hi, 1);
             tc::mma_commit(bar(BAR_PV_DONE + slot));
-            if constexpr (kPair) tc::mma_commit_multicast(bar(M::BAR_FREE + slot), kBoth);
           }
           MLA_STAMP(kStPvIssued, k);
         }
@@ -893,14 +862,13 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
           griddep_wait();  // the split kernel has completed and its writes are visible
           const bool live = h < H;
           if constexpr (kTree) {
-            nodes_seen = tree_row_mask(plan, p.tree_mask, row, row0 + h);
-            row_live = tree_row_live(plan, row, row0 + h);
+            nodes_seen = tree_row_mask(plan, p.tree_mask, row, h);
+            row_live = tree_row_live(plan, row, h);
           }
-          const int64_t q_row = kPair ? 2 * (int64_t)row + half : row;
-          qmul = live ? __ldcg(p.ws.q_mul + q_row * 64 + h) : 0.f;
+          qmul = live ? __ldcg(p.ws.q_mul + (int64_t)row * 64 + h) : 0.f;
           const int r = 32 * q4 + lane;
           const uint4* src =
-              reinterpret_cast<const uint4*>(p.ws.q_op + q_row * kQOpRowBytes) + r;
+              reinterpret_cast<const uint4*>(p.ws.q_op + (int64_t)row * kQOpRowBytes) + r;
           uint4 qc[18];
 #pragma unroll
           for (int u = 0; u < 16; ++u)
@@ -1134,16 +1102,16 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
             linv_s[h] = l > 0.f ? p.kv_scale / l : 0.f;
             if (h < H)
               // (a NaN among the scores: lse = +inf, with which the merge makes the row NaN)
-              p.ws.part_lse[(int64_t)slot * row_step + row0 + h] =
+              p.ws.part_lse[(int64_t)slot * H + h] =
                   l > 0.f    ? (m - (float)kPOffset + log2f(l)) * kLn2
                   : l == 0.f ? -INFINITY
                              : INFINITY;
           }
-          if (t == 0 && half == 0) p.ws.piece_err[slot] = bad;  // (a pair's pages are the same)
+          if (t == 0) p.ws.piece_err[slot] = bad;
           named_bar_softmax();
           // O^T lane = dim 128*blk + 32*(w%4) + lane; this warp writes heads 32g .. 32g+31
           if (32 * g < H) {
-            float* out = p.ws.part_out + ((int64_t)slot * row_step + row0) * kDLatent + 32 * q4 + lane;
+            float* out = p.ws.part_out + (int64_t)slot * H * kDLatent + 32 * q4 + lane;
 #pragma unroll 1
             for (int blk = 0; blk < 4; ++blk) {
               uint32_t rr[32];
@@ -1186,8 +1154,6 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  // (the other CTA's copies and commits go to this one's shared memory as long as it works)
-  if constexpr (kPair) tc::cluster_sync();
   tc::fence_after_sync();
   if (warp == kQkWarp) tc::tmem_dealloc(tmem, kTmemCols);
   if (tid == 0) MLA_STAMP(kStExit, 0);
@@ -1348,7 +1314,7 @@ __global__ void __launch_bounds__(32) group_plan_kernel(const Fp8Params p) {
 }  // namespace
 
 // One variant of the decode kernel: its shared-memory limit once per device, then the launch.
-template <bool kGrouped, bool kE2m1, bool kTree = false, bool kPair = false>
+template <bool kGrouped, bool kE2m1, bool kTree = false>
 static cudaError_t launch_variant(const Fp8Params& p, const CUtensorMap& lat_map,
                                   const CUtensorMap& rope_map, cudaStream_t stream) {
   using M = Map<kE2m1>;
@@ -1357,20 +1323,20 @@ static cudaError_t launch_variant(const Fp8Params& p, const CUtensorMap& lat_map
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !configured[dev].load()) {
-    cudaError_t e = cudaFuncSetAttribute(decode_fp8_kernel<kGrouped, kE2m1, kTree, kPair>,
+    cudaError_t e = cudaFuncSetAttribute(decode_fp8_kernel<kGrouped, kE2m1, kTree>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev].store(1);
   }
-  cudaLaunchAttribute attr[2] = {pdl_attribute(), pair_attribute()};
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(kPair ? 2 * p.G : p.G));
+  cfg.gridDim = dim3((unsigned)p.G);
   cfg.blockDim = dim3(M::kThreads);
   cfg.dynamicSmemBytes = kBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = kPair ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, decode_fp8_kernel<kGrouped, kE2m1, kTree, kPair>, p, lat_map, rope_map);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_fp8_kernel<kGrouped, kE2m1, kTree>, p, lat_map, rope_map);
 }
 
 // Tensor maps of an e4m3 pool viewed as [num_pages * 64 rows][576 bytes] (a page is 64
@@ -1433,7 +1399,6 @@ cudaError_t launch_decode_fp8(const DecodeLaunch& d, cudaStream_t stream) {
   p.max_nodes = d.max_nodes;
   p.node_heads = d.node_heads;
   p.query_rows = d.query_rows();
-  const bool pair = d.heads > 64;  // (a tree decode's tiles of 128 rows)
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   if (grouped) {
     cudaLaunchConfig_t gc = {};
@@ -1446,21 +1411,19 @@ cudaError_t launch_decode_fp8(const DecodeLaunch& d, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   {
-    const int q_heads = pair ? 64 : d.heads, q_rows = pair ? 2 * d.nq : d.nq;  // of a request
-    const int groups = (q_heads + kSplitHeads - 1) / kSplitHeads;
+    const int groups = (d.heads + kSplitHeads - 1) / kSplitHeads;
     cudaLaunchConfig_t sc = {};
-    sc.gridDim = dim3((unsigned)((int64_t)d.batch * q_rows * groups));
+    sc.gridDim = dim3((unsigned)((int64_t)d.batch * d.nq * groups));
     sc.blockDim = dim3(kSplitThreads);
     sc.stream = stream;
     sc.attrs = attr;
     sc.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&sc, q_split_kernel, d.q, q_heads, q_rows, p.query_rows, d.score_mul,
-                                       d.ws.q_op, d.ws.q_mul);
+    cudaError_t e = cudaLaunchKernelEx(&sc, q_split_kernel, d.q, d.heads, d.nq, p.query_rows,
+                                       d.score_mul, d.ws.q_op, d.ws.q_mul);
     if (e != cudaSuccess) return e;
   }
   if (d.tree_mask != nullptr)
     return d.e2m1 ? launch_variant<false, true, true>(p, lat_map, rope_map, stream)
-           : pair ? launch_variant<false, false, true, true>(p, lat_map, rope_map, stream)
                   : launch_variant<false, false, true>(p, lat_map, rope_map, stream);
   if (d.e2m1)
     return grouped ? launch_variant<true, true>(p, lat_map, rope_map, stream)

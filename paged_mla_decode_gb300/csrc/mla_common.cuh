@@ -50,10 +50,8 @@ __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a -
 
 // `passes` is 1 for mla_decode and 2 for the grouped decode, whose prefix and
 // suffix passes each add up to num_ctas + rows pieces.
-// A tree decode's rows of 128 heads (pairs of tiles) have two query operands each.
 __host__ __device__ inline WorkspaceLayout workspace_layout(int64_t rows, int heads, int num_ctas,
                                                             int passes = 1) {
-  const int64_t q_rows = heads > 64 ? 2 * rows : rows;
   WorkspaceLayout w;
   w.max_pieces = (int64_t)passes * (num_ctas + rows);
   size_t off = 256;
@@ -63,8 +61,8 @@ __host__ __device__ inline WorkspaceLayout workspace_layout(int64_t rows, int he
   w.piece_err = off; off = align_up(off + 4 * w.max_pieces, 256);
   w.part_lse = off; off = align_up(off + 4 * w.max_pieces * heads, 256);
   w.part_out = off; off = align_up(off + 4 * w.max_pieces * heads * (int64_t)kDLatent, 256);
-  w.q_op = off; off = align_up(off + (size_t)kQOpRowBytes * q_rows, 256);
-  w.q_mul = off; off = align_up(off + 4 * 64 * q_rows, 256);
+  w.q_op = off; off = align_up(off + (size_t)kQOpRowBytes * rows, 256);
+  w.q_mul = off; off = align_up(off + 4 * 64 * rows, 256);
   w.total = off;
   return w;
 }
@@ -213,7 +211,7 @@ struct GroupPlan {
 // `tile_rows` rows, whatever nodes those belong to, and a plan row is one tile,
 // r = b * tiles + i, over all L tokens of its request (which of the last n, the
 // nodes', a query row sees is its node's mask). Tiles with no node of the request
-// have no tokens. Tiles of 128 rows are worked by a pair of CTAs, 64 rows each. A request is bad if n is outside [0, max_nodes] or L outside
+// have no tokens. A request is bad if n is outside [0, max_nodes] or L outside
 // [n, max_pages * 64].
 // ---------------------------------------------------------------------------
 struct TreePlan {

@@ -44,8 +44,7 @@ struct DecodeLaunch {
   int forks = 1;
   const int32_t* prefix_pages = nullptr;
   // tree decode only (else tree_mask == nullptr): nq is the tiles of a request, heads the
-  // rows of a tile (see TreePlan; 128: for a pair of CTAs, of which there are G), of which a
-  // request has max_nodes * node_heads in all
+  // rows of a tile (see TreePlan), of which a request has max_nodes * node_heads in all
   const uint64_t* tree_mask = nullptr;
   const int32_t* num_nodes = nullptr;  // may be null
   int max_nodes = 0, node_heads = 0;
@@ -80,16 +79,6 @@ inline cudaLaunchAttribute pdl_attribute() {
   cudaLaunchAttribute a;
   a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a.val.programmaticStreamSerializationAllowed = 1;
-  return a;
-}
-
-// Launch attribute for clusters of two CTAs.
-inline cudaLaunchAttribute pair_attribute() {
-  cudaLaunchAttribute a;
-  a.id = cudaLaunchAttributeClusterDimension;
-  a.val.clusterDim.x = 2;
-  a.val.clusterDim.y = 1;
-  a.val.clusterDim.z = 1;
   return a;
 }
 

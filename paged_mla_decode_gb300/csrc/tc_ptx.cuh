@@ -109,18 +109,6 @@ __device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const void* tmap,
       : "memory");
 }
 
-// As tma_load_2d_hint, into the same place of every CTA of the cluster whose bit is set in
-// `ctas`, each signalling the mbarrier at the same place there.
-__device__ __forceinline__ void tma_load_2d_multicast_hint(uint32_t dst, const void* tmap, int x,
-                                                           int y, uint32_t mbar, uint16_t ctas,
-                                                           uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".multicast::cluster.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5, %6;\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(mbar), "h"(ctas), "l"(policy)
-      : "memory");
-}
-
 // Contiguous bulk copy global -> shared (both 16-byte aligned, bytes a multiple
 // of 16); completion is signalled on `mbar` as transaction bytes.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -263,28 +251,6 @@ __device__ __forceinline__ void mma_commit(uint32_t mbar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(mbar)
       : "memory");
-}
-
-// As mma_commit, on the mbarrier at the same place of every CTA whose bit is set in `ctas`.
-__device__ __forceinline__ void mma_commit_multicast(uint32_t mbar, uint16_t ctas) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;\n" ::"r"(mbar), "h"(ctas)
-      : "memory");
-}
-
-// ---------------------------------------------------------------------------
-// Clusters
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
-  return r;
-}
-// Barrier over all threads of the cluster's CTAs (every path of a kernel that has clusters
-// gets there in bounded time).
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
