@@ -260,10 +260,11 @@ MLA_API mla_status mla_decode_grouped(const void* q, const void* kv_pages, int64
  * node sees. A chain of drafts is the mask 2^(j + 1) - 1.
  *
  * The max_nodes * num_heads query rows of a request are cut into tiles of 64, whatever
- * nodes they belong to; a tile's rows share each page that is read, and where that is faster
- * two tiles do. Arithmetic as mla_decode's;
- * so a NaN in an entry makes the rows that see it NaN, and no others. (A cached bf16
- * infinity makes the rows that see it NaN, or drops out where its score is -inf.)
+ * nodes they belong to; a tile's rows share each page that is read. Arithmetic as
+ * mla_decode's; so a NaN in an entry makes the rows that see it NaN, and no others. A
+ * cached bf16 infinity does so too, except in rows whose score of it is -inf: there the
+ * entry has no weight in out or lse, but the latent dims of out at which a context token
+ * (not a node) holds the infinity may be NaN, as 0 times it.
  *
  * tree_mask   device, uint64 [batch][max_nodes]
  * num_nodes   device, int32 [batch]; NULL: max_nodes each. Rows j >= num_nodes[b] get
