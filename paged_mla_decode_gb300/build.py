@@ -23,9 +23,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmla.so")
-# Test build: the FP8 decode kernel's QK issuer waits on a barrier that nothing
-# completes and waits between roles give up after 20 ms, so that the timeout path
-# (status bit, stop, drain, TMEM freed) can be run and checked. Not the product.
+# Test build: the QK issuer of the FP8 and of the bf16 tree decode kernel waits on a
+# barrier that nothing completes and waits between roles give up after 20 ms, so that
+# the timeout path (status bit, stop, drain, TMEM freed) can be run and checked. Not the product.
+STALL_SOURCES = ("decode_fp8", "decode_bf16_tree")
 STALL_LIB_PATH = os.path.join(PKG, "libmla_stall_test.so")
 STALL_DEFINES = ["-DMLA_TEST_STALL_QK", "-DMLA_PIPELINE_WAIT_NS=20000000ull"]
 
@@ -93,15 +94,14 @@ def build(verbose: bool = False, force: bool = False) -> str:
     if force:
         for o in glob.glob(os.path.join(BUILD_DIR, "*.o")):
             os.remove(o)
-    fp8 = os.path.join(CSRC, "decode_fp8.cu")
-    jobs = [(src, "", ()) for src in srcs] + [(fp8, "_stall", tuple(STALL_DEFINES))]
+    jobs = [(src, "", ()) for src in srcs]
+    jobs += [(os.path.join(CSRC, f"{name}.cu"), "_stall", tuple(STALL_DEFINES)) for name in STALL_SOURCES]
     with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
         objs = list(ex.map(lambda j: _compile(nvcc, j[0], verbose, j[1], j[2]), jobs))
     product = objs[:len(srcs)]
     _link(nvcc, LIB_PATH, product)
-    stall_obj = objs[len(srcs)]
-    fp8_obj = os.path.join(BUILD_DIR, "decode_fp8.o")
-    _link(nvcc, STALL_LIB_PATH, [o for o in product if o != fp8_obj] + [stall_obj])
+    replaced = {os.path.join(BUILD_DIR, f"{name}.o") for name in STALL_SOURCES}
+    _link(nvcc, STALL_LIB_PATH, [o for o in product if o not in replaced] + objs[len(srcs):])
     return LIB_PATH
 
 

@@ -31,7 +31,7 @@
 // TMEM (512 columns): S buffers [0,64) [64,128), O^T [256,512).
 //
 // Every wait is bounded (2 s); on timeout the CTA records MLA_DEVICE_ERR_TIMEOUT, stops, drains
-// its MMAs and copies (bounded, 2 s) and frees TMEM.
+// its MMAs and copies (bounded, 2 s) and frees TMEM; tests/test_gpu_tree_bf16_timeout.py runs that.
 #include <atomic>
 
 #include <cuda.h>
@@ -56,7 +56,13 @@ constexpr int kSlots = 2;
 constexpr int kGroups = 3;                          // QK starts on a third of a page
 constexpr int kPrefetch = 4;                        // pages ahead that L2 is asked for
 constexpr float kRescaleThresh = 7.0f;              // log2 units
-constexpr uint64_t kWaitNs = 2000000000ull;         // every wait
+// Limits of a wait on another role, which a test build lowers to make the timeout path run, and of
+// a wait for copies and MMAs already issued.
+#ifndef MLA_PIPELINE_WAIT_NS
+#define MLA_PIPELINE_WAIT_NS 2000000000ull
+#endif
+constexpr uint64_t kWaitNs = MLA_PIPELINE_WAIT_NS;
+constexpr uint64_t kDrainWaitNs = 2000000000ull;
 constexpr int kDescRing = 64;    // page descriptors in flight
 constexpr int kTableAhead = 32;  // pages described (block-table read started) before issue
 
@@ -86,7 +92,14 @@ enum Bar {
   BAR_DRAIN = BAR_Q_EMPTY + 1,        // [2] one per issuer warp
   // [2][kGroups] the page's PV has read the third in the slot
   BAR_FREE = BAR_DRAIN + 2,
+#ifdef MLA_TEST_STALL_QK
+  // Test build only: a barrier that nothing ever completes, on which the QK issuer waits before its
+  // third page (as in decode_fp8.cu).
+  BAR_TEST_STALL = BAR_FREE + 2 * kGroups,
+  kNumBars
+#else
   kNumBars = BAR_FREE + 2 * kGroups
+#endif
 };
 constexpr int kOffTmem = kOffBar + 8 * kNumBars;
 constexpr int kSmemBytes = kOffTmem + 16 + 1024;  // slack for the 1024 alignment
@@ -295,11 +308,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int64_t jj = j > kSlots ? j - kSlots : 0; jj < j; ++jj)
           for (int g = 0; g < kGroups; ++g)
             landed = landed && tc::mbar_wait(bar(BAR_PAGE_FULL + kGroups * (int)(jj % kSlots) + g),
-                                             (uint32_t)(jj / kSlots) & 1, kWaitNs);
+                                             (uint32_t)(jj / kSlots) & 1, kDrainWaitNs);
         for (int g = 0; g < part; ++g)
           landed = landed && tc::mbar_wait(bar(BAR_PAGE_FULL + kGroups * (int)(j % kSlots) + g),
-                                           (uint32_t)(j / kSlots) & 1, kWaitNs);
-        if (piece > 0) tc::mbar_wait(bar(BAR_Q_FULL), (uint32_t)(piece - 1) & 1, kWaitNs);
+                                           (uint32_t)(j / kSlots) & 1, kDrainWaitNs);
+        if (piece > 0) tc::mbar_wait(bar(BAR_Q_FULL), (uint32_t)(piece - 1) & 1, kDrainWaitNs);
       }
       __syncwarp();
     } else if (warp >= kQkWarp) {
@@ -332,6 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++piece;
         }
         if (is_qk) {
+#ifdef MLA_TEST_STALL_QK
+          if (k == 2) ok = ok && wait(BAR_TEST_STALL, 0);
+#endif
           if (ok && k >= 2) ok = wait(BAR_S_EMPTY + slot, ((k >> 1) - 1) & 1);
           const uint64_t kb = tc::smem_desc_sw128(page, 16, 1024);
           const uint32_t d_s = tmem + s_col(k & 1u);
@@ -381,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // drain: every MMA this warp issued has finished before TMEM is freed
       const int db = BAR_DRAIN + (is_qk ? 0 : 1);
       if (tc::elect_one()) tc::mma_commit(bar(db));
-      if (!tc::mbar_wait(bar(db), 0, kWaitNs)) atomicOr(p.ws.status, MLA_DEVICE_ERR_TIMEOUT);
+      if (!tc::mbar_wait(bar(db), 0, kDrainWaitNs)) atomicOr(p.ws.status, MLA_DEVICE_ERR_TIMEOUT);
       __syncwarp();
     } else {
       // =================== softmax + epilogue (warps 0-7) ===================
