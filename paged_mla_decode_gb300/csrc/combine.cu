@@ -98,7 +98,7 @@ __device__ __forceinline__ void merge_row(const float* __restrict__ out_base, in
 // throughout, both beside an earlier decode kernel); 48 rows of one page 21 (28, 42); one
 // row of 100k tokens among 31 of one page 91 (101, 110). A tree decode's 32 x 992 rows
 // merge in 25 us by a warp a row, 48 by a warp a quarter. For the few rows the first kernel
-// stays: it has 40 registers a thread, the second 72.
+// stays: it has 32 registers a thread, the second 64.
 constexpr int kFewPieces = 16;
 constexpr int kWarpMergeLoads = 2;  // pieces whose loads are in flight (each all four quarters)
 
@@ -162,11 +162,12 @@ __device__ __forceinline__ int find_row_of_many(const MergeParams& p, int k) {
 // One (row, head) by one warp: lane l keeps dims 128 q + 4l .. + 3 of each quarter q, and the
 // weight of one of 32 pieces at a time. (A warp a quarter had four times the warps wait for the
 // same chain of reads: row table, lse, partials.)
+template <bool kTiled>
 __device__ __forceinline__ void merge_row_by_warp(const MergeParams& p, int64_t rh, int lane) {
   const int r = (int)(rh / p.heads), h = (int)(rh - (int64_t)r * p.heads);
   const int np = __ldcg(p.row_np + r), base = __ldcg(p.row_base + r);
-  const int64_t to = p.to_rows.of(r, h, p.heads);
-  if (np > kFewPieces || to < 0) return;  // another block's, or nobody's
+  const int64_t to = p.to_rows.of<kTiled>(rh, r, h, p.heads);
+  if (np > kFewPieces || (kTiled && to < 0)) return;  // another block's, or nobody's
   float l_own = -INFINITY;
   int bad = 0;
   if (lane < np) {
@@ -222,6 +223,7 @@ __device__ __forceinline__ void merge_row_by_warp(const MergeParams& p, int64_t 
 }
 
 // Unit `unit` by the whole block.
+template <bool kTiled>
 __device__ __forceinline__ void merge_unit_by_block(const MergeParams& p, int64_t unit) {
   extern __shared__ float4 stage[];                 // [stage_pieces][32] float4
   __shared__ __align__(8) uint64_t mbar;
@@ -232,7 +234,7 @@ __device__ __forceinline__ void merge_unit_by_block(const MergeParams& p, int64_
     tc::fence_mbar_init();
   }
   uint32_t phase = 0;
-  const bool ok = merge_unit(
+  const bool ok = merge_unit<kTiled>(
       unit, p.heads, p.row_base, p.row_np, p.piece_err, p.part_lse, p.part_out, p.out, p.lse,
       p.to_rows, p.stage_pieces, stage, sm, mb, phase, (int)threadIdx.x, [] { __syncthreads(); },
       [](bool pred) { return __syncthreads_or(pred ? 1 : 0) != 0; });
@@ -240,24 +242,29 @@ __device__ __forceinline__ void merge_unit_by_block(const MergeParams& p, int64_
 }
 
 // Both are launched as dependents of the decode kernel: its partials are visible after
-// griddep_wait.
+// griddep_wait. kTiled: a tree decode whose requests' rows end inside a tile. (Where rows are the
+// output's as they are, finding them out costs the few-rows kernel eight registers, and with them
+// two blocks an SM: 4 requests of 3,000 tokens, four drafts, 64 heads, bf16 cache, a call of 46.9 us
+// with it, 46.3 without.)
+template <bool kTiled>
 __global__ void __launch_bounds__(kMergeThreads) combine_pieces_kernel(const MergeParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  merge_unit_by_block(p, blockIdx.x);
+  merge_unit_by_block<kTiled>(p, blockIdx.x);
 }
 
+template <bool kTiled>
 __global__ void __launch_bounds__(kMergeThreads) combine_rows_kernel(const MergeParams p) {
   griddep_wait();
   griddep_launch_dependents();
   if (blockIdx.x >= p.many_blocks) {
     const int64_t rh = (int64_t)(blockIdx.x - p.many_blocks) * kMergeWarps + (threadIdx.x >> 5);
-    if (rh < p.units / kMergeQuarters) merge_row_by_warp(p, rh, threadIdx.x & 31);
+    if (rh < p.units / kMergeQuarters) merge_row_by_warp<kTiled>(p, rh, threadIdx.x & 31);
     return;
   }
   const unsigned per_row = (unsigned)p.heads * kMergeQuarters;
   const int row = find_row_of_many(p, (int)(blockIdx.x / per_row));
-  if (row >= 0) merge_unit_by_block(p, (int64_t)row * per_row + blockIdx.x % per_row);
+  if (row >= 0) merge_unit_by_block<kTiled>(p, (int64_t)row * per_row + blockIdx.x % per_row);
 }
 
 // Standalone merge: part_out [S][rows][512], part_lse [S][rows]; one block per row.
@@ -280,7 +287,8 @@ cudaError_t launch_combine_pieces(const DecodeWorkspace& ws, int rows, int heads
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !configured[dev].load()) {
-    for (const auto kernel : {combine_pieces_kernel, combine_rows_kernel}) {
+    for (const auto kernel : {combine_pieces_kernel<false>, combine_pieces_kernel<true>,
+                              combine_rows_kernel<false>, combine_rows_kernel<true>}) {
       cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kMergeStagePieces * (int)kMergeSliceBytes);
       if (e != cudaSuccess) return e;
@@ -306,7 +314,8 @@ cudaError_t launch_combine_pieces(const DecodeWorkspace& ws, int rows, int heads
   p.out = out;
   p.lse = lse;
   p.status = ws.status;
-  p.to_rows = OutputRows{tiles, query_rows < tiles * heads ? query_rows : 0};
+  p.to_rows = OutputRows{tiles, query_rows};
+  const bool tiled = query_rows > 0 && query_rows < tiles * heads;
   p.stage_pieces = merge_stage_pieces(max_pieces_per_row, rows);
   const int64_t blocks =
       few_rows ? p.units
@@ -320,7 +329,9 @@ cudaError_t launch_combine_pieces(const DecodeWorkspace& ws, int rows, int heads
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_rows ? combine_pieces_kernel : combine_rows_kernel, p);
+  const auto kernel = few_rows ? (tiled ? combine_pieces_kernel<true> : combine_pieces_kernel<false>)
+                               : (tiled ? combine_rows_kernel<true> : combine_rows_kernel<false>);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace mla

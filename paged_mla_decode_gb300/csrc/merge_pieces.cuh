@@ -23,12 +23,13 @@ constexpr int kMergeStagePieces = 160;
 constexpr uint32_t kMergeSliceBytes = 128 * 4;
 constexpr uint64_t kMergeWaitNs = 2000000000ull;
 
-// Output row of row r, head h: r * heads + h, or the request's where its rows end inside
-// the last of its tiles (launch_combine_pieces); -1: none.
+// Output row of row r, head h (r * heads + h = rh): rh itself, or, kTiled, the request's where its
+// query_rows rows end inside the last of its tiles (launch_combine_pieces); -1: none.
 struct OutputRows {
-  int tiles, query_rows;  // query_rows = 0: as many as tiles * heads
-  __device__ __forceinline__ int64_t of(int r, int h, int heads) const {
-    if (query_rows == 0) return (int64_t)r * heads + h;
+  int tiles, query_rows;
+  template <bool kTiled>
+  __device__ __forceinline__ int64_t of(int64_t rh, int r, int h, int heads) const {
+    if constexpr (!kTiled) return rh;
     const int b = r / tiles, at = (r - b * tiles) * heads + h;
     return at < query_rows ? (int64_t)b * query_rows + at : -1;
   }
@@ -51,21 +52,22 @@ struct MergeShared {
 // shared memory (lane = 4 dims) and the warps' sums are added. `sync()` and
 // `sync_or(p)` are barriers over the group's threads (tid 0 .. kMergeThreads - 1).
 // Returns false if a copy did not land within its bound (recorded by the caller).
-template <class Sync, class SyncOr>
+template <bool kTiled, class Sync, class SyncOr>
 __device__ inline bool merge_unit(int64_t unit, int heads, const int32_t* __restrict__ row_base,
                                   const int32_t* __restrict__ row_np,
                                   const int32_t* __restrict__ piece_err,
                                   const float* __restrict__ part_lse,
                                   const float* __restrict__ part_out,
                                   __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
-                                  const OutputRows& to_rows, int stage_pieces, float4* stage, MergeShared& sm, uint32_t mb,
-                                  uint32_t& phase, int tid, Sync sync, SyncOr sync_or) {
+                                  const OutputRows& to_rows, int stage_pieces, float4* stage,
+                                  MergeShared& sm, uint32_t mb, uint32_t& phase, int tid, Sync sync,
+                                  SyncOr sync_or) {
   const int quarter = (int)(unit % kMergeQuarters);
   const int64_t rh = unit / kMergeQuarters;
   const int r = (int)(rh / heads);
   const int h = (int)(rh - (int64_t)r * heads);
-  const int64_t to = to_rows.of(r, h, heads);
-  if (to < 0) return true;
+  const int64_t to = to_rows.template of<kTiled>(rh, r, h, heads);
+  if (kTiled && to < 0) return true;
   const int warp = tid >> 5, lane = tid & 31;
   const int np = __ldcg(row_np + r);
   const int base = __ldcg(row_base + r);
