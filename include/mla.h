@@ -495,7 +495,8 @@ MLA_API mla_status mla_verify_drafts(const void* target_probs, int64_t target_st
  *   p(v) = exp((x(v) - max x) / temperature) / sum.
  * A temperature that is not above 0 puts all weight on the maximum, the lowest token of
  * equal ones; tokens at +inf share the weight; a row without a token above -inf is 0
- * throughout (the verifications then give the token -1). Arithmetic in fp32, rounded once.
+ * throughout (the verifications then give the token -1). Arithmetic in fp32 (a logit that leaves
+ * its range is an infinity), rounded once.
  *
  * logits        device, [batch][rows] rows of `vocab`, logit_stride >= vocab elements apart
  * probs         device, likewise, prob_stride apart; may be `logits` (same type and stride)

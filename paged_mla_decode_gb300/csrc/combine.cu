@@ -93,11 +93,12 @@ __device__ __forceinline__ void merge_row(const float* __restrict__ out_base, in
 // `many_rows` (every CTA's range cuts one row at most), and of the others a warp takes a
 // (row, head) each: a block would spend its barriers and its staging on a few pieces there. The grid
 // then starts with the blocks of the rows of many pieces; each looks for its row in the
-// row table and leaves if there is none. A decode call of 256 rows of 8 pages, 64 heads,
-// takes 74 us (84 when a warp took a quarter of the dims and 178 with a block per unit
-// throughout, both beside an earlier decode kernel); 48 rows of one page 21 (28, 42); one
-// row of 100k tokens among 31 of one page 91 (101, 110). A tree decode's 32 x 992 rows
-// merge in 25 us by a warp a row, 48 by a warp a quarter. For the few rows the first kernel
+// row table and leaves if there is none. Decode calls over a bf16 cache, 64 heads, in turn with
+// a warp for each quarter of the dims: 256 rows of 8 pages 118 and 132 us, 32 requests of 2,000
+// tokens with four queries 174 and 180, 48 rows of one page 25.0 and 27.3, one row of 100k tokens
+// among 31 of one page 133 and 133 (a block per unit throughout: 178 us over a 4-bit cache for the 256
+// rows, where a warp a quarter took 84). A tree decode's 32 x 992 rows merge in 25 us by a warp a
+// row, 48 by a warp a quarter. For the few rows the first kernel
 // stays: it has 32 registers a thread, the second 64.
 constexpr int kFewPieces = 16;
 constexpr int kWarpMergeLoads = 2;  // pieces whose loads are in flight (each all four quarters)

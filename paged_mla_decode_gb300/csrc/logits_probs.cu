@@ -11,20 +11,28 @@
 //   p = exp((x - max x) / temperature) / sum
 // A drafted token's row also counts the drafts on its own path (the node mask's bits).
 //
-// A row is read and written, and the SMs together get some 5.8 TB/s from L2, whether the bytes
-// come from DRAM or were there: bytes bound many rows. A cluster of up to eight blocks works a
-// row in two passes over its logits: the first sums exponentials in every thread, relative to a
-// reference that moves only when a logit lies far above it, and the blocks exchange references and
-// sums through distributed shared memory; the second writes exp(x - reference) / sum. (A row kept on
-// chip in between reads half, but leaves too few blocks an SM to cover the exchange.) The
-// counts are read once for several rows of a request: a block keeps a byte a token, which picks
-// the token's two factors and its difference from a table. A row whose sum is not a positive
-// finite number (infinities, NaNs, nothing allowed) is done again one token at a time, with a
-// running maximum and every case looked at.
+// A cluster of up to eight blocks works a row in two passes over its logits: the first sums
+// exponentials in every thread, relative to a reference that moves only when a logit lies far above
+// it, and the blocks exchange references and sums through distributed shared memory; the second
+// writes exp(x - reference) / sum. (A row kept on chip in between reads half, but leaves too few
+// blocks an SM to cover the exchange.) The counts are read once for several rows of a request: a
+// block keeps a byte a token, which picks the token's two factors and its difference from a table.
+// A row whose sum is not a positive finite number (infinities, NaNs, nothing allowed) is done again
+// one token at a time, with a running maximum and every case looked at.
 //
-// Measured: 32 x 8 rows of 163,840 logits 112 us, 128 x 1 73 (what a copy of the bytes that cross
-// takes), one request's four rows of 131,072 8.6; with rows kept on chip 1.3 times as long, with a
-// ring of asynchronous copies 75 for 73.
+// Measured, with what crosses between L2 and the SMs (logits twice, probabilities, counts once a
+// group of rows, masks; a copy of 128 float rows moves 168 MB there in 27 us, 6.2 TB/s).
+// Temperature alone: 32 x 8 rows of 163,840 bf16 logits to floats 75 us (336 MB, 4.5 TB/s), to bf16
+// 53 (252 MB, 4.7); 128 x 1 float rows 52 (252 MB, 4.8). Settings cost more than their bytes, in
+// work for each token: the 32 x 8 rows take 94 us with penalties, 93 with biases and a grammar, 111
+// with all (390 MB, 3.5 TB/s; issue slots 49% busy); the 128 x 1 rows 74 with penalties and biases
+// (336 MB, 4.5 TB/s). One request's four rows of 131,072 9.5. Rows kept on chip took 1.3 times as
+// long, a ring of asynchronous copies 75 us for 73. Rows that do not allow 16-byte accesses go one
+// token at a time: 32 x 8 rows of 163,841 307 us with temperature alone and 462 with all, 128 x 1
+// with penalties and biases 234.
+//
+// Roundings beyond fp32's own: exp2 is good to 2^-22, and a repetition penalty divides by its rounded
+// inverse. Against 64 bits the 32 x 8 rows are off by 1.7e-7 of their norm, a plain fp32 form by 3.5e-8.
 //
 // Tokens that a list names (biases, drafts) are left out of the passes, by a bit each, and
 // worked out by a thread an entry, which adds up all of its token's entries in order.
