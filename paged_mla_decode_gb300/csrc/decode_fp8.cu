@@ -465,6 +465,7 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
       GroupPlan A = group_plan(p, 1), B = group_plan(p, 2);
       A.set_total(plan_total_tiles_warp(A));
       B.set_total(plan_total_tiles_warp(B));
+      if (A.T + B.T == 0) griddep_wait();  // (as below)
       const int w = c / p.forks, f = c - w * p.forks;
       const bool in_a = c < p.forks * p.workers && w < A.G;
       const bool in_b = c < B.G;
@@ -484,6 +485,9 @@ __global__ void __launch_bounds__(Map<kE2m1>::kThreads, 1)
       // the whole plan in one warp pass: total tiles, then this CTA's first row
       RowPlan pl = plan;
       pl.set_total(plan_total_tiles_warp(pl));
+      // a call without any page: no role below waits for the split kernel, but the merge waits for
+      // this grid's end alone, and the next call may have the same workspace
+      if (pl.T == 0) griddep_wait();
       const int64_t xb = c < pl.G ? pl.cta_start(c) : 0;
       RowCursor f = plan_find_row_warp(pl, xb, c == 0, p.ws.row_base, p.ws.row_np, p.ws.status);
       if (lane == 0) {
